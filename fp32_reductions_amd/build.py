@@ -24,7 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libreduce.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.hip", "reduce1d.hip", "rows.hip", "colprod.hip"]
+SOURCES = ["api.hip", "reduce1d.hip", "rows.hip", "colprod.hip", "rowloss.hip",
+           "rowloss_f32.hip", "rowloss_f16.hip", "rowloss_bf16.hip"]
 # Measurement only (the benchmark's read-only streaming ceiling): a library
 # of its own.
 CALIB_SOURCES = ["calib_read.hip"]

@@ -7,8 +7,10 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <initializer_list>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -16,6 +18,7 @@
 
 #include "internal.hpp"
 #include "reduce.h"
+#include "rowloss.hpp"
 
 namespace {
 
@@ -419,6 +422,179 @@ int colprod(ColType t, const void* src, size_t R, size_t C, size_t ld,
     return hip_status(red::launch_colprod(t, src, R, C, ld, dst, plan, ws, s));
 }
 
+// ---- losses over rows of logits --------------------------------------------
+
+using red::LogitType;
+using red::Logits;
+
+bool positive(float v) { return v > 0.0f && std::isfinite(v); }
+
+// The scale, its reciprocal and its exponent factor are usable numbers.
+bool scale_ok(float scale)
+{
+    return positive(scale) && scale <= 1e30f && scale >= 1e-30f;
+}
+
+// A row-sized fp32 argument: null only where `needed` is false.
+int check_values(const void* p, size_t n, size_t elem, bool needed)
+{
+    if (!p)
+        return needed ? RED_ERR_INVALID : RED_OK;
+    if (n > SIZE_MAX / elem)
+        return RED_ERR_INVALID;
+    return aligned(p, elem) ? RED_OK : RED_ERR_ALIGN;
+}
+
+struct Values {
+    const void* p;
+    size_t n, elem;
+    bool needed;
+};
+
+// Checks the matrices, then the values: invalid arguments first, alignment
+// second, as the other entry points do.
+int check_logits(LogitType t, const Logits& m, bool grad_needed,
+                 std::initializer_list<Values> values)
+{
+    const size_t es = t == LogitType::F32 ? 4 : 2;
+    if (!m.z || m.V >= (size_t(1) << 31) || m.ld < m.V || !extent_ok(m.rows, m.ld, m.V, es) ||
+        !scale_ok(m.scale) || (grad_needed && !m.dz))
+        return RED_ERR_INVALID;
+    if (m.dz && (m.ldd < m.V || !extent_ok(m.rows, m.ldd, m.V, es) ||
+                 (m.dz == m.z && m.ldd != m.ld)))
+        return RED_ERR_INVALID;
+    int worst = aligned(m.z, es) && aligned(m.dz, es) ? RED_OK : RED_ERR_ALIGN;
+    for (const Values& v : values) {
+        const int st = check_values(v.p, v.n, v.elem, v.needed);
+        if (st == RED_ERR_INVALID)
+            return st;
+        if (st != RED_OK)
+            worst = st;
+    }
+    return worst;
+}
+
+int token_logprob(LogitType t, const Logits& m, const int64_t* targets, float* logp, float* lse,
+                  float* entropy, red_stream_t stream)
+{
+    if (m.rows == 0 || m.V == 0)
+        return RED_OK;
+    int st = check_logits(t, m, false,
+                          {{targets, m.rows, 8, true}, {logp, m.rows, 4, true},
+                           {lse, m.rows, 4, true}, {entropy, m.rows, 4, false}});
+    if (st != RED_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    clear_stale_error();
+    return hip_status(red::launch_token_logprob(t, {m, targets, logp, lse, entropy}, info,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int token_logprob_grad(LogitType t, const Logits& m, const int64_t* targets, const float* lse,
+                       const float* entropy, const float* glogp, const float* gentropy,
+                       red_stream_t stream)
+{
+    if (m.rows == 0 || m.V == 0)
+        return RED_OK;
+    int st = check_logits(t, m, true,
+                          {{targets, m.rows, 8, true}, {lse, m.rows, 4, true},
+                           {entropy, m.rows, 4, gentropy != nullptr},
+                           {glogp, m.rows, 4, true}, {gentropy, m.rows, 4, false}});
+    if (st != RED_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    clear_stale_error();
+    return hip_status(red::launch_token_logprob_grad(
+        t, {m, targets, lse, entropy, glogp, gentropy}, info, static_cast<hipStream_t>(stream)));
+}
+
+// The calls that join row losses: device and workspace, then the launches.
+template <class Launch>
+int with_workspace(red_stream_t stream, Launch launch)
+{
+    int dev, st;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    Workspace ws;
+    HeldWorkspace held;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = stream_workspace(dev, s, &ws, &held)) != RED_OK)
+        return st;
+    clear_stale_error();
+    return hip_status(launch(info, ws, s));
+}
+
+int distill_topk(LogitType t, const red::DistillCall& a, red_stream_t stream)
+{
+    const Logits& m = a.m;
+    if (m.rows == 0 || m.V == 0)
+        return RED_OK;
+    if (a.K < 1 || a.K > red::kTopkMax || a.ldk < a.K || m.V > red::kTopkColsMax ||
+        !extent_ok(m.rows, a.ldk, a.K, 8))
+        return RED_ERR_INVALID;
+    const int st = check_logits(t, m, false,
+                                {{a.idx, 0, 8, true}, {a.val, 0, 4, true},
+                                 {a.teacher_lse, m.rows, 4, false}, {a.weight, m.rows, 4, false},
+                                 {a.loss, 1, 4, true}, {a.row_loss, m.rows, 4, false}});
+    if (st != RED_OK)
+        return st;
+    return with_workspace(stream, [&](const DeviceInfo& d, const Workspace& ws, hipStream_t s) {
+        return red::launch_distill_topk(t, a, d, ws, s);
+    });
+}
+
+int policy_loss(LogitType t, const red::PolicyCall& a, red_stream_t stream)
+{
+    const Logits& m = a.m;
+    if (m.rows == 0 || m.V == 0)
+        return RED_OK;
+    if (!(a.clip_low >= 0.0f) || !(a.clip_high >= 0.0f) || !std::isfinite(a.kl_coef) ||
+        !std::isfinite(a.entropy_coef))
+        return RED_ERR_INVALID;
+    const int st = check_logits(
+        t, m, false,
+        {{a.targets, m.rows, 8, true}, {a.old_logp, m.rows, 4, true},
+         {a.ref_logp, m.rows, 4, a.kl_coef != 0.0f}, {a.advantage, m.rows, 4, true},
+         {a.weight, m.rows, 4, false}, {a.loss, 1, 4, true}, {a.logp, m.rows, 4, true},
+         {a.entropy, m.rows, 4, false}});
+    if (st != RED_OK)
+        return st;
+    red::PolicyCall call = a;
+    if (call.kl_coef == 0.0f)
+        call.ref_logp = nullptr;
+    return with_workspace(stream, [&](const DeviceInfo& d, const Workspace& ws, hipStream_t s) {
+        return red::launch_policy_loss(t, call, d, ws, s);
+    });
+}
+
+int preference_loss(LogitType t, const red::PreferenceCall& a, red_stream_t stream)
+{
+    const Logits& m = a.m;
+    if (m.rows == 0 || m.V == 0 || a.pairs == 0)
+        return RED_OK;
+    if (m.rows > red::kPrefRowsMax || a.pairs > red::kPrefPairsMax ||
+        a.kind < RED_PREF_SIGMOID || a.kind > RED_PREF_SQUARED || !positive(a.beta) ||
+        !std::isfinite(a.margin) || !(a.smoothing >= 0.0f && a.smoothing <= 1.0f))
+        return RED_ERR_INVALID;
+    const int st = check_logits(
+        t, m, false,
+        {{a.targets, m.rows, 8, true}, {a.starts, 2 * a.pairs + 1, 8, true},
+         {a.ref_logp, 2 * a.pairs, 4, false}, {a.weight, a.pairs, 4, false},
+         {a.loss, 1, 4, true}, {a.seq_logp, 2 * a.pairs, 4, true}});
+    if (st != RED_OK)
+        return st;
+    return with_workspace(stream, [&](const DeviceInfo& d, const Workspace& ws, hipStream_t s) {
+        return red::launch_preference_loss(t, a, d, ws, s);
+    });
+}
+
 } // namespace
 
 extern "C" {
@@ -527,6 +703,156 @@ int red_colprod_u32(const uint32_t* src, size_t R, size_t C, size_t ld, uint32_t
                     red_stream_t stream)
 {
     return colprod(ColType::I32, src, R, C, ld, dst, stream);
+}
+
+int red_token_logprob_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                      const int64_t* targets, float scale, float* logp, float* lse,
+                      float* entropy, red_stream_t stream)
+{
+    return token_logprob(LogitType::F32, {logits, nullptr, rows, V, ld, 0, scale}, targets, logp,
+                         lse, entropy, stream);
+}
+int red_token_logprob_grad_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                           const int64_t* targets, float scale, const float* lse,
+                           const float* entropy, const float* glogp, const float* gentropy,
+                           float* dlogits, size_t ldd, red_stream_t stream)
+{
+    return token_logprob_grad(LogitType::F32, {logits, dlogits, rows, V, ld, ldd, scale}, targets,
+                              lse, entropy, glogp, gentropy, stream);
+}
+int red_distill_topk_f32(const float* logits, size_t rows, size_t V, size_t ld, const int64_t* idx,
+                     const float* val, size_t K, size_t ldk, const float* teacher_lse,
+                     const float* weight, float scale, float* loss, int accum, float* row_loss,
+                     float* dlogits, size_t ldd, red_stream_t stream)
+{
+    return distill_topk(LogitType::F32,
+                        {{logits, dlogits, rows, V, ld, ldd, scale}, idx, val, K, ldk,
+                         teacher_lse, weight, loss, row_loss, accum},
+                        stream);
+}
+int red_policy_loss_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                    const int64_t* targets, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, float scale, float clip_low,
+                    float clip_high, float kl_coef, float entropy_coef, float* loss, int accum,
+                    float* logp, float* entropy, float* dlogits, size_t ldd, red_stream_t stream)
+{
+    return policy_loss(LogitType::F32,
+                       {{logits, dlogits, rows, V, ld, ldd, scale}, targets, old_logp, ref_logp,
+                        advantage, weight, clip_low, clip_high, kl_coef, entropy_coef, loss, logp,
+                        entropy, accum},
+                       stream);
+}
+int red_preference_loss_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                        const int64_t* targets, const int64_t* starts, size_t pairs,
+                        const float* ref_logp, const float* weight, int kind, float beta,
+                        float margin, float smoothing, int average, float* loss, int accum,
+                        float* seq_logp, float* dlogits, size_t ldd, red_stream_t stream)
+{
+    return preference_loss(LogitType::F32,
+                           {{logits, dlogits, rows, V, ld, ldd, 1.0f}, targets, starts, pairs,
+                            ref_logp, weight, kind, average, beta, margin, smoothing, loss,
+                            seq_logp, accum},
+                           stream);
+}
+
+int red_token_logprob_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                      const int64_t* targets, float scale, float* logp, float* lse,
+                      float* entropy, red_stream_t stream)
+{
+    return token_logprob(LogitType::F16, {logits, nullptr, rows, V, ld, 0, scale}, targets, logp,
+                         lse, entropy, stream);
+}
+int red_token_logprob_grad_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                           const int64_t* targets, float scale, const float* lse,
+                           const float* entropy, const float* glogp, const float* gentropy,
+                           uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return token_logprob_grad(LogitType::F16, {logits, dlogits, rows, V, ld, ldd, scale}, targets,
+                              lse, entropy, glogp, gentropy, stream);
+}
+int red_distill_topk_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld, const int64_t* idx,
+                     const float* val, size_t K, size_t ldk, const float* teacher_lse,
+                     const float* weight, float scale, float* loss, int accum, float* row_loss,
+                     uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return distill_topk(LogitType::F16,
+                        {{logits, dlogits, rows, V, ld, ldd, scale}, idx, val, K, ldk,
+                         teacher_lse, weight, loss, row_loss, accum},
+                        stream);
+}
+int red_policy_loss_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                    const int64_t* targets, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, float scale, float clip_low,
+                    float clip_high, float kl_coef, float entropy_coef, float* loss, int accum,
+                    float* logp, float* entropy, uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return policy_loss(LogitType::F16,
+                       {{logits, dlogits, rows, V, ld, ldd, scale}, targets, old_logp, ref_logp,
+                        advantage, weight, clip_low, clip_high, kl_coef, entropy_coef, loss, logp,
+                        entropy, accum},
+                       stream);
+}
+int red_preference_loss_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                        const int64_t* targets, const int64_t* starts, size_t pairs,
+                        const float* ref_logp, const float* weight, int kind, float beta,
+                        float margin, float smoothing, int average, float* loss, int accum,
+                        float* seq_logp, uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return preference_loss(LogitType::F16,
+                           {{logits, dlogits, rows, V, ld, ldd, 1.0f}, targets, starts, pairs,
+                            ref_logp, weight, kind, average, beta, margin, smoothing, loss,
+                            seq_logp, accum},
+                           stream);
+}
+
+int red_token_logprob_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                      const int64_t* targets, float scale, float* logp, float* lse,
+                      float* entropy, red_stream_t stream)
+{
+    return token_logprob(LogitType::BF16, {logits, nullptr, rows, V, ld, 0, scale}, targets, logp,
+                         lse, entropy, stream);
+}
+int red_token_logprob_grad_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                           const int64_t* targets, float scale, const float* lse,
+                           const float* entropy, const float* glogp, const float* gentropy,
+                           uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return token_logprob_grad(LogitType::BF16, {logits, dlogits, rows, V, ld, ldd, scale}, targets,
+                              lse, entropy, glogp, gentropy, stream);
+}
+int red_distill_topk_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld, const int64_t* idx,
+                     const float* val, size_t K, size_t ldk, const float* teacher_lse,
+                     const float* weight, float scale, float* loss, int accum, float* row_loss,
+                     uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return distill_topk(LogitType::BF16,
+                        {{logits, dlogits, rows, V, ld, ldd, scale}, idx, val, K, ldk,
+                         teacher_lse, weight, loss, row_loss, accum},
+                        stream);
+}
+int red_policy_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                    const int64_t* targets, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, float scale, float clip_low,
+                    float clip_high, float kl_coef, float entropy_coef, float* loss, int accum,
+                    float* logp, float* entropy, uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return policy_loss(LogitType::BF16,
+                       {{logits, dlogits, rows, V, ld, ldd, scale}, targets, old_logp, ref_logp,
+                        advantage, weight, clip_low, clip_high, kl_coef, entropy_coef, loss, logp,
+                        entropy, accum},
+                       stream);
+}
+int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                        const int64_t* targets, const int64_t* starts, size_t pairs,
+                        const float* ref_logp, const float* weight, int kind, float beta,
+                        float margin, float smoothing, int average, float* loss, int accum,
+                        float* seq_logp, uint16_t* dlogits, size_t ldd, red_stream_t stream)
+{
+    return preference_loss(LogitType::BF16,
+                           {{logits, dlogits, rows, V, ld, ldd, 1.0f}, targets, starts, pairs,
+                            ref_logp, weight, kind, average, beta, margin, smoothing, loss,
+                            seq_logp, accum},
+                           stream);
 }
 
 int red_release_workspace(red_stream_t stream)

@@ -1,0 +1,1310 @@
+// rowloss_kernels.hpp -- losses over rows of logits: kernels and launches,
+// instantiated once per element type.
+//
+// Every operator here reduces a row z[0..V) of logits to
+//
+//     m = max z,   S = sum 2^((z - m) c),   U = sum 2^((z - m) c) (z - m) c,
+//
+// with c = scale * log2(e), so that p_v = 2^((z_v - m) c) / S is the softmax
+// of the scaled row, ln S + scale * m its log-sum-exp and ln S - ln 2 * U / S
+// its entropy.  The gradient of each row loss with respect to the logits is
+//
+//     dz_v = 2^((z_v - m) c) (A + B (z_v - m) c) + (terms in a few columns)
+//
+// with A and B from the loss of that row alone.  So a loss and its gradient
+// need one read of the row and one write: row_kernel keeps the row in the
+// registers of its workgroup between the two.  What bounds it is HBM; at 16
+// bits the exponentials come near it (two per element, each element unpacked
+// three times).
+//
+// Statistics are fp32 per thread (sums of at most a few hundred terms, then
+// a tree); what is computed once per row (logarithms, ratios, losses) is
+// fp64, so that a sum of thousands of log-probabilities keeps its last bits.
+// Terms below 2^-126 of a row's largest count as zero (v_exp_f32).
+//
+// Determinism: no atomics on results; every sum has a fixed order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.hpp"
+#include "rowloss.hpp"
+
+namespace red {
+
+// ---- element types ---------------------------------------------------------
+//
+// Vec holds W elements in 16 bytes.  pack rounds each value once, to nearest
+// even.
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+struct ElemF32 {
+    typedef float S;
+    static constexpr int W = 4;
+    static constexpr unsigned kNegInf = 0xff800000u;
+    static __device__ __forceinline__ void unpack(const u32x4_t& v, float (&f)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = __uint_as_float(v[i]);
+    }
+    static __device__ __forceinline__ u32x4_t pack(const float (&f)[4])
+    {
+        u32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __float_as_uint(f[i]);
+        return v;
+    }
+    static __device__ __forceinline__ float widen(S s) { return s; }
+    static __device__ __forceinline__ S narrow(float f) { return f; }
+};
+
+struct ElemF16 {
+    typedef uint16_t S;
+    static constexpr int W = 8;
+    static constexpr unsigned kNegInf = 0xfc00fc00u;
+    static __device__ __forceinline__ void unpack(const u32x4_t& v, float (&f)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f16x2_t h = __builtin_bit_cast(f16x2_t, (unsigned)v[i]);
+            f[2 * i] = (float)h.x;
+            f[2 * i + 1] = (float)h.y;
+        }
+    }
+    static __device__ __forceinline__ u32x4_t pack(const float (&f)[8])
+    {
+        u32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f16x2_t h;
+            h.x = (_Float16)f[2 * i];
+            h.y = (_Float16)f[2 * i + 1];
+            v[i] = __builtin_bit_cast(unsigned, h);
+        }
+        return v;
+    }
+    static __device__ __forceinline__ float widen(S s)
+    {
+        return (float)__builtin_bit_cast(_Float16, s);
+    }
+    static __device__ __forceinline__ S narrow(float f)
+    {
+        return __builtin_bit_cast(S, (_Float16)f);
+    }
+};
+
+struct ElemBF16 {
+    typedef uint16_t S;
+    static constexpr int W = 8;
+    static constexpr unsigned kNegInf = 0xff80ff80u;
+    static __device__ __forceinline__ void unpack(const u32x4_t& v, float (&f)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float((unsigned)v[i] << 16);
+            f[2 * i + 1] = __uint_as_float((unsigned)v[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ u32x4_t pack(const float (&f)[8])
+    {
+        u32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x2_t p;
+            p.x = f[2 * i];
+            p.y = f[2 * i + 1];
+            v[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(p, bf16x2_t));
+        }
+        return v;
+    }
+    static __device__ __forceinline__ float widen(S s)
+    {
+        return __uint_as_float((unsigned)s << 16);
+    }
+    static __device__ __forceinline__ S narrow(float f)
+    {
+        return __builtin_bit_cast(S, (__bf16)f);
+    }
+};
+
+namespace rowloss {
+
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr double kLn2 = 0.69314718055994530942;
+// Exponents are clamped here where they multiply a probability, so that a
+// probability of zero (a logit of -inf) contributes 0 and not 0 * inf.
+constexpr float kLowest = -1.0e30f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- a row's elements and the threads that own them ------------------------
+//
+// `head` elements up to the first 16-byte boundary, `nvec` vectors, and the
+// rest.  Vector j belongs to thread j mod GT of the row's GT threads; the
+// head and the rest (at most 2 (W - 1) <= 14 elements) go one each to the
+// first threads.
+struct Span {
+    uint32_t head, nvec, tail, singles;
+    template <class T>
+    static __device__ __forceinline__ Span of(const typename T::S* row, uint32_t V)
+    {
+        Span s;
+        const uint32_t past = (uint32_t)((uintptr_t)row & 15u) / (uint32_t)sizeof(typename T::S);
+        const uint32_t head = past ? T::W - past : 0;
+        s.head = head < V ? head : V;
+        s.nvec = (V - s.head) / T::W;
+        s.tail = s.head + s.nvec * T::W;
+        s.singles = s.head + (V - s.tail);
+        return s;
+    }
+    __device__ __forceinline__ uint32_t single(uint32_t t) const
+    {
+        return t < head ? t : t - head + tail;
+    }
+};
+
+// A gradient row need not share its logits' alignment: gfx950 stores
+// unaligned 16-byte vectors to global memory.
+typedef unsigned u32x4u_t __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool STREAM>
+__device__ __forceinline__ u32x4_t load_vec(const u32x4_t* p)
+{
+    if constexpr (STREAM)
+        return __builtin_nontemporal_load(p);
+    else
+        return *p;
+}
+
+__device__ __forceinline__ void store_vec(void* p, const u32x4_t& v)
+{
+    u32x4u_t u;
+    u.x = v.x; u.y = v.y; u.z = v.z; u.w = v.w;
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4u_t*>(p));
+}
+
+// The vectors j = first + k GT + t (k < NV) of a row; slots past the row's
+// end hold -inf, which adds nothing to any statistic.
+template <class T, int GT, int NV, bool STREAM>
+__device__ __forceinline__ void load_chunk(const u32x4_t* base, uint32_t first, uint32_t nvec,
+                                           uint32_t t, u32x4_t (&v)[NV])
+{
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const uint32_t j = first + k * GT + t;
+        v[k] = u32x4_t{T::kNegInf, T::kNegInf, T::kNegInf, T::kNegInf};
+        if (j < nvec)
+            v[k] = load_vec<STREAM>(base + j);
+    }
+}
+
+// ---- statistics ------------------------------------------------------------
+struct Stat {
+    float m, s, u;
+};
+
+// The reference of an exponent: the maximum, or 0 while every element so far
+// is -inf (whose terms then come out as 0).
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// The exponent of an element is one fused step, z c - shift, with shift the
+// rounded product of the reference and c.  What that rounding drops (delta =
+// ref c - shift, exact in one fused step) is a factor 2^-delta common to all
+// of a thread's terms, put back once per chunk.  Where shift is so large that
+// delta is no small number any more (a row filled with its type's lowest
+// value, say), the difference z - ref is taken first.
+constexpr float kWideShift = 1048576.0f; // delta below 2^-4
+__device__ __forceinline__ bool is_wide(float shift) { return !(fabsf(shift) < kWideShift); }
+
+// What a term of the sums leaves out: nothing, or the columns of a bitmap
+// with one bit per element and W bits per vector.
+struct TakeAll {
+    static constexpr bool kSome = false;
+    __device__ __forceinline__ unsigned skip(uint32_t) const { return 0; }
+    __device__ __forceinline__ bool skip_one(uint32_t) const { return false; }
+};
+
+template <int W>
+struct TakeUnmarked {
+    static constexpr bool kSome = true;
+    const uint32_t* bits;
+    uint32_t head, nvec;
+    __device__ __forceinline__ unsigned skip(uint32_t j) const
+    {
+        const uint32_t at = ((j < nvec ? j : nvec) + 1) * W; // no mark past the row's end
+        return (reinterpret_cast<const unsigned char*>(bits)[at >> 3] >> (at & 7)) & ((1u << W) - 1);
+    }
+    __device__ __forceinline__ bool skip_one(uint32_t e) const
+    {
+        const uint32_t at = e - head + W;
+        return (bits[at >> 5] >> (at & 31)) & 1;
+    }
+};
+
+// Folds the chunk v (vectors first + k GT + t) and the single element `one`
+// into st: first the maximum, then the sums against it.
+template <class T, int GT, int NV, bool ENT, class Take>
+__device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t first, uint32_t nvec,
+                                           uint32_t t, float one, bool skip_one, float c,
+                                           const Take& take, Stat& st)
+{
+    constexpr int W = T::W;
+    float m0 = fmaxf(st.m, one), m1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (k && first + k * GT >= nvec)
+            break;
+        float f[W];
+        T::unpack(v[k], f);
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            m0 = fmaxf(fmaxf(m0, f[i]), f[i + 1]);
+            m1 = fmaxf(fmaxf(m1, f[i + 2]), f[i + 3]);
+        }
+    }
+    const float m = fmaxf(m0, m1);
+    const float ref = reference(m), mc = ref * c;
+    // What was summed against the old maximum moves to the new one.
+    const float d = fmaxf((st.m - ref) * c, kLowest), r = exp2_fast(d);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+    const bool wide = is_wide(mc);
+    auto sums = [&](auto exponent) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k && first + k * GT >= nvec)
+                break;
+            float f[W];
+            T::unpack(v[k], f);
+            if constexpr (Take::kSome) {
+                const unsigned skip = take.skip(first + k * GT + t);
+                if (skip) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        if ((skip >> i) & 1)
+                            f[i] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float x = exponent(f[i]), e = exp2_fast(x);
+                s[i & 3] += e;
+                if constexpr (ENT)
+                    u[i & 1] = fmaf(e, fmaxf(x, kLowest), u[i & 1]);
+            }
+        }
+        if (!skip_one) {
+            const float x = exponent(one), e = exp2_fast(x);
+            s[1] += e;
+            if constexpr (ENT)
+                u[1] = fmaf(e, fmaxf(x, kLowest), u[1]);
+        }
+    };
+    if (__builtin_expect(wide, 0))
+        sums([&](float z) { return (z - ref) * c; });
+    else
+        sums([&](float z) { return fmaf(z, c, -mc); });
+    const float delta = wide ? 0.0f : fmaf(ref, c, -mc), back = exp2_fast(-delta);
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if constexpr (ENT)
+        st.u = fmaf(r, fmaf(st.s, d, st.u), back * fmaf(-delta, sum, u[0] + u[1]));
+    st.s = fmaf(st.s, r, back * sum);
+    st.m = m;
+}
+
+// Moves st to the maximum m (>= st.m).
+template <bool ENT>
+__device__ __forceinline__ void move_to(Stat& st, float m, float c)
+{
+    const float d = fmaxf((st.m - reference(m)) * c, kLowest), r = exp2_fast(d);
+    if constexpr (ENT)
+        st.u = r * fmaf(st.s, d, st.u);
+    st.s *= r;
+    st.m = m;
+}
+
+// The statistics of a row from those of its GT threads, in every thread.
+// lds: 3 floats per wave of a group of more than one.
+template <int GT, bool ENT>
+__device__ __forceinline__ Stat combine(Stat st, float c, float* lds)
+{
+    move_to<ENT>(st, wave_reduce<OpMax>(st.m), c);
+    st.s = wave_reduce<OpSum>(st.s);
+    if constexpr (ENT)
+        st.u = wave_reduce<OpSum>(st.u);
+    if constexpr (GT > kWave) {
+        constexpr int kParts = GT / kWave;
+        const int w = (threadIdx.x % GT) / kWave;
+        if ((threadIdx.x & 63) == 0) {
+            lds[w] = st.m;
+            lds[kParts + w] = st.s;
+            if constexpr (ENT)
+                lds[2 * kParts + w] = st.u;
+        }
+        __syncthreads();
+        float m = lds[0];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k)
+            m = fmaxf(m, lds[k]);
+        Stat all = {m, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            Stat part = {lds[k], lds[kParts + k], ENT ? lds[2 * kParts + k] : 0.0f};
+            move_to<ENT>(part, m, c);
+            all.s += part.s;
+            if constexpr (ENT)
+                all.u += part.u;
+        }
+        st = all;
+    }
+    return st;
+}
+
+// dz = 2^x (A + B x) for every element of a row.
+struct Slope {
+    float a, b;
+};
+
+template <bool ENT>
+__device__ __forceinline__ float slope_at(float x, const Slope& k)
+{
+    const float e = exp2_fast(x);
+    if constexpr (ENT)
+        return e * fmaf(k.b, fmaxf(x, kLowest), k.a);
+    else
+        return e * k.a;
+}
+
+// The exponent x of a logit against the row's maximum; `lost` is what the
+// fused form's shift leaves out of it (delta above).
+struct Exponent {
+    float ref, c, shift, lost;
+    bool wide;
+    __device__ __forceinline__ Exponent(float reference_, float c_) : ref(reference_), c(c_)
+    {
+        shift = ref * c;
+        wide = is_wide(shift);
+        lost = wide ? 0.0f : fmaf(ref, c, -shift);
+    }
+    __device__ __forceinline__ float at(float z) const { return (z - ref) * c; }
+    // A + B x in terms of the exponent that leaves `lost` out.
+    __device__ __forceinline__ Slope fused(const Slope& k) const
+    {
+        const float back = exp2_fast(-lost);
+        return {back * fmaf(-lost, k.b, k.a), back * k.b};
+    }
+};
+
+template <class T, int GT, int NV, bool ENT>
+__device__ __forceinline__ void write_chunk(const u32x4_t (&v)[NV], typename T::S* out,
+                                            uint32_t first, uint32_t nvec, uint32_t t,
+                                            const Exponent& ex, const Slope& exact_slope)
+{
+    constexpr int W = T::W;
+    const Slope slope = ex.fused(exact_slope);
+    auto put = [&](auto exponent) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (k && first + k * GT >= nvec)
+                break;
+            const uint32_t j = first + k * GT + t;
+            float f[W];
+            T::unpack(v[k], f);
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                f[i] = slope_at<ENT>(exponent(f[i]), slope);
+            if (j < nvec)
+                store_vec(out + (size_t)j * W, T::pack(f));
+        }
+    };
+    if (__builtin_expect(ex.wide, 0))
+        put([&](float z) { return (z - ex.ref) * ex.c; });
+    else
+        put([&](float z) { return fmaf(z, ex.c, -ex.shift); });
+}
+
+template <class T, int GT>
+__device__ __forceinline__ void write_zeros(typename T::S* row, const Span& sp, uint32_t t)
+{
+    for (uint32_t j = t; j < sp.nvec; j += GT)
+        store_vec(row + sp.head + (size_t)j * T::W, u32x4_t{0, 0, 0, 0});
+    if (t < sp.singles)
+        row[sp.single(t)] = 0;
+}
+
+// ---- the operators ---------------------------------------------------------
+//
+// An operator has: kEntropy (U is needed), kList (its row has a teacher's
+// list), Args, Row (what it loads of a row before its logits: `live` says
+// whether the row counts at all, `y` its target column), and
+//   done(row, stat, zy, leader): outputs of the row (by the leader alone),
+//     and the slope of its gradient;
+//   fix: what is added to the gradient in the target's column.
+
+// The fp64 part of a row: ln p of a logit, and the entropy.
+struct RowLogs {
+    double ln_s, scale, ref;
+    __device__ __forceinline__ RowLogs(const Stat& st, float scale_)
+        : ln_s(log((double)st.s)), scale(scale_), ref(reference(st.m))
+    {
+    }
+    __device__ __forceinline__ double logp(float z) const { return ((double)z - ref) * scale - ln_s; }
+    __device__ __forceinline__ double lse() const { return ref * scale + ln_s; }
+    __device__ __forceinline__ double entropy(const Stat& st) const
+    {
+        return ln_s - kLn2 * ((double)st.u / (double)st.s);
+    }
+};
+
+// Log-probability of the target, log-sum-exp and entropy.
+template <bool ENT>
+struct LogprobOp {
+    static constexpr bool kEntropy = ENT, kList = false, kHasGrad = false;
+    struct Args {
+        const int64_t* targets;
+        float *logp, *lse, *entropy;
+        float scale;
+    };
+    struct Row {
+        bool live, hit;
+        uint32_t y;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
+    {
+        const int64_t y = a.targets[row];
+        const bool hit = (uint64_t)y < V;
+        return {true, hit, hit ? (uint32_t)y : 0u};
+    }
+    static __device__ __forceinline__ Slope done(const Args& a, const Row& r, size_t row,
+                                                 const Stat& st, float zy, bool leader, float& fix)
+    {
+        if (leader) {
+            const RowLogs l(st, a.scale);
+            a.logp[row] = r.hit ? (float)l.logp(zy) : 0.0f;
+            a.lse[row] = (float)l.lse();
+            if constexpr (ENT)
+                a.entropy[row] = (float)l.entropy(st);
+        }
+        fix = 0.0f;
+        return {0.0f, 0.0f};
+    }
+    static __device__ __forceinline__ void dead(const Args&, size_t, bool) {}
+};
+
+// First pass of the preference loss: maximum, sum and log-probability.
+struct PreferenceOp {
+    static constexpr bool kEntropy = false, kList = false, kHasGrad = false;
+    struct Args {
+        const int64_t* targets;
+        float2* stat;
+        double* logp;
+        float* slope;
+    };
+    struct Row {
+        bool live;
+        uint32_t y;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
+    {
+        const int64_t y = a.targets[row];
+        const bool hit = (uint64_t)y < V;
+        return {hit, hit ? (uint32_t)y : 0u};
+    }
+    static __device__ __forceinline__ Slope done(const Args& a, const Row&, size_t row,
+                                                 const Stat& st, float zy, bool leader, float& fix)
+    {
+        if (leader) {
+            const RowLogs l(st, 1.0f);
+            a.stat[row] = make_float2(st.m, st.s);
+            a.logp[row] = l.logp(zy);
+            a.slope[row] = 0.0f;
+        }
+        fix = 0.0f;
+        return {0.0f, 0.0f};
+    }
+    static __device__ __forceinline__ void dead(const Args& a, size_t row, bool leader)
+    {
+        if (leader) {
+            a.stat[row] = make_float2(0.0f, 1.0f);
+            a.logp[row] = 0.0;
+            a.slope[row] = 0.0f;
+        }
+    }
+};
+
+// Clipped policy loss.  With r = exp(logp - old), d = ref - logp:
+//   loss  = -min(r A, clip(r) A) + kl (exp(d) - d - 1) - ent H
+//   slope = -(r A where r A <= clip(r) A, else 0) + kl (1 - exp(d))   (to logp)
+// and d logp / dz_v = scale (delta_vy - p_v), dH / dz_v = -scale p_v (ln p_v + H).
+template <bool ENT>
+struct PolicyOp {
+    static constexpr bool kEntropy = ENT, kList = false, kHasGrad = true;
+    struct Args {
+        const int64_t* targets;
+        const float *old_logp, *ref_logp, *advantage, *weight;
+        double clip_min, clip_max, kl, ent;
+        float scale, mean;
+        float *logp, *entropy;
+        double* row_loss;
+    };
+    struct Row {
+        bool live;
+        uint32_t y;
+        float weight;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
+    {
+        const int64_t y = a.targets[row];
+        const float w = a.weight ? a.weight[row] : a.mean;
+        const bool hit = (uint64_t)y < V;
+        return {hit && w != 0.0f, hit ? (uint32_t)y : 0u, w};
+    }
+    static __device__ __forceinline__ Slope done(const Args& a, const Row& r, size_t row,
+                                                 const Stat& st, float zy, bool leader, float& fix)
+    {
+        const RowLogs l(st, a.scale);
+        const double logp = l.logp(zy), adv = a.advantage[row], w = r.weight;
+        const double ratio = exp(logp - (double)a.old_logp[row]);
+        const double free = ratio * adv;
+        const double bound = ratio < a.clip_min   ? a.clip_min
+                             : ratio > a.clip_max ? a.clip_max
+                                                  : ratio;
+        const double clipped = bound * adv;
+        // Not (free > clipped), so that a NaN stays one.
+        double loss = free > clipped ? -clipped : -free;
+        double g = free > clipped ? 0.0 : -free;
+        if (a.ref_logp) {
+            const double d = (double)a.ref_logp[row] - logp, k = expm1(d);
+            loss += a.kl * (k - d);
+            g -= a.kl * k;
+        }
+        double H = 0.0;
+        if constexpr (ENT) {
+            H = l.entropy(st);
+            loss -= a.ent * H;
+        }
+        if (leader) {
+            a.logp[row] = (float)logp;
+            if (ENT && a.entropy)
+                a.entropy[row] = (float)H;
+            a.row_loss[row] = w * loss;
+        }
+        const double gw = w * g * l.scale;
+        fix = (float)gw;
+        Slope k = {(float)(-gw / (double)st.s), 0.0f};
+        if constexpr (ENT) {
+            const double hw = w * a.ent * l.scale / (double)st.s;
+            k.a = (float)(-gw / (double)st.s + hw * (H - l.ln_s));
+            k.b = (float)(hw * kLn2);
+        }
+        return k;
+    }
+    static __device__ __forceinline__ void dead(const Args& a, size_t row, bool leader)
+    {
+        if (leader) {
+            a.logp[row] = 0.0f;
+            if (ENT && a.entropy)
+                a.entropy[row] = 0.0f;
+            a.row_loss[row] = 0.0;
+        }
+    }
+};
+
+// Divergence from a teacher's largest logits.  S: the columns listed, q_k
+// the teacher's probability of entry k, Q their sum and, with TAIL, q_r =
+// 1 - Q the rest's, against p_r = sum of p outside S:
+//   loss = sum_k q_k (ln q_k - ln p_k) [+ q_r (ln q_r - ln p_r)]
+//   dz_v = w scale (p_v (Q + q_r) - q_v) in S,
+//          w scale p_v (Q + q_r - q_r / p_r) outside
+// (Q and no second term without TAIL).
+template <bool TAIL>
+struct DistillOp {
+    static constexpr bool kEntropy = false, kList = true, kTail = TAIL, kHasGrad = true;
+    struct Args {
+        const int64_t* idx;
+        const float *val, *teacher_lse, *weight;
+        uint32_t K;
+        size_t ldk;
+        float scale, mean;
+        float* row_loss_out;
+        double* row_loss;
+    };
+    struct Row {
+        bool live;
+        float weight;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t)
+    {
+        const float w = a.weight ? a.weight[row] : a.mean;
+        return {w != 0.0f, w};
+    }
+    static __device__ __forceinline__ void dead(const Args& a, size_t row, bool leader)
+    {
+        if (leader) {
+            a.row_loss[row] = 0.0;
+            if (a.row_loss_out)
+                a.row_loss_out[row] = 0.0f;
+        }
+    }
+};
+
+// A row's teacher in LDS: its columns (-1: padding; the high bit marks the
+// later ones of a column listed more than once), probabilities, the logits
+// in those columns, and a bit for each listed column.
+struct TeacherLds {
+    uint32_t* bits;
+    int* col;
+    float* q;
+    float* z;
+    double* cross; // sum q (ln q - scale (z - ref)), ref the largest logit listed
+    double* sum;   // Q
+    int* state;    // [0]: the row has a teacher; [1]: listed columns; [2]: ref
+    static __host__ __device__ size_t bytes(size_t words, size_t K)
+    {
+        return (32 + 4 * words + 12 * K + 15) / 16 * 16;
+    }
+    __device__ __forceinline__ TeacherLds(char* base, uint32_t words, uint32_t K)
+    {
+        cross = reinterpret_cast<double*>(base);
+        sum = cross + 1;
+        state = reinterpret_cast<int*>(base + 16);
+        bits = reinterpret_cast<uint32_t*>(base + 32);
+        col = reinterpret_cast<int*>(bits + words);
+        q = reinterpret_cast<float*>(col + K);
+        z = q + K;
+    }
+};
+
+// Words of the bitmap of V columns: vectors start at bit W, so the columns
+// before the first vector (fewer than W) have bits of their own.
+template <class T>
+__host__ __device__ inline uint32_t bitmap_words(uint32_t V)
+{
+    return (V + 2 * T::W) / 32 + 1;
+}
+
+__device__ __forceinline__ double wave_sum64(double v)
+{
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        v += __shfl_xor(v, m);
+    return v;
+}
+
+// LDS written by one lane of a wave and read by another of the same wave.
+__device__ __forceinline__ void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One wave reads the row's list and fills `l`.  fp64: a row's loss is a small
+// difference of these sums.
+template <class T, bool TAIL>
+__device__ __forceinline__ void read_teacher(const typename DistillOp<TAIL>::Args& a, size_t row,
+                                             const typename T::S* z, uint32_t V, uint32_t head,
+                                             uint32_t words, uint32_t lane, const TeacherLds& l)
+{
+    for (uint32_t i = lane; i < words; i += kWave)
+        l.bits[i] = 0;
+    const int64_t* idx = a.idx + row * a.ldk;
+    const float* val = a.val + row * a.ldk;
+    float top = -INFINITY, ref = -INFINITY;
+    for (uint32_t k = lane; k < a.K; k += kWave) {
+        const int64_t i = idx[k];
+        const float v = val[k];
+        const bool in = (uint64_t)i < V;
+        const float zk = in ? T::widen(z[i]) : -INFINITY;
+        l.col[k] = in ? (int)i : -1;
+        l.q[k] = in ? v : -INFINITY;
+        l.z[k] = zk;
+        top = fmaxf(top, in ? v : -INFINITY);
+        ref = fmaxf(ref, zk);
+    }
+    top = wave_reduce<OpMax>(top);
+    ref = reference(wave_reduce<OpMax>(ref));
+    wave_lds_fence();
+    const double scale = a.scale;
+    double shift;
+    if constexpr (TAIL) {
+        shift = a.teacher_lse[row];
+    } else {
+        double s = 0.0;
+        const double most = reference(top);
+        for (uint32_t k = lane; k < a.K; k += kWave)
+            s += exp(((double)l.q[k] - most) * scale);
+        shift = most * scale + log(wave_sum64(s));
+    }
+    double sum = 0.0, cross = 0.0;
+    int listed = 0;
+    bool again = false;
+    for (uint32_t k = lane; k < a.K; k += kWave) {
+        const double lq = (double)l.q[k] * scale - shift, q = exp(lq);
+        const int col = l.col[k];
+        l.q[k] = col >= 0 ? (float)q : 0.0f;
+        if (col < 0)
+            continue;
+        sum += q;
+        if (q != 0.0) // an entry of no probability adds nothing, whatever its logit
+            cross += q * (lq - ((double)l.z[k] - (double)ref) * scale);
+        const uint32_t at = (uint32_t)col + T::W - head;
+        const uint32_t bit = 1u << (at & 31);
+        const bool seen = atomicOr(&l.bits[at >> 5], bit) & bit;
+        again |= seen;
+        listed += !seen;
+    }
+    sum = wave_sum64(sum);
+    cross = wave_sum64(cross);
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        listed += __shfl_xor(listed, m);
+    wave_lds_fence();
+    if (__any(again)) {
+        // A column listed more than once: its first entry takes the sum of
+        // the probabilities, the others are marked.
+        for (uint32_t k = lane; k < a.K; k += kWave) {
+            const int col = l.col[k] & 0x7fffffff;
+            if (col == 0x7fffffff)
+                continue;
+            uint32_t first = k;
+            float q = 0.0f;
+            for (uint32_t j = 0; j < a.K; ++j)
+                if ((l.col[j] & 0x7fffffff) == col) {
+                    first = j < first ? j : first;
+                    q += l.q[j];
+                }
+            if (first == k)
+                l.q[k] = q;
+            else
+                l.col[k] = col | (int)0x80000000;
+        }
+    }
+    if (lane == 0) {
+        *l.sum = sum;
+        *l.cross = cross;
+        l.state[0] = TAIL || top != -INFINITY;
+        l.state[1] = listed;
+        l.state[2] = __float_as_int(ref);
+    }
+    wave_lds_fence();
+}
+
+// ---- one read and one write per row ----------------------------------------
+//
+// GT threads share a row (64: four rows per workgroup of 256).  Thread t
+// holds vectors t, t + GT, ... of the row, NV of them; MULTI rows are longer
+// than that and come in chunks of GT NV vectors, of which the last one read
+// is still there when the gradient is written and the others are read again
+// (from the caches: the rows in flight on 256 compute units fit there).
+// GRAD: the gradient is written.
+template <class T, int GT, int NV, bool MULTI, bool GRAD, class Op>
+__global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
+    const typename T::S* z, typename T::S* dz, uint32_t rows, uint32_t V, size_t ld, size_t ldd,
+    float c, typename Op::Args args)
+{
+    typedef typename T::S S;
+    constexpr int kRowsPerGroup = GT < 256 ? 256 / GT : 1;
+    extern __shared__ __align__(16) char dynamic_lds[];
+    __shared__ float parts[GT > kWave ? 3 * (GT / kWave) : 1];
+    const uint32_t t = threadIdx.x % GT;
+    const uint32_t group = __builtin_amdgcn_readfirstlane(threadIdx.x / GT);
+    const uint32_t row = blockIdx.x * kRowsPerGroup + group;
+    if (row >= rows)
+        return; // whole waves; a group of more than one wave has a row
+    const S* zr = z + (size_t)row * ld;
+    S* dr = GRAD ? dz + (size_t)row * ldd : nullptr;
+    const bool leader = t == 0;
+    const Span sp = Span::of<T>(zr, V);
+    const typename Op::Row r = Op::begin(args, row, V);
+    if (!r.live) {
+        Op::dead(args, row, leader);
+        if constexpr (GRAD)
+            write_zeros<T, GT>(dr, sp, t);
+        return;
+    }
+    const u32x4_t* vec = reinterpret_cast<const u32x4_t*>(zr + sp.head);
+    constexpr uint32_t kChunk = GT * NV;
+    const uint32_t chunks = MULTI ? (sp.nvec + kChunk - 1) / kChunk : 1;
+    // Every load of the row (of its first chunk) is under way before the
+    // first is used.
+    u32x4_t v[NV];
+    load_chunk<T, GT, NV, !(MULTI && GRAD)>(vec, 0, sp.nvec, t, v);
+    const bool has_one = t < sp.singles;
+    const uint32_t at_one = has_one ? sp.single(t) : 0;
+    const float one = has_one ? T::widen(zr[at_one]) : -INFINITY;
+
+    Stat st = {-INFINITY, 0.0f, 0.0f};
+    float zy = 0.0f;
+    const uint32_t words = Op::kList ? bitmap_words<T>(V) : 0;
+    if constexpr (Op::kList) {
+        const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
+        if (t < kWave)
+            read_teacher<T, Op::kTail>(args, row, zr, V, sp.head, words, t, l);
+        if constexpr (GT > kWave && Op::kTail)
+            __syncthreads(); // the sums need the bitmap
+        auto fold = [&](uint32_t first, float single, bool skip) {
+            if constexpr (Op::kTail)
+                fold_chunk<T, GT, NV, false>(v, first, sp.nvec, t, single, skip, c,
+                                             TakeUnmarked<T::W>{l.bits, sp.head, sp.nvec}, st);
+            else
+                fold_chunk<T, GT, NV, false>(v, first, sp.nvec, t, single, skip, c, TakeAll{}, st);
+        };
+        bool skip = false;
+        if constexpr (Op::kTail)
+            skip = has_one && TakeUnmarked<T::W>{l.bits, sp.head, sp.nvec}.skip_one(at_one);
+        fold(0, one, skip);
+        if constexpr (MULTI)
+            for (uint32_t ch = 1; ch < chunks; ++ch) {
+                load_chunk<T, GT, NV, !GRAD>(vec, ch * kChunk, sp.nvec, t, v);
+                fold(ch * kChunk, -INFINITY, false);
+            }
+    } else {
+        zy = T::widen(zr[r.y]);
+        fold_chunk<T, GT, NV, Op::kEntropy>(v, 0, sp.nvec, t, one, false, c, TakeAll{}, st);
+        if constexpr (MULTI)
+            for (uint32_t ch = 1; ch < chunks; ++ch) {
+                load_chunk<T, GT, NV, !GRAD>(vec, ch * kChunk, sp.nvec, t, v);
+                fold_chunk<T, GT, NV, Op::kEntropy>(v, ch * kChunk, sp.nvec, t, -INFINITY, false,
+                                                    c, TakeAll{}, st);
+            }
+    }
+    st = combine<GT, Op::kEntropy>(st, c, parts);
+    const Exponent ex(reference(st.m), c);
+
+    Slope slope;
+    float fix = 0.0f, factor = 0.0f, mass = 0.0f;
+    if constexpr (Op::kList) {
+        const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
+        if (!l.state[0]) { // no teacher: the row does not count
+            Op::dead(args, row, leader);
+            if constexpr (GRAD)
+                write_zeros<T, GT>(dr, sp, t);
+            return;
+        }
+        const double Q = *l.sum;
+        double rest = 0.0, outside = st.s;
+        if constexpr (Op::kTail) {
+            float in = 0.0f;
+            for (uint32_t k = t & 63; k < args.K; k += kWave)
+                if (l.col[k] >= 0)
+                    in += exp2_fast(ex.at(l.z[k]));
+            in = wave_reduce<OpSum>(in);
+            st.s += in;
+            if (l.state[1] < (int)V && Q < 1.0)
+                rest = 1.0 - Q;
+        }
+        if (leader) {
+            const RowLogs logs(st, args.scale);
+            const double ref = __int_as_float(l.state[2]);
+            double loss = *l.cross + Q * ((logs.ref - ref) * logs.scale + logs.ln_s);
+            if (Op::kTail && rest > 0.0)
+                loss += rest * (log(rest) - log(outside) + logs.ln_s);
+            args.row_loss[row] = (double)r.weight * loss;
+            if (args.row_loss_out)
+                args.row_loss_out[row] = (float)loss;
+        }
+        factor = r.weight * args.scale;
+        mass = (float)(Q + rest);
+        double a = (Q + rest) / (double)st.s;
+        if (Op::kTail && outside > 0.0)
+            a -= rest / outside;
+        slope = {(float)((double)factor * a), 0.0f};
+    } else {
+        slope = Op::done(args, r, row, st, zy, leader, fix);
+    }
+
+    if constexpr (GRAD) {
+        S* dvec = dr + sp.head;
+        write_chunk<T, GT, NV, Op::kEntropy>(v, dvec, (chunks - 1) * kChunk, sp.nvec, t, ex, slope);
+        if constexpr (MULTI)
+            for (uint32_t ch = chunks - 1; ch-- > 0;) {
+                load_chunk<T, GT, NV, true>(vec, ch * kChunk, sp.nvec, t, v);
+                write_chunk<T, GT, NV, Op::kEntropy>(v, dvec, ch * kChunk, sp.nvec, t, ex, slope);
+            }
+        if (has_one)
+            dr[at_one] = T::narrow(slope_at<Op::kEntropy>(ex.at(one), slope));
+        // The few columns with more to them are written again, after the
+        // stores above.
+        if constexpr (Op::kList) {
+            const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words,
+                               args.K);
+            if constexpr (GT > kWave)
+                __syncthreads();
+            for (uint32_t k = t; k < args.K; k += GT)
+                if (l.col[k] >= 0)
+                    dr[l.col[k]] = T::narrow(
+                        factor * (exp2_fast(ex.at(l.z[k])) / st.s * mass - l.q[k]));
+        } else {
+            uint32_t owner = 0;
+            if (r.y >= sp.head && r.y < sp.tail)
+                owner = (r.y - sp.head) / T::W % GT;
+            else
+                owner = r.y < sp.head ? r.y : r.y - sp.tail + sp.head;
+            if (t == owner)
+                dr[r.y] = T::narrow(slope_at<Op::kEntropy>(ex.at(zy), slope) + fix);
+        }
+    }
+}
+
+// ---- a gradient whose statistics are there already --------------------------
+//
+// A segment of GT * NV vectors of a row per group of threads: nothing is
+// reduced, so rows are cut as finely as the device wants.
+
+// Gradient of the log-probability (glogp) and the entropy (gentropy):
+//   dz = scale (g (delta_vy - p) - h p (ln p + H)),  ln p = scale z - lse.
+// p = 2^((z - lse / scale) c): the row's reference is lse / scale.
+template <bool ENT>
+struct LogprobGradOp {
+    static constexpr bool kEntropy = ENT;
+    struct Args {
+        const int64_t* targets;
+        const float *lse, *entropy, *glogp, *gentropy;
+        float scale;
+        double inverse; // 1 / scale
+    };
+    struct Row {
+        bool live, hit;
+        uint32_t y;
+        float ref, fix;
+        Slope slope;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V, float c)
+    {
+        Row r;
+        const int64_t y = a.targets[row];
+        r.hit = (uint64_t)y < V;
+        r.y = r.hit ? (uint32_t)y : 0u;
+        const float g = r.hit ? a.glogp[row] : 0.0f, h = ENT ? a.gentropy[row] : 0.0f;
+        r.live = g != 0.0f || h != 0.0f;
+        const double ref = (double)a.lse[row] * a.inverse;
+        r.ref = (float)ref;
+        // p = 2^((z - ref) c); what fp32 drops of ref is one more factor.
+        const float lost = fabsf(r.ref) < INFINITY ? (float)((ref - (double)r.ref) * (double)c) : 0.0f;
+        const float back = exp2f(-lost) * a.scale;
+        r.fix = g * a.scale;
+        r.slope = {-back * g, 0.0f};
+        if constexpr (ENT) {
+            r.slope.a = -back * fmaf(h, a.entropy[row] - lost * (float)kLn2, g);
+            r.slope.b = -back * h * (float)kLn2;
+        }
+        return r;
+    }
+};
+
+// Second pass of the preference loss: the row's slope times d logp / dz.
+struct PreferenceGradOp {
+    static constexpr bool kEntropy = false;
+    struct Args {
+        const int64_t* targets;
+        const float2* stat;
+        const float* slope;
+    };
+    struct Row {
+        bool live, hit;
+        uint32_t y;
+        float ref, fix;
+        Slope slope;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V, float)
+    {
+        Row r;
+        const int64_t y = a.targets[row];
+        r.hit = (uint64_t)y < V;
+        r.y = r.hit ? (uint32_t)y : 0u;
+        const float g = r.hit ? a.slope[row] : 0.0f;
+        r.live = g != 0.0f;
+        const float2 st = a.stat[row];
+        r.ref = reference(st.x);
+        r.fix = g;
+        r.slope = {-g / st.y, 0.0f};
+        return r;
+    }
+};
+
+template <class T, int GT, int NV, class Op>
+__global__ __launch_bounds__(256) void grad_kernel(const typename T::S* z, typename T::S* dz,
+                                                   uint32_t rows, uint32_t V, uint32_t segs,
+                                                   size_t ld, size_t ldd, float c,
+                                                   typename Op::Args args)
+{
+    typedef typename T::S S;
+    constexpr int kGroups = 256 / GT;
+    const uint32_t t = threadIdx.x % GT;
+    const uint32_t item = blockIdx.x * kGroups + __builtin_amdgcn_readfirstlane(threadIdx.x / GT);
+    const uint32_t row = item / segs, first = (item % segs) * (GT * NV);
+    if (row >= rows)
+        return;
+    const S* zr = z + (size_t)row * ld;
+    S* dr = dz + (size_t)row * ldd;
+    const Span sp = Span::of<T>(zr, V);
+    const typename Op::Row r = Op::begin(args, row, V, c);
+    const bool has_one = first == 0 && t < sp.singles;
+    const uint32_t at_one = has_one ? sp.single(t) : 0;
+    if (!r.live) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t j = first + k * GT + t;
+            if (j < sp.nvec)
+                store_vec(dr + sp.head + (size_t)j * T::W, u32x4_t{0, 0, 0, 0});
+        }
+        if (has_one)
+            dr[at_one] = 0;
+        return;
+    }
+    u32x4_t v[NV];
+    load_chunk<T, GT, NV, true>(reinterpret_cast<const u32x4_t*>(zr + sp.head), first, sp.nvec, t,
+                                v);
+    const float one = has_one ? T::widen(zr[at_one]) : 0.0f;
+    // The thread that writes the target's column reads it first: in place,
+    // another thread's read could come after that write.
+    bool mine = false;
+    if (r.hit) {
+        if (r.y >= sp.head && r.y < sp.tail) {
+            const uint32_t j = (r.y - sp.head) / T::W;
+            mine = j >= first && j - first < GT * NV && (j - first) % GT == t;
+        } else {
+            mine = has_one && at_one == r.y;
+        }
+    }
+    const float zy = mine ? T::widen(zr[r.y]) : 0.0f;
+    const Exponent ex(r.ref, c);
+    write_chunk<T, GT, NV, Op::kEntropy>(v, dr + sp.head, first, sp.nvec, t, ex, r.slope);
+    if (has_one)
+        dr[at_one] = T::narrow(slope_at<Op::kEntropy>(ex.at(one), r.slope));
+    if (mine)
+        dr[r.y] = T::narrow(slope_at<Op::kEntropy>(ex.at(zy), r.slope) + r.fix);
+}
+
+// ---- launches ----------------------------------------------------------------
+
+struct Part { // rows [row0, row0 + rows) of a call, on `stream`
+    size_t row0;
+    uint32_t rows;
+    hipStream_t stream;
+};
+
+inline float exponent_scale(float scale) { return (float)((double)scale * kLog2e); }
+
+template <class T, int GT, int NV, bool MULTI, bool GRAD, class Op>
+void launch_rows_as(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds)
+{
+    typedef typename T::S S;
+    constexpr uint32_t per = GT < 256 ? 256 / GT : 1;
+    const S* z = static_cast<const S*>(m.z) + p.row0 * m.ld;
+    S* dz = GRAD ? static_cast<S*>(m.dz) + p.row0 * m.ldd : nullptr;
+    hipLaunchKernelGGL((row_kernel<T, GT, NV, MULTI, GRAD, Op>), dim3((p.rows + per - 1) / per),
+                       dim3(GT < 256 ? 256 : GT), lds * per, p.stream, z, dz, p.rows,
+                       (uint32_t)m.V, m.ld, m.ldd, exponent_scale(m.scale), args);
+}
+
+// The threads and registers of a row by its length.  With a gradient the row
+// stays in registers, in the smallest group that holds it; without, rows
+// pass through a workgroup of 256.
+template <class T, class Op>
+void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds)
+{
+    const size_t nvec = (m.V + T::W - 1) / T::W;
+    if (!m.dz) {
+        if (nvec <= 64 * 8)
+            launch_rows_as<T, 64, 8, false, false, Op>(m, p, args, lds);
+        else
+            launch_rows_as<T, 256, 8, true, false, Op>(m, p, args, lds);
+    } else if constexpr (Op::kHasGrad) {
+        if (nvec <= 64 * 8)
+            launch_rows_as<T, 64, 8, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 256 * 8)
+            launch_rows_as<T, 256, 8, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 256 * 16)
+            launch_rows_as<T, 256, 16, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 512 * 16)
+            launch_rows_as<T, 512, 16, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 512 * 32)
+            launch_rows_as<T, 512, 32, false, true, Op>(m, p, args, lds);
+        else
+            launch_rows_as<T, 512, 32, true, true, Op>(m, p, args, lds);
+    }
+}
+
+template <class F>
+hipError_t each_part(size_t rows, size_t most, hipStream_t stream, F f)
+{
+    for (size_t row0 = 0; row0 < rows; row0 += most) {
+        const size_t n = rows - row0 < most ? rows - row0 : most;
+        f(Part{row0, (uint32_t)n, stream});
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+constexpr int kGradVecs = 4; // vectors per thread of the gradient kernel
+
+// Workgroups per row of the gradient kernel; 0: several rows per workgroup.
+template <class T>
+uint32_t grad_segments(const Logits& m)
+{
+    const size_t nvec = (m.V + T::W - 1) / T::W, per = 256 * kGradVecs;
+    return nvec <= 64 * kGradVecs ? 0 : (uint32_t)((nvec + per - 1) / per);
+}
+
+// Rows of one launch of the gradient kernel: at most 2^32 - 1 work-items.
+template <class T>
+size_t grad_rows_per_launch(const Logits& m)
+{
+    const size_t segs = grad_segments<T>(m) ? grad_segments<T>(m) : 1;
+    const size_t fit = ((size_t(1) << 24) - 1) / segs;
+    return fit < kRowsPerLaunch ? fit : kRowsPerLaunch;
+}
+
+template <class T, class Op>
+void launch_grad(const Logits& m, const Part& p, const typename Op::Args& args)
+{
+    typedef typename T::S S;
+    const S* z = static_cast<const S*>(m.z) + p.row0 * m.ld;
+    S* dz = static_cast<S*>(m.dz) + p.row0 * m.ldd;
+    const float c = exponent_scale(m.scale);
+    const uint32_t segs = grad_segments<T>(m);
+    if (!segs)
+        hipLaunchKernelGGL((grad_kernel<T, 64, kGradVecs, Op>), dim3((p.rows + 3) / 4), dim3(256),
+                           0, p.stream, z, dz, p.rows, (uint32_t)m.V, 1u, m.ld, m.ldd, c, args);
+    else
+        hipLaunchKernelGGL((grad_kernel<T, 256, kGradVecs, Op>), dim3(p.rows * segs), dim3(256), 0,
+                           p.stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
+}
+
+} // namespace rowloss
+
+// ---- the calls of one element type -------------------------------------------
+
+template <class T>
+hipError_t RowLoss<T>::logprob(const LogprobCall& a, const DeviceInfo&, hipStream_t stream)
+{
+    using namespace rowloss;
+    return each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
+        const size_t r = p.row0;
+        if (a.entropy)
+            launch_rows_op<T, LogprobOp<true>>(
+                a.m, p, {a.targets + r, a.logp + r, a.lse + r, a.entropy + r, a.m.scale}, 0);
+        else
+            launch_rows_op<T, LogprobOp<false>>(
+                a.m, p, {a.targets + r, a.logp + r, a.lse + r, nullptr, a.m.scale}, 0);
+    });
+}
+
+template <class T>
+hipError_t RowLoss<T>::logprob_grad(const LogprobGradCall& a, const DeviceInfo&,
+                                    hipStream_t stream)
+{
+    using namespace rowloss;
+    return each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
+        const size_t r = p.row0;
+        const double inverse = 1.0 / (double)a.m.scale;
+        if (a.gentropy)
+            launch_grad<T, LogprobGradOp<true>>(a.m, p,
+                                                {a.targets + r, a.lse + r, a.entropy + r,
+                                                 a.glogp + r, a.gentropy + r, a.m.scale, inverse});
+        else
+            launch_grad<T, LogprobGradOp<false>>(a.m, p,
+                                                 {a.targets + r, a.lse + r, nullptr, a.glogp + r,
+                                                  nullptr, a.m.scale, inverse});
+    });
+}
+
+template <class T>
+hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Workspace& ws,
+                               hipStream_t stream)
+{
+    using namespace rowloss;
+    double* row_loss = static_cast<double*>(ws.partials);
+    const size_t lds = TeacherLds::bytes(bitmap_words<T>((uint32_t)a.m.V), a.K);
+    const float mean = (float)(1.0 / (double)a.m.rows);
+    hipError_t e = hipSuccess;
+    const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
+        const size_t r = p.row0;
+        const float* weight = a.weight ? a.weight + r : nullptr;
+        float* out = a.row_loss ? a.row_loss + r : nullptr;
+        const int64_t* idx = a.idx + r * a.ldk;
+        const float* val = a.val + r * a.ldk;
+        if (a.teacher_lse)
+            launch_rows_op<T, DistillOp<true>>(a.m, p,
+                                               {idx, val, a.teacher_lse + r, weight, (uint32_t)a.K,
+                                                a.ldk, a.m.scale, mean, out, row_loss},
+                                               lds);
+        else
+            launch_rows_op<T, DistillOp<false>>(a.m, p,
+                                                {idx, val, nullptr, weight, (uint32_t)a.K, a.ldk,
+                                                 a.m.scale, mean, out, row_loss},
+                                                lds);
+        const hipError_t s = launch_loss_sum(row_loss, p.rows, a.loss, a.accum || r, stream);
+        e = e == hipSuccess ? s : e;
+    });
+    return f == hipSuccess ? e : f;
+}
+
+template <class T>
+hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Workspace& ws,
+                              hipStream_t stream)
+{
+    using namespace rowloss;
+    double* row_loss = static_cast<double*>(ws.partials);
+    const float mean = (float)(1.0 / (double)a.m.rows);
+    hipError_t e = hipSuccess;
+    const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
+        const size_t r = p.row0;
+        auto launch = [&](auto op) {
+            typedef decltype(op) Op;
+            launch_rows_op<T, Op>(
+                a.m, p,
+                {a.targets + r, a.old_logp + r, a.ref_logp ? a.ref_logp + r : nullptr,
+                 a.advantage + r, a.weight ? a.weight + r : nullptr, 1.0 - (double)a.clip_low,
+                 1.0 + (double)a.clip_high, (double)a.kl_coef, (double)a.entropy_coef, a.m.scale,
+                 mean, a.logp + r, a.entropy ? a.entropy + r : nullptr, row_loss},
+                0);
+        };
+        if (a.entropy || a.entropy_coef != 0.0f)
+            launch(PolicyOp<true>{});
+        else
+            launch(PolicyOp<false>{});
+        const hipError_t s = launch_loss_sum(row_loss, p.rows, a.loss, a.accum || r, stream);
+        e = e == hipSuccess ? s : e;
+    });
+    return f == hipSuccess ? e : f;
+}
+
+template <class T>
+hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo&, const Workspace& ws,
+                                  hipStream_t stream)
+{
+    using namespace rowloss;
+    // Workspace: fp64 log-probabilities, (maximum, sum), slopes, pair losses.
+    double* logp = static_cast<double*>(ws.partials);
+    float2* stat = reinterpret_cast<float2*>(logp + kPrefRowsMax);
+    double* pair_loss = reinterpret_cast<double*>(stat + kPrefRowsMax);
+    float* slope = reinterpret_cast<float*>(pair_loss + kPrefPairsMax);
+    static_assert(kPrefRowsMax * (8 + 8 + 4) + kPrefPairsMax * 8 <= (size_t(16) << 20),
+                  "the statistics fit the workspace");
+    Logits read = a.m;
+    read.dz = nullptr;
+    hipError_t e = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
+        launch_rows_op<T, PreferenceOp>(
+            read, p, {a.targets + p.row0, stat + p.row0, logp + p.row0, slope + p.row0}, 0);
+    });
+    if (e == hipSuccess)
+        e = launch_preference_pairs(a, logp, slope, pair_loss, stream);
+    if (e == hipSuccess && a.m.dz)
+        e = each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
+            const size_t r = p.row0;
+            launch_grad<T, PreferenceGradOp>(a.m, p, {a.targets + r, stat + r, slope + r});
+        });
+    if (e == hipSuccess)
+        e = launch_loss_sum(pair_loss, a.pairs, a.loss, a.accum, stream);
+    return e;
+}
+
+} // namespace red

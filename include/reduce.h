@@ -2,7 +2,7 @@
  * reduce.h -- C ABI of libreduce: dense-array reduction on AMD Instinct
  * MI355X (gfx950).
  *
- * Two families of operations:
+ * Three families of operations:
  *
  *   1. A 1-D fp32 vector reduced to one scalar by sum, max or min, with an
  *      accum mode that folds the old destination value into the result
@@ -18,6 +18,12 @@
  *      columns; "Constraints" -- row-major layout, dst and src share the
  *      element type, the column counts agree, and a tile with zero valid
  *      rows or columns returns early).
+ *
+ *   3. Losses over rows of logits: each row of an fp32, fp16 or bf16 matrix
+ *      reduced by its log-sum-exp, the rows joined into a loss, and the
+ *      loss's gradient with respect to the matrix: token log-probabilities,
+ *      distillation from a teacher's largest logits, a clipped policy loss
+ *      and a preference loss.
  *
  * Conventions shared by every entry point:
  *
@@ -36,7 +42,9 @@
  *     reports what hipGetLastError() returned.  Faults raised while a
  *     kernel runs surface at the caller's next synchronisation, as for any
  *     HIP kernel.
- *   - The destination must not overlap the source (not checked).
+ *   - The destination must not overlap the source (not checked).  A
+ *     gradient of logits may be written over the logits themselves:
+ *     dlogits == logits with equal row strides.
  *   - Empty input (n == 0, rows == 0, R == 0 or C == 0) returns RED_OK,
  *     enqueues nothing and leaves the destination untouched, also under
  *     accum; for column products this is TCOLPROD's early return, and the
@@ -51,8 +59,8 @@
  *     input, device model and library build the result bits never change
  *     between runs.
  *   - Workspace.  The calls that combine per-workgroup partials in a second
- *     kernel (1-D, fused, column and column-product calls, and row calls
- *     with very long rows or very few rows) keep those partials in a
+ *     kernel (1-D, fused, column and column-product calls, row calls
+ *     with very long rows or very few rows, and the losses) keep those partials in a
  *     16 MiB workspace the library allocates on the first such call for a
  *     (device, stream) pair and keeps until red_release_workspace.  For
  *     hipStreamPerThread, which names a different stream in every host
@@ -85,7 +93,7 @@
 extern "C" {
 #endif
 
-#define RED_ABI_VERSION 2
+#define RED_ABI_VERSION 3
 
 /* A hipStream_t, passed as an opaque pointer (NULL: the null stream). */
 typedef void* red_stream_t;
@@ -93,7 +101,8 @@ typedef void* red_stream_t;
 enum red_status {
     RED_OK = 0,
     RED_ERR_INVALID = 1, /* null pointer for non-empty input, ld too small,
-                            or a size whose byte extent overflows size_t */
+                            a size whose byte extent overflows size_t, or a
+                            number outside the range its argument states */
     RED_ERR_ALIGN = 2,   /* a pointer not aligned to its element size */
     RED_ERR_NOMEM = 3,   /* the per-stream workspace could not be allocated */
     RED_ERR_HIP = 4,     /* the HIP runtime reported an error */
@@ -267,6 +276,172 @@ int red_colprod_u16(const uint16_t* src, size_t R, size_t C, size_t ld,
                     uint16_t* dst, red_stream_t stream);
 int red_colprod_u32(const uint32_t* src, size_t R, size_t C, size_t ld,
                     uint32_t* dst, red_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Losses over rows of logits
+ *
+ * Notation: z is a row of V logits, s the scale (1 / temperature),
+ * lse = ln sum_v exp(s z_v), ln p_v = s z_v - lse, H = -sum_v p_v ln p_v.
+ *
+ * logits  : row-major rows x V matrix of f32, f16 or bf16 (16-bit types as
+ *           uint16_t bit patterns), aligned to its element size only; row r
+ *           starts at logits + r * ld, ld >= V, V < 2^31.  Elements between
+ *           V and ld are never read.
+ * dlogits : the gradient, same element type, row stride ldd >= V (not
+ *           accumulated: every one of its rows x V elements is written, none
+ *           beyond).  NULL where a call allows it: the loss alone.  It may
+ *           be logits itself, with ldd == ld.
+ * targets : rows column numbers.  A row whose target is not in [0, V) (-100,
+ *           say) does not count: its log-probability and its gradient are 0.
+ * scale   : finite and positive.
+ * weight  : one fp32 factor per row (for the preference loss, per pair) in
+ *           the sum that makes the loss; NULL: 1 / rows each (1 / pairs).  A
+ *           row of weight 0 does not count: its outputs are 0 and its logits
+ *           are not looked at.  A mask and a normaliser are both weights.
+ * loss    : one fp32 value, the weighted sum of row losses; accum != 0 adds
+ *           it to the old value.
+ *
+ * Losses carry their gradient: a call given dlogits writes
+ * d loss / d logits of its own sum (a factor from later in a program goes
+ * into the weights), in the same pass over the logits.
+ *
+ * Logits are widened exactly to fp32.  A thread's statistics are fp32, what
+ * is computed once per row and the sums over rows are fp64, and every result
+ * is rounded once to its type.  A term below 2^-126 of its row's largest
+ * counts as 0.  Logits of -inf have probability 0.  A row with a NaN or +inf,
+ * or with nothing but -inf, has NaN results unless it does not count; its
+ * neighbours are not touched by it.  A row filled with one finite value is
+ * uniform, the type's lowest value included.
+ * All results are deterministic.
+ * ------------------------------------------------------------------- */
+
+/* logp[r] = ln p_target, lse[r], and, where entropy is not NULL,
+ * entropy[r] = H.  A row whose target is no column still has its lse and
+ * entropy. */
+int red_token_logprob_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                          const int64_t* targets, float scale, float* logp, float* lse,
+                          float* entropy, red_stream_t stream);
+int red_token_logprob_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                          const int64_t* targets, float scale, float* logp, float* lse,
+                          float* entropy, red_stream_t stream);
+int red_token_logprob_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                           const int64_t* targets, float scale, float* logp, float* lse,
+                           float* entropy, red_stream_t stream);
+
+/* The gradient of red_token_logprob: with g = glogp[r] and h = gentropy[r]
+ * the gradients of the row's two outputs,
+ *   dlogits[r, v] = s (g (delta_{v, target} - p_v) - h p_v (ln p_v + H)).
+ * lse and entropy are what the forward call wrote.  gentropy and entropy
+ * are both NULL where the entropy has no gradient.  Where g (or the target's
+ * column) and h are 0 the row's logits are not looked at. */
+int red_token_logprob_grad_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                               const int64_t* targets, float scale, const float* lse,
+                               const float* entropy, const float* glogp, const float* gentropy,
+                               float* dlogits, size_t ldd, red_stream_t stream);
+int red_token_logprob_grad_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                               const int64_t* targets, float scale, const float* lse,
+                               const float* entropy, const float* glogp, const float* gentropy,
+                               uint16_t* dlogits, size_t ldd, red_stream_t stream);
+int red_token_logprob_grad_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                                const int64_t* targets, float scale, const float* lse,
+                                const float* entropy, const float* glogp, const float* gentropy,
+                                uint16_t* dlogits, size_t ldd, red_stream_t stream);
+
+/* Distillation from a teacher of which each row keeps K entries: columns
+ * idx[r * ldk + k] and their logits val[r * ldk + k] (fp32; log-probabilities
+ * are logits too).  An entry whose column is not in [0, V) is padding.
+ * 1 <= K <= 1024, ldk >= K, V <= 393216.
+ *
+ * teacher_lse NULL: the teacher is the softmax of the row's entries,
+ *   q_k = exp(s val_k) / sum_j exp(s val_j),
+ *   row loss = sum_k q_k (ln q_k - ln p_{idx_k}).
+ * A row of padding alone (or of -inf alone) does not count.
+ *
+ * teacher_lse given (ln sum exp(s .) over the teacher's whole row): q_k =
+ * exp(s val_k - teacher_lse), and the columns not listed, with the teacher's
+ * rest q_r = 1 - sum q and the student's p_r = their sum of p, count as one:
+ *   row loss = sum_k q_k (ln q_k - ln p_{idx_k}) + q_r (ln q_r - ln p_r).
+ * The rest is 0 where sum q >= 1 or every column is listed.
+ *
+ * An entry of probability 0 adds nothing.  Each entry of a column listed
+ * more than once counts.  row_loss, where not NULL, takes the rows' losses
+ * without their weights.  (The factor 1 / s^2 that some recipes put on this
+ * loss goes into the weights.) */
+int red_distill_topk_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                         const int64_t* idx, const float* val, size_t K, size_t ldk,
+                         const float* teacher_lse, const float* weight, float scale,
+                         float* loss, int accum, float* row_loss, float* dlogits, size_t ldd,
+                         red_stream_t stream);
+int red_distill_topk_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                         const int64_t* idx, const float* val, size_t K, size_t ldk,
+                         const float* teacher_lse, const float* weight, float scale,
+                         float* loss, int accum, float* row_loss, uint16_t* dlogits, size_t ldd,
+                         red_stream_t stream);
+int red_distill_topk_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                          const int64_t* idx, const float* val, size_t K, size_t ldk,
+                          const float* teacher_lse, const float* weight, float scale,
+                          float* loss, int accum, float* row_loss, uint16_t* dlogits, size_t ldd,
+                          red_stream_t stream);
+
+/* Clipped policy loss.  With A = advantage[r], ratio = exp(ln p_target -
+ * old_logp[r]) and d = ref_logp[r] - ln p_target,
+ *   row loss = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *              + kl_coef (exp(d) - d - 1) - entropy_coef H.
+ * Where the two products are equal the first one's gradient is taken.
+ * clip_low, clip_high >= 0 (infinity: no bound); kl_coef and entropy_coef
+ * finite; ref_logp may be NULL where kl_coef is 0 and is not read then.
+ * logp takes ln p_target, entropy (NULL: not wanted) H. */
+int red_policy_loss_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                        const int64_t* targets, const float* old_logp, const float* ref_logp,
+                        const float* advantage, const float* weight, float scale,
+                        float clip_low, float clip_high, float kl_coef, float entropy_coef,
+                        float* loss, int accum, float* logp, float* entropy, float* dlogits,
+                        size_t ldd, red_stream_t stream);
+int red_policy_loss_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                        const int64_t* targets, const float* old_logp, const float* ref_logp,
+                        const float* advantage, const float* weight, float scale,
+                        float clip_low, float clip_high, float kl_coef, float entropy_coef,
+                        float* loss, int accum, float* logp, float* entropy, uint16_t* dlogits,
+                        size_t ldd, red_stream_t stream);
+int red_policy_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                         const int64_t* targets, const float* old_logp, const float* ref_logp,
+                         const float* advantage, const float* weight, float scale,
+                         float clip_low, float clip_high, float kl_coef, float entropy_coef,
+                         float* loss, int accum, float* logp, float* entropy, uint16_t* dlogits,
+                         size_t ldd, red_stream_t stream);
+
+/* Preference loss of `pairs` pairs of packed sequences.  Sequence i has the
+ * rows [starts[i], starts[i + 1]); sequences 0 .. pairs - 1 are the chosen
+ * ones and pairs .. 2 pairs - 1 the rejected ones of the same pairs (2 pairs
+ * + 1 starts, nondecreasing; bounds outside [0, rows] are moved into it).
+ * Rows of no sequence do not count.  With S_i the sum of ln p_target over
+ * the sequence's rows that count (average != 0: their mean; an empty
+ * sequence has 0), ref_logp[i] the same from a reference model (NULL: 0),
+ *   D = (S_c - ref_c) - (S_r - ref_r),   h = beta D - margin,
+ *   RED_PREF_SIGMOID: loss = -(1 - smoothing) ln sigmoid(h)
+ *                            - smoothing ln sigmoid(-h)
+ *   RED_PREF_HINGE  : loss = max(0, 1 - h)
+ *   RED_PREF_SQUARED: loss = ((h - 1/2) / beta)^2
+ * beta > 0, margin finite, 0 <= smoothing <= 1, rows <= 524288, pairs <=
+ * 131072.  seq_logp takes the 2 pairs values S_i.  The logits are read twice
+ * when there is a gradient: it needs the whole pair's sum. */
+enum red_preference { RED_PREF_SIGMOID = 0, RED_PREF_HINGE = 1, RED_PREF_SQUARED = 2 };
+int red_preference_loss_f32(const float* logits, size_t rows, size_t V, size_t ld,
+                            const int64_t* targets, const int64_t* starts, size_t pairs,
+                            const float* ref_logp, const float* weight, int kind, float beta,
+                            float margin, float smoothing, int average, float* loss, int accum,
+                            float* seq_logp, float* dlogits, size_t ldd, red_stream_t stream);
+int red_preference_loss_f16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                            const int64_t* targets, const int64_t* starts, size_t pairs,
+                            const float* ref_logp, const float* weight, int kind, float beta,
+                            float margin, float smoothing, int average, float* loss, int accum,
+                            float* seq_logp, uint16_t* dlogits, size_t ldd, red_stream_t stream);
+int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size_t ld,
+                             const int64_t* targets, const int64_t* starts, size_t pairs,
+                             const float* ref_logp, const float* weight, int kind, float beta,
+                             float margin, float smoothing, int average, float* loss, int accum,
+                             float* seq_logp, uint16_t* dlogits, size_t ldd,
+                             red_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * Utilities
