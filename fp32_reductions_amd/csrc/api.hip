@@ -30,6 +30,8 @@ using red::Workspace;
 // Fixed workspace per (device, stream) for partial results.  The kernels
 // size their grids so that they never need more than this.
 constexpr size_t kPartialBytes = size_t(16) << 20;
+// The workspace's counter lies behind the partials, on cache lines of its own.
+constexpr size_t kCounterBytes = 256;
 
 // One workspace and the lock a call holds while it enqueues the kernels
 // that use it: the first pass writes the partials and the second reads
@@ -142,13 +144,20 @@ int find_slot(int dev, hipStream_t stream, std::shared_ptr<Slot>* out)
     if (fail && fail[0] == '1')
         return RED_ERR_NOMEM;
     void* base = nullptr;
-    if (hipMalloc(&base, kPartialBytes) != hipSuccess) {
+    if (hipMalloc(&base, kPartialBytes + kCounterBytes) != hipSuccess) {
         (void)hipGetLastError(); // clear the sticky allocation error
         return RED_ERR_NOMEM;
     }
     auto slot = std::make_shared<Slot>();
     slot->ws.partials = base;
     slot->ws.partial_bytes = kPartialBytes;
+    slot->ws.counter = reinterpret_cast<unsigned*>(static_cast<char*>(base) + kPartialBytes);
+    // Before the workspace's first use, on the stream that uses it.
+    (void)hipGetLastError();
+    if (red::launch_fill_u32(slot->ws.counter, kCounterBytes / 4, 0, stream) != hipSuccess) {
+        (void)hipFree(base);
+        return RED_ERR_HIP;
+    }
     g_ws.emplace(key, slot);
     *out = slot;
     return RED_OK;

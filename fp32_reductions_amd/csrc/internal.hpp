@@ -16,6 +16,9 @@ enum class OpKind { Sum, Max, Min };
 struct Workspace {
     void* partials = nullptr;
     size_t partial_bytes = 0;
+    // A count of arrivals, zero between launches (null in scratch that has
+    // none).  A launch that counts leaves it at zero again.
+    unsigned* counter = nullptr;
 };
 
 // Launch geometry chosen by the host from the device.

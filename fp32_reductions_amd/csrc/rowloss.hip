@@ -8,6 +8,7 @@
 #include "device.hpp"
 #include "reduce.h"
 #include "rowloss.hpp"
+#include "rowloss_join.hpp"
 
 namespace red {
 namespace {
@@ -53,7 +54,7 @@ struct PairArgs {
     const int64_t *targets, *starts;
     const float *ref_logp, *weight;
     float* seq_logp;
-    double* pair_loss;
+    Join join;
     int64_t rows, V;
     uint32_t pairs;
     int kind, average;
@@ -114,14 +115,17 @@ __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
     if (threadIdx.x == 0) {
         a.seq_logp[p] = (float)seq[0].logp;
         a.seq_logp[(uint64_t)a.pairs + p] = (float)seq[1].logp;
-        a.pair_loss[p] = w != 0.0 ? w * loss : 0.0;
+        a.join.put(p, w != 0.0 ? w * loss : 0.0);
     }
+    const unsigned before = threadIdx.x < kWave ? a.join.arrive() : 0;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const float mine = (float)((side ? -g : g) / seq[side].count);
         for (int64_t r = seq[side].begin + threadIdx.x; r < seq[side].end; r += 256)
             a.row_slope[r] = mine;
     }
+    if (threadIdx.x < kWave)
+        a.join.finish(before, a.pairs);
 }
 
 } // namespace
@@ -135,15 +139,16 @@ hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int ac
 }
 
 hipError_t launch_preference_pairs(const PreferenceCall& a, const double* row_logp,
-                                   float* row_slope, double* pair_loss, hipStream_t stream)
+                                   float* row_slope, const Join& join, hipStream_t stream)
 {
     const PairArgs args = {row_logp,     row_slope,  a.targets,         a.starts,
-                           a.ref_logp,   a.weight,   a.seq_logp,        pair_loss,
+                           a.ref_logp,   a.weight,   a.seq_logp,        join,
                            (int64_t)a.m.rows, (int64_t)a.m.V, (uint32_t)a.pairs, a.kind,
                            a.average,    a.beta,     a.margin,          a.smoothing};
     hipLaunchKernelGGL(preference_pairs_kernel, dim3((uint32_t)a.pairs), dim3(256), 0, stream,
                        args);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? sum_joined(join, a.pairs, stream) : e;
 }
 
 #define RED_BY_TYPE(t, call)                        \

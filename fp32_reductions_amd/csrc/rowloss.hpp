@@ -114,8 +114,9 @@ extern template struct RowLoss<ElemBF16>;
 hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int accum,
                            hipStream_t stream);
 // The pairs of a preference loss: from the log-probabilities of the rows to
-// the sequences', the pairs' losses and the rows' slopes (rowloss.hip).
+// the sequences', the rows' slopes and the loss (rowloss.hip).
+struct Join;
 hipError_t launch_preference_pairs(const PreferenceCall& a, const double* row_logp,
-                                   float* row_slope, double* pair_loss, hipStream_t stream);
+                                   float* row_slope, const Join& join, hipStream_t stream);
 
 } // namespace red

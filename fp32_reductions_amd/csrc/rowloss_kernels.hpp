@@ -30,6 +30,7 @@
 
 #include "device.hpp"
 #include "rowloss.hpp"
+#include "rowloss_join.hpp"
 
 namespace red {
 
@@ -194,6 +195,12 @@ template <class T, int GT, int NV, bool STREAM>
 __device__ __forceinline__ void load_chunk(const u32x4_t* base, uint32_t first, uint32_t nvec,
                                            uint32_t t, u32x4_t (&v)[NV])
 {
+    if (first + NV * GT <= nvec) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            v[k] = load_vec<STREAM>(base + first + k * GT + t);
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const uint32_t j = first + k * GT + t;
@@ -246,17 +253,17 @@ struct TakeUnmarked {
     }
 };
 
-// Folds the chunk v (vectors first + k GT + t) and the single element `one`
-// into st: first the maximum, then the sums against it.
-template <class T, int GT, int NV, bool ENT, class Take>
-__device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t first, uint32_t nvec,
+// Folds the NG vectors first + k GT + t and the single element `one` into st:
+// first the maximum, then the sums against it.
+template <class T, int GT, int NG, bool ENT, class Take>
+__device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t first, uint32_t nvec,
                                            uint32_t t, float one, bool skip_one, float c,
                                            const Take& take, Stat& st)
 {
     constexpr int W = T::W;
     float m0 = fmaxf(st.m, one), m1 = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    for (int k = 0; k < NG; ++k) {
         if (k && first + k * GT >= nvec)
             break;
         float f[W];
@@ -273,9 +280,9 @@ __device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t firs
     const float d = fmaxf((st.m - ref) * c, kLowest), r = exp2_fast(d);
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
     const bool wide = is_wide(mc);
-    auto sums = [&](auto exponent) {
+    auto sums = [&](auto exponent) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
+        for (int k = 0; k < NG; ++k) {
             if (k && first + k * GT >= nvec)
                 break;
             float f[W];
@@ -314,6 +321,29 @@ __device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t firs
         st.u = fmaf(r, fmaf(st.s, d, st.u), back * fmaf(-delta, sum, u[0] + u[1]));
     st.s = fmaf(st.s, r, back * sum);
     st.m = m;
+}
+
+// Folds a chunk of NV vectors and one single element, kFold vectors at a
+// time: while the first are folded the others are still on their way.
+constexpr int kFold = 8;
+template <class T, int GT, int NV, bool ENT, class Take>
+__device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t first, uint32_t nvec,
+                                           uint32_t t, float one, bool skip_one, float c,
+                                           const Take& take, Stat& st)
+{
+    constexpr int NG = NV < kFold ? NV : kFold;
+    static_assert(NV % NG == 0, "whole groups");
+#pragma unroll
+    for (int g = 0; g < NV; g += NG) {
+        if (g && first + g * GT >= nvec)
+            break;
+        u32x4_t part[NG];
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+            part[k] = v[g + k];
+        fold_group<T, GT, NG, ENT>(part, first + g * GT, nvec, t, g ? -INFINITY : one,
+                                   g ? true : skip_one, c, take, st);
+    }
 }
 
 // Moves st to the maximum m (>= st.m).
@@ -406,7 +436,7 @@ __device__ __forceinline__ void write_chunk(const u32x4_t (&v)[NV], typename T::
 {
     constexpr int W = T::W;
     const Slope slope = ex.fused(exact_slope);
-    auto put = [&](auto exponent) {
+    auto put = [&](auto exponent) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (k && first + k * GT >= nvec)
@@ -493,6 +523,7 @@ struct LogprobOp {
         return {0.0f, 0.0f};
     }
     static __device__ __forceinline__ void dead(const Args&, size_t, bool) {}
+    static __device__ __forceinline__ NoJoin join(const Args&) { return {}; }
 };
 
 // First pass of the preference loss: maximum, sum and log-probability.
@@ -534,6 +565,7 @@ struct PreferenceOp {
             a.slope[row] = 0.0f;
         }
     }
+    static __device__ __forceinline__ NoJoin join(const Args&) { return {}; }
 };
 
 // Clipped policy loss.  With r = exp(logp - old), d = ref - logp:
@@ -549,26 +581,27 @@ struct PolicyOp {
         double clip_min, clip_max, kl, ent;
         float scale, mean;
         float *logp, *entropy;
-        double* row_loss;
+        Join join;
     };
     struct Row {
         bool live;
         uint32_t y;
-        float weight;
+        float weight, old_logp, advantage, ref_logp;
     };
     static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
     {
         const int64_t y = a.targets[row];
         const float w = a.weight ? a.weight[row] : a.mean;
         const bool hit = (uint64_t)y < V;
-        return {hit && w != 0.0f, hit ? (uint32_t)y : 0u, w};
+        return {hit && w != 0.0f, hit ? (uint32_t)y : 0u, w, a.old_logp[row], a.advantage[row],
+                a.ref_logp ? a.ref_logp[row] : 0.0f};
     }
     static __device__ __forceinline__ Slope done(const Args& a, const Row& r, size_t row,
                                                  const Stat& st, float zy, bool leader, float& fix)
     {
         const RowLogs l(st, a.scale);
-        const double logp = l.logp(zy), adv = a.advantage[row], w = r.weight;
-        const double ratio = exp(logp - (double)a.old_logp[row]);
+        const double logp = l.logp(zy), adv = r.advantage, w = r.weight;
+        const double ratio = exp(logp - (double)r.old_logp);
         const double free = ratio * adv;
         const double bound = ratio < a.clip_min   ? a.clip_min
                              : ratio > a.clip_max ? a.clip_max
@@ -578,7 +611,7 @@ struct PolicyOp {
         double loss = free > clipped ? -clipped : -free;
         double g = free > clipped ? 0.0 : -free;
         if (a.ref_logp) {
-            const double d = (double)a.ref_logp[row] - logp, k = expm1(d);
+            const double d = (double)r.ref_logp - logp, k = expm1(d);
             loss += a.kl * (k - d);
             g -= a.kl * k;
         }
@@ -591,7 +624,7 @@ struct PolicyOp {
             a.logp[row] = (float)logp;
             if (ENT && a.entropy)
                 a.entropy[row] = (float)H;
-            a.row_loss[row] = w * loss;
+            a.join.put(row, w * loss);
         }
         const double gw = w * g * l.scale;
         fix = (float)gw;
@@ -609,9 +642,10 @@ struct PolicyOp {
             a.logp[row] = 0.0f;
             if (ENT && a.entropy)
                 a.entropy[row] = 0.0f;
-            a.row_loss[row] = 0.0;
+            a.join.put(row, 0.0);
         }
     }
+    static __device__ __forceinline__ const Join& join(const Args& a) { return a.join; }
 };
 
 // Divergence from a teacher's largest logits.  S: the columns listed, q_k
@@ -631,7 +665,7 @@ struct DistillOp {
         size_t ldk;
         float scale, mean;
         float* row_loss_out;
-        double* row_loss;
+        Join join;
     };
     struct Row {
         bool live;
@@ -645,11 +679,12 @@ struct DistillOp {
     static __device__ __forceinline__ void dead(const Args& a, size_t row, bool leader)
     {
         if (leader) {
-            a.row_loss[row] = 0.0;
+            a.join.put(row, 0.0);
             if (a.row_loss_out)
                 a.row_loss_out[row] = 0.0f;
         }
     }
+    static __device__ __forceinline__ const Join& join(const Args& a) { return a.join; }
 };
 
 // A row's teacher in LDS: its columns (-1: padding; the high bit marks the
@@ -820,18 +855,26 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const bool leader = t == 0;
     const Span sp = Span::of<T>(zr, V);
     const typename Op::Row r = Op::begin(args, row, V);
-    if (!r.live) {
+    const auto join = Op::join(args);
+    auto dead_row = [&]() __attribute__((always_inline)) {
         Op::dead(args, row, leader);
+        const unsigned before = t < kWave ? join.arrive() : 0;
         if constexpr (GRAD)
             write_zeros<T, GT>(dr, sp, t);
+        if (t < kWave)
+            join.finish(before, rows);
+    };
+    if (!r.live) {
+        dead_row();
         return;
     }
     const u32x4_t* vec = reinterpret_cast<const u32x4_t*>(zr + sp.head);
     constexpr uint32_t kChunk = GT * NV;
     const uint32_t chunks = MULTI ? (sp.nvec + kChunk - 1) / kChunk : 1;
+    const uint32_t words = Op::kList ? bitmap_words<T>(V) : 0;
+    u32x4_t v[NV];
     // Every load of the row (of its first chunk) is under way before the
     // first is used.
-    u32x4_t v[NV];
     load_chunk<T, GT, NV, !(MULTI && GRAD)>(vec, 0, sp.nvec, t, v);
     const bool has_one = t < sp.singles;
     const uint32_t at_one = has_one ? sp.single(t) : 0;
@@ -839,38 +882,30 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
 
     Stat st = {-INFINITY, 0.0f, 0.0f};
     float zy = 0.0f;
-    const uint32_t words = Op::kList ? bitmap_words<T>(V) : 0;
+    auto fold_row = [&](bool skip, const auto& take) __attribute__((always_inline)) {
+        fold_chunk<T, GT, NV, Op::kEntropy>(v, 0, sp.nvec, t, one, skip, c, take, st);
+        if constexpr (MULTI)
+            for (uint32_t ch = 1; ch < chunks; ++ch) {
+                load_chunk<T, GT, NV, !GRAD>(vec, ch * kChunk, sp.nvec, t, v);
+                fold_chunk<T, GT, NV, Op::kEntropy>(v, ch * kChunk, sp.nvec, t, -INFINITY, true, c,
+                                                    take, st);
+            }
+    };
     if constexpr (Op::kList) {
         const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
         if (t < kWave)
             read_teacher<T, Op::kTail>(args, row, zr, V, sp.head, words, t, l);
         if constexpr (GT > kWave && Op::kTail)
             __syncthreads(); // the sums need the bitmap
-        auto fold = [&](uint32_t first, float single, bool skip) {
-            if constexpr (Op::kTail)
-                fold_chunk<T, GT, NV, false>(v, first, sp.nvec, t, single, skip, c,
-                                             TakeUnmarked<T::W>{l.bits, sp.head, sp.nvec}, st);
-            else
-                fold_chunk<T, GT, NV, false>(v, first, sp.nvec, t, single, skip, c, TakeAll{}, st);
-        };
-        bool skip = false;
-        if constexpr (Op::kTail)
-            skip = has_one && TakeUnmarked<T::W>{l.bits, sp.head, sp.nvec}.skip_one(at_one);
-        fold(0, one, skip);
-        if constexpr (MULTI)
-            for (uint32_t ch = 1; ch < chunks; ++ch) {
-                load_chunk<T, GT, NV, !GRAD>(vec, ch * kChunk, sp.nvec, t, v);
-                fold(ch * kChunk, -INFINITY, false);
-            }
+        if constexpr (Op::kTail) {
+            const TakeUnmarked<T::W> take{l.bits, sp.head, sp.nvec};
+            fold_row(has_one && take.skip_one(at_one), take);
+        } else {
+            fold_row(false, TakeAll{});
+        }
     } else {
         zy = T::widen(zr[r.y]);
-        fold_chunk<T, GT, NV, Op::kEntropy>(v, 0, sp.nvec, t, one, false, c, TakeAll{}, st);
-        if constexpr (MULTI)
-            for (uint32_t ch = 1; ch < chunks; ++ch) {
-                load_chunk<T, GT, NV, !GRAD>(vec, ch * kChunk, sp.nvec, t, v);
-                fold_chunk<T, GT, NV, Op::kEntropy>(v, ch * kChunk, sp.nvec, t, -INFINITY, false,
-                                                    c, TakeAll{}, st);
-            }
+        fold_row(false, TakeAll{});
     }
     st = combine<GT, Op::kEntropy>(st, c, parts);
     const Exponent ex(reference(st.m), c);
@@ -880,9 +915,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     if constexpr (Op::kList) {
         const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
         if (!l.state[0]) { // no teacher: the row does not count
-            Op::dead(args, row, leader);
-            if constexpr (GRAD)
-                write_zeros<T, GT>(dr, sp, t);
+            dead_row();
             return;
         }
         const double Q = *l.sum;
@@ -903,7 +936,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             double loss = *l.cross + Q * ((logs.ref - ref) * logs.scale + logs.ln_s);
             if (Op::kTail && rest > 0.0)
                 loss += rest * (log(rest) - log(outside) + logs.ln_s);
-            args.row_loss[row] = (double)r.weight * loss;
+            args.join.put(row, (double)r.weight * loss);
             if (args.row_loss_out)
                 args.row_loss_out[row] = (float)loss;
         }
@@ -916,6 +949,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     } else {
         slope = Op::done(args, r, row, st, zy, leader, fix);
     }
+    const unsigned before = t < kWave ? join.arrive() : 0;
 
     if constexpr (GRAD) {
         S* dvec = dr + sp.head;
@@ -948,6 +982,8 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
                 dr[r.y] = T::narrow(slope_at<Op::kEntropy>(ex.at(zy), slope) + fix);
         }
     }
+    if (t < kWave)
+        join.finish(before, rows);
 }
 
 // ---- a gradient whose statistics are there already --------------------------
@@ -1097,9 +1133,10 @@ void launch_rows_as(const Logits& m, const Part& p, const typename Op::Args& arg
     constexpr uint32_t per = GT < 256 ? 256 / GT : 1;
     const S* z = static_cast<const S*>(m.z) + p.row0 * m.ld;
     S* dz = GRAD ? static_cast<S*>(m.dz) + p.row0 * m.ldd : nullptr;
-    hipLaunchKernelGGL((row_kernel<T, GT, NV, MULTI, GRAD, Op>), dim3((p.rows + per - 1) / per),
-                       dim3(GT < 256 ? 256 : GT), lds * per, p.stream, z, dz, p.rows,
-                       (uint32_t)m.V, m.ld, m.ldd, exponent_scale(m.scale), args);
+    hipLaunchKernelGGL((row_kernel<T, GT, NV, MULTI, GRAD, Op>),
+                       dim3((p.rows + per - 1) / per), dim3(GT < 256 ? 256 : GT),
+                       lds * per, p.stream, z, dz, p.rows, (uint32_t)m.V, m.ld,
+                       m.ldd, exponent_scale(m.scale), args);
 }
 
 // The threads and registers of a row by its length.  With a gradient the row
@@ -1108,7 +1145,7 @@ void launch_rows_as(const Logits& m, const Part& p, const typename Op::Args& arg
 template <class T, class Op>
 void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds)
 {
-    const size_t nvec = (m.V + T::W - 1) / T::W;
+    const size_t nvec = m.V / T::W;
     if (!m.dz) {
         if (nvec <= 64 * 8)
             launch_rows_as<T, 64, 8, false, false, Op>(m, p, args, lds);
@@ -1221,12 +1258,12 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Wo
                                hipStream_t stream)
 {
     using namespace rowloss;
-    double* row_loss = static_cast<double*>(ws.partials);
     const size_t lds = TeacherLds::bytes(bitmap_words<T>((uint32_t)a.m.V), a.K);
     const float mean = (float)(1.0 / (double)a.m.rows);
     hipError_t e = hipSuccess;
     const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
         const size_t r = p.row0;
+        const Join join = join_of(ws, ws.partials, p.rows, a.loss, a.accum || r);
         const float* weight = a.weight ? a.weight + r : nullptr;
         float* out = a.row_loss ? a.row_loss + r : nullptr;
         const int64_t* idx = a.idx + r * a.ldk;
@@ -1234,14 +1271,14 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Wo
         if (a.teacher_lse)
             launch_rows_op<T, DistillOp<true>>(a.m, p,
                                                {idx, val, a.teacher_lse + r, weight, (uint32_t)a.K,
-                                                a.ldk, a.m.scale, mean, out, row_loss},
+                                                a.ldk, a.m.scale, mean, out, join},
                                                lds);
         else
             launch_rows_op<T, DistillOp<false>>(a.m, p,
                                                 {idx, val, nullptr, weight, (uint32_t)a.K, a.ldk,
-                                                 a.m.scale, mean, out, row_loss},
+                                                 a.m.scale, mean, out, join},
                                                 lds);
-        const hipError_t s = launch_loss_sum(row_loss, p.rows, a.loss, a.accum || r, stream);
+        const hipError_t s = sum_joined(join, p.rows, stream);
         e = e == hipSuccess ? s : e;
     });
     return f == hipSuccess ? e : f;
@@ -1252,11 +1289,11 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Work
                               hipStream_t stream)
 {
     using namespace rowloss;
-    double* row_loss = static_cast<double*>(ws.partials);
     const float mean = (float)(1.0 / (double)a.m.rows);
     hipError_t e = hipSuccess;
     const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
         const size_t r = p.row0;
+        const Join join = join_of(ws, ws.partials, p.rows, a.loss, a.accum || r);
         auto launch = [&](auto op) {
             typedef decltype(op) Op;
             launch_rows_op<T, Op>(
@@ -1264,14 +1301,14 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Work
                 {a.targets + r, a.old_logp + r, a.ref_logp ? a.ref_logp + r : nullptr,
                  a.advantage + r, a.weight ? a.weight + r : nullptr, 1.0 - (double)a.clip_low,
                  1.0 + (double)a.clip_high, (double)a.kl_coef, (double)a.entropy_coef, a.m.scale,
-                 mean, a.logp + r, a.entropy ? a.entropy + r : nullptr, row_loss},
+                 mean, a.logp + r, a.entropy ? a.entropy + r : nullptr, join},
                 0);
         };
         if (a.entropy || a.entropy_coef != 0.0f)
             launch(PolicyOp<true>{});
         else
             launch(PolicyOp<false>{});
-        const hipError_t s = launch_loss_sum(row_loss, p.rows, a.loss, a.accum || r, stream);
+        const hipError_t s = sum_joined(join, p.rows, stream);
         e = e == hipSuccess ? s : e;
     });
     return f == hipSuccess ? e : f;
@@ -1296,14 +1333,13 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo&, co
             read, p, {a.targets + p.row0, stat + p.row0, logp + p.row0, slope + p.row0}, 0);
     });
     if (e == hipSuccess)
-        e = launch_preference_pairs(a, logp, slope, pair_loss, stream);
+        e = launch_preference_pairs(a, logp, slope, join_of(ws, pair_loss, a.pairs, a.loss, a.accum),
+                                    stream);
     if (e == hipSuccess && a.m.dz)
         e = each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
             const size_t r = p.row0;
             launch_grad<T, PreferenceGradOp>(a.m, p, {a.targets + r, stat + r, slope + r});
         });
-    if (e == hipSuccess)
-        e = launch_loss_sum(pair_loss, a.pairs, a.loss, a.accum, stream);
     return e;
 }
 
