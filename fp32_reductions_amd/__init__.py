@@ -34,7 +34,6 @@ tensors alive and unchanged in shape while the plan is in use.
 from __future__ import annotations
 
 import ctypes
-import inspect
 import os
 
 import torch
@@ -384,200 +383,17 @@ def colprod_u32(src, out, C=None, stream=None):
 # losses over rows of logits
 # ---------------------------------------------------------------------------
 
-_LOGITS_DTYPE = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
-PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+# These calls take many tensors, and small ones take no longer on the GPU than
+# their checks would in Python: the functions are those of the extension
+# module built from csrc/rowloss_binding.cpp.
 
+if not os.path.exists(os.path.join(_PKG, "_rowloss.so")):
+    raise ImportError("_rowloss.so is not built beside libreduce.so; run "
+                      "'python fp32_reductions_amd/build.py'")
 
-def _matrix(t, dtype, what: str):
-    """(pointer, rows, columns, row stride) of a 2-D device tensor whose rows
-    are contiguous; the row stride may exceed the columns."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % what)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device (cuda/HIP) tensor" % what)
-    if t.dim() != 2:
-        raise ValueError("%s must be 2-D" % what)
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError("the rows of %s must be contiguous" % what)
-    if rows <= 1:
-        ld = cols
-    elif ld < cols:
-        raise ValueError("the rows of %s must not overlap" % what)
-    return t.data_ptr(), rows, cols, ld
+from . import _rowloss  # noqa: E402
 
-
-def _vector(t, dtype, n: int, what: str, optional: bool = False):
-    """Pointer of a contiguous device tensor of exactly n elements (None: 0)."""
-    if t is None and optional:
-        return None
-    _need(t, dtype, what)
-    if t.numel() != n:
-        raise ValueError("%s must have %d element(s), has %d" % (what, n, t.numel()))
-    return t.data_ptr()
-
-
-def _gradient(dlogits, dtype, rows: int, cols: int, optional: bool = True):
-    if dlogits is None and optional:
-        return None, 0
-    ptr, r, c, ldd = _matrix(dlogits, dtype, "dlogits")
-    if (r, c) != (rows, cols):
-        raise ValueError("dlogits must have the shape of logits")
-    return ptr, ldd
-
-
-def _same_device(logits, *others) -> None:
-    for t in others:
-        if t is not None and t.device != logits.device:
-            raise ValueError("all tensors must be on the device of logits")
-
-
-def _args_token_logprob(name, logits, targets, logp, lse, entropy=None, scale=1.0, stream=None):
-    """logp[r] = ln p_target, lse[r] = ln sum exp(scale * logits[r]) and, where
-    given, entropy[r] of each row's softmax p at inverse temperature `scale`.
-
-    logits (rows, V) with contiguous rows of any stride; targets int64 (a
-    target outside [0, V) gives logp 0); logp, lse, entropy fp32."""
-    dtype = _LOGITS_DTYPE[name.rsplit("_", 1)[1]]
-    z, rows, V, ld = _matrix(logits, dtype, "logits")
-    f32 = torch.float32
-    _same_device(logits, targets, logp, lse, entropy)
-    return (z, rows, V, ld, _vector(targets, torch.int64, rows, "targets"), float(scale),
-            _vector(logp, f32, rows, "logp"), _vector(lse, f32, rows, "lse"),
-            _vector(entropy, f32, rows, "entropy", True),
-            _stream(stream)), (logits, targets, logp, lse, entropy)
-
-
-def _args_token_logprob_grad(name, logits, targets, lse, glogp, dlogits, entropy=None,
-                             gentropy=None, scale=1.0, stream=None):
-    """dlogits from the gradients glogp (of logp) and gentropy (of entropy) of
-    token_logprob, whose lse and entropy the caller kept.  dlogits may be
-    logits itself."""
-    dtype = _LOGITS_DTYPE[name.rsplit("_", 1)[1]]
-    z, rows, V, ld = _matrix(logits, dtype, "logits")
-    f32 = torch.float32
-    dz, ldd = _gradient(dlogits, dtype, rows, V, False)
-    if gentropy is not None and entropy is None:
-        raise ValueError("gentropy needs entropy")
-    _same_device(logits, targets, lse, glogp, dlogits, entropy, gentropy)
-    return (z, rows, V, ld, _vector(targets, torch.int64, rows, "targets"), float(scale),
-            _vector(lse, f32, rows, "lse"), _vector(entropy, f32, rows, "entropy", True),
-            _vector(glogp, f32, rows, "glogp"), _vector(gentropy, f32, rows, "gentropy", True),
-            dz, ldd, _stream(stream)), (logits, targets, lse, glogp, dlogits, entropy, gentropy)
-
-
-def _args_distill_topk(name, logits, idx, val, loss, dlogits=None, teacher_lse=None, weight=None,
-                       row_loss=None, scale=1.0, accum=False, stream=None):
-    """loss[0] = [loss[0] +] sum_r weight[r] KL(teacher || softmax(scale *
-    logits[r])) for a teacher given by K columns idx (rows, K) int64 and
-    their logits val (rows, K) fp32; columns outside [0, V) are padding.
-    Without teacher_lse the teacher is the softmax of its entries; with the
-    log-sum-exp of its whole scaled row, the columns not listed count as one
-    more.  weight: 1 / rows each when None; 0 leaves a row out.  dlogits
-    takes the gradient (it may be logits itself), row_loss the rows' losses."""
-    dtype = _LOGITS_DTYPE[name.rsplit("_", 1)[1]]
-    z, rows, V, ld = _matrix(logits, dtype, "logits")
-    f32 = torch.float32
-    i, irows, K, ldk = _matrix(idx, torch.int64, "idx")
-    v, vrows, vk, ldv = _matrix(val, f32, "val")
-    if irows != rows or vrows != rows or vk != K:
-        raise ValueError("idx and val must both be (rows, K)")
-    if ldk != ldv:
-        raise ValueError("idx and val must have the same row stride")
-    dz, ldd = _gradient(dlogits, dtype, rows, V)
-    _same_device(logits, idx, val, loss, dlogits, teacher_lse, weight, row_loss)
-    return (z, rows, V, ld, i, v, K, ldk, _vector(teacher_lse, f32, rows, "teacher_lse", True),
-            _vector(weight, f32, rows, "weight", True), float(scale),
-            _vector(loss, f32, 1, "loss"), int(bool(accum)),
-            _vector(row_loss, f32, rows, "row_loss", True), dz, ldd,
-            _stream(stream)), (logits, idx, val, loss, dlogits, teacher_lse, weight, row_loss)
-
-
-def _args_policy_loss(name, logits, targets, old_logp, advantage, loss, logp, dlogits=None,
-                      ref_logp=None, weight=None, entropy=None, scale=1.0, clip_low=0.2,
-                      clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, accum=False, stream=None):
-    """loss[0] = [loss[0] +] sum_r weight[r] (-min(ratio A, clip(ratio) A) +
-    kl_coef (exp(d) - d - 1) - entropy_coef H) with ratio = exp(logp[r] -
-    old_logp[r]) clipped to [1 - clip_low, 1 + clip_high], A = advantage[r],
-    d = ref_logp[r] - logp[r] and H the entropy of softmax(scale *
-    logits[r]).  logp and entropy take the rows' values, dlogits the gradient
-    (it may be logits itself).  weight: 1 / rows each when None; rows of
-    weight 0, or without a target in [0, V), do not count."""
-    dtype = _LOGITS_DTYPE[name.rsplit("_", 1)[1]]
-    z, rows, V, ld = _matrix(logits, dtype, "logits")
-    f32 = torch.float32
-    dz, ldd = _gradient(dlogits, dtype, rows, V)
-    if kl_coef and ref_logp is None:
-        raise ValueError("kl_coef needs ref_logp")
-    _same_device(logits, targets, old_logp, advantage, loss, logp, dlogits, ref_logp, weight,
-                 entropy)
-    return (z, rows, V, ld, _vector(targets, torch.int64, rows, "targets"),
-            _vector(old_logp, f32, rows, "old_logp"),
-            _vector(ref_logp, f32, rows, "ref_logp", True),
-            _vector(advantage, f32, rows, "advantage"),
-            _vector(weight, f32, rows, "weight", True), float(scale), float(clip_low),
-            float(clip_high), float(kl_coef), float(entropy_coef),
-            _vector(loss, f32, 1, "loss"), int(bool(accum)), _vector(logp, f32, rows, "logp"),
-            _vector(entropy, f32, rows, "entropy", True), dz, ldd,
-            _stream(stream)), (logits, targets, old_logp, advantage, loss, logp, dlogits,
-                               ref_logp, weight, entropy)
-
-
-def _args_preference_loss(name, logits, targets, starts, loss, seq_logp, dlogits=None,
-                          ref_logp=None, weight=None, kind="sigmoid", beta=0.1, margin=0.0,
-                          smoothing=0.0, average=False, accum=False, stream=None):
-    """loss[0] = [loss[0] +] sum_p weight[p] l(beta D_p - margin), D_p the
-    log-ratio of pair p's chosen sequence (number p) over its rejected one
-    (number pairs + p), each against ref_logp; l is "sigmoid" (with label
-    smoothing), "hinge" or "squared".  Sequence i has the rows starts[i] to
-    starts[i + 1] (int64, 2 * pairs + 1 of them); seq_logp (2 * pairs) takes
-    the sums (average: means) of their targets' log-probabilities, dlogits the
-    gradient (it may be logits itself).  weight: 1 / pairs each when None."""
-    dtype = _LOGITS_DTYPE[name.rsplit("_", 1)[1]]
-    z, rows, V, ld = _matrix(logits, dtype, "logits")
-    f32 = torch.float32
-    _need(starts, torch.int64, "starts")
-    if starts.numel() % 2 == 0:
-        raise ValueError("starts must have 2 * pairs + 1 elements")
-    pairs = starts.numel() // 2
-    if kind not in PREFERENCE_KINDS:
-        raise ValueError("kind must be one of %s" % ", ".join(sorted(PREFERENCE_KINDS)))
-    dz, ldd = _gradient(dlogits, dtype, rows, V)
-    _same_device(logits, targets, starts, loss, seq_logp, dlogits, ref_logp, weight)
-    return (z, rows, V, ld, _vector(targets, torch.int64, rows, "targets"), starts.data_ptr(),
-            pairs, _vector(ref_logp, f32, 2 * pairs, "ref_logp", True),
-            _vector(weight, f32, pairs, "weight", True), PREFERENCE_KINDS[kind], float(beta),
-            float(margin), float(smoothing), int(bool(average)), _vector(loss, f32, 1, "loss"),
-            int(bool(accum)), _vector(seq_logp, f32, 2 * pairs, "seq_logp"), dz, ldd,
-            _stream(stream)), (logits, targets, starts, loss, seq_logp, dlogits, ref_logp, weight)
-
-
-_ROWLOSS = {"token_logprob": _args_token_logprob, "token_logprob_grad": _args_token_logprob_grad,
-            "distill_topk": _args_distill_topk, "policy_loss": _args_policy_loss,
-            "preference_loss": _args_preference_loss}
-
-
-def _typed(cname: str, marshal):
-    """The public function of one C entry point: marshal, call, check."""
-    fn = getattr(_lib, cname)
-
-    def call(*args, **kwargs):
-        cargs, _ = marshal(cname, *args, **kwargs)
-        _check(fn(*cargs), cname)
-
-    sig = inspect.signature(marshal)
-    call.__signature__ = sig.replace(parameters=list(sig.parameters.values())[1:])
-    call.__name__ = call.__qualname__ = cname[len("red_"):]
-    call.__doc__ = marshal.__doc__
-    return call
-
-
-for _name, _marshal in _ROWLOSS.items():
-    for _t in _LOGITS_DTYPE:
-        globals()["%s_%s" % (_name, _t)] = _typed("red_%s_%s" % (_name, _t), _marshal)
+globals().update(_rowloss.CALLS)
 
 
 # ---------------------------------------------------------------------------
@@ -594,14 +410,14 @@ _MARSHAL["sum_max_min_f32"] = ("red_sum_max_min_f32", _args_reduce1d)
 _MARSHAL["sum_max_min_f32_noalloc"] = ("red_sum_max_min_f32_noalloc", _args_reduce1d)
 for _t in ("f32", "f16", "bf16", "i32", "i16", "u16", "u32"):
     _MARSHAL["colprod_" + _t] = ("red_colprod_" + _t, _args_colprod)
-for _name, _marshal in _ROWLOSS.items():
-    for _t in _LOGITS_DTYPE:
-        _MARSHAL["%s_%s" % (_name, _t)] = ("red_%s_%s" % (_name, _t), _marshal)
 
 
 def plan(name: str, *args, **kwargs) -> Plan:
     """Marshal the arguments of entry point ``name`` (e.g. "sum_f32") once;
     the returned Plan enqueues the call each time it is called."""
+    if name in _rowloss.MARSHALS:
+        cargs = _rowloss.MARSHALS[name](*args, **kwargs)
+        return Plan("red_" + name, cargs, (args, kwargs))
     cname, marshal = _MARSHAL[name]
     cargs, keep = marshal(cname, *args, **kwargs)
     return Plan(cname, cargs, keep)

@@ -703,3 +703,63 @@ def test_gradients_against_differences(red, V):
         up, down = loss(z + step * direction), loss(z - step * direction)
         size = max(1.0, abs(value))
         assert abs((up - down) / (2 * step) - slope) <= step ** 2 * rows * 4 + 8 * ref.U * size / step
+
+
+# --- what the Python functions refuse -------------------------------------------------------
+
+def test_refused_tensors(red):
+    """Shapes, types, strides and devices, with everything else right; the
+    calls raise before a kernel runs."""
+    s = all_state(4, 100, 1)
+    z, y, lp, lse = s["z"], s["y"], s["logp"], s["lse"]
+    call = red.token_logprob_bf16
+    wide = torch.zeros(4, 200, device="cuda", dtype=torch.bfloat16)
+    for bad, why in [
+        ((z.float(), y, lp, lse), TypeError), ((z[0], y, lp, lse), ValueError),
+        ((wide[:, ::2], y, lp, lse), ValueError), ((z, y[:3], lp, lse), ValueError),
+        ((z, y.int(), lp, lse), TypeError), ((z, y.cpu(), lp, lse), ValueError),
+        ((z, y, lp.double(), lse), TypeError), ((z, y, wide[:, 0].float()[::2], lse), ValueError),
+        ((z, y, lp, None), TypeError), ((z[:1].expand(4, 100), y, lp, lse), ValueError),
+    ]:
+        with pytest.raises(why):
+            call(*bad)
+    for kw, why in [(dict(scale=0.0), red.ReduceError), (dict(scale="1"), TypeError),
+                    (dict(entropy=lp[:2]), ValueError), (dict(stream="s"), ValueError)]:
+        with pytest.raises(why):
+            call(z, y, lp, lse, **kw)
+    with pytest.raises(ValueError):  # the gradient's shape
+        red.token_logprob_grad_bf16(z, y, lse, lp, wide)
+    with pytest.raises(ValueError):  # an entropy gradient without the entropy
+        red.token_logprob_grad_bf16(z, y, lse, lp, s["d0"], gentropy=lp)
+    with pytest.raises(ValueError):
+        red.distill_topk_bf16(z, s["idx"][:, :5], s["val"], s["l1"])
+    with pytest.raises(ValueError):  # two row strides
+        red.distill_topk_bf16(z, s["idx"][:, :5], s["val"][:, :5].contiguous(), s["l1"])
+    with pytest.raises(ValueError):
+        red.policy_loss_bf16(z, y, lp, lp, s["l2"], s["lp2"], kl_coef=0.1)
+    with pytest.raises(ValueError):
+        red.preference_loss_bf16(z, y, s["starts"][:4], s["l3"], s["seq"])
+    with pytest.raises(ValueError):
+        red.preference_loss_bf16(z, y, s["starts"], s["l3"], s["seq"], kind="other")
+    with pytest.raises(red.ReduceError):
+        red.preference_loss_bf16(z, y, s["starts"], s["l3"], s["seq"], beta=0.0)
+    torch.cuda.synchronize()
+
+
+def test_streams_by_handle_and_object(red):
+    s = all_state(5, 700, 2)
+    side = torch.cuda.Stream()
+    want, got = f32(5), f32(5)
+    red.token_logprob_bf16(s["z"], s["y"], want, s["lse"])
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        got.zero_()
+        torch.cuda.synchronize()
+        red.token_logprob_bf16(s["z"], s["y"], got, s["lse"], stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want)
+    plan = red.plan("token_logprob_bf16", s["z"], s["y"], got.zero_(), s["lse"], stream=side)
+    torch.cuda.synchronize()
+    plan()
+    side.synchronize()
+    assert torch.equal(got, want)

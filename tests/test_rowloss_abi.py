@@ -132,3 +132,29 @@ def test_python_checks(red):
             f = getattr(red, "%s_%s" % (name, t))
             assert f.__doc__ and f.__name__ == "%s_%s" % (name, t)
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+@pytest.mark.parametrize("name,t", PAIRS)
+def test_python_arguments(red, name, t):
+    """Names, order and defaults of the Python functions, and what a call with
+    the wrong ones raises before any tensor is looked at."""
+    import inspect
+
+    f = getattr(red, "%s_%s" % (name, t))
+    names = list(inspect.signature(f).parameters)
+    assert names[0] == "logits" and names[-1] == "stream"
+    need = [k for k, p in inspect.signature(f).parameters.items()
+            if p.default is inspect.Parameter.empty]
+    assert names[:len(need)] == need
+    with pytest.raises(TypeError, match="missing"):
+        f(*[None] * (len(need) - 1))
+    with pytest.raises(TypeError, match="unexpected"):
+        f(*[None] * len(need), nothing=1)
+    with pytest.raises(TypeError, match="multiple"):
+        f(*[None] * len(need), logits=None)
+    with pytest.raises(TypeError, match="at most"):
+        f(*[None] * (len(names) + 1))
+    with pytest.raises(TypeError, match="logits must be a torch.Tensor"):
+        f(*[None] * len(need))
+    with pytest.raises(TypeError, match="logits must be"):
+        red.plan("%s_%s" % (name, t), *[None] * len(need))
