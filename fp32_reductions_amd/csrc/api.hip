@@ -30,8 +30,8 @@ using red::Workspace;
 // Fixed workspace per (device, stream) for partial results.  The kernels
 // size their grids so that they never need more than this.
 constexpr size_t kPartialBytes = size_t(16) << 20;
-// The workspace's counter lies behind the partials, on cache lines of its own.
-constexpr size_t kCounterBytes = 256;
+// The workspace's counts lie behind the partials.
+constexpr size_t kCounterBytes = red::kCounterWords * sizeof(unsigned);
 
 // One workspace and the lock a call holds while it enqueues the kernels
 // that use it: the first pass writes the partials and the second reads
@@ -151,10 +151,10 @@ int find_slot(int dev, hipStream_t stream, std::shared_ptr<Slot>* out)
     auto slot = std::make_shared<Slot>();
     slot->ws.partials = base;
     slot->ws.partial_bytes = kPartialBytes;
-    slot->ws.counter = reinterpret_cast<unsigned*>(static_cast<char*>(base) + kPartialBytes);
+    slot->ws.counters = reinterpret_cast<unsigned*>(static_cast<char*>(base) + kPartialBytes);
     // Before the workspace's first use, on the stream that uses it.
     (void)hipGetLastError();
-    if (red::launch_fill_u32(slot->ws.counter, kCounterBytes / 4, 0, stream) != hipSuccess) {
+    if (red::launch_fill_u32(slot->ws.counters, red::kCounterWords, 0, stream) != hipSuccess) {
         (void)hipFree(base);
         return RED_ERR_HIP;
     }
@@ -497,9 +497,14 @@ int token_logprob(LogitType t, const Logits& m, const int64_t* targets, float* l
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != RED_OK)
         return st;
+    Workspace ws;
+    HeldWorkspace held;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (red::token_logprob_shares(t, m) && (st = stream_workspace(dev, s, &ws, &held)) != RED_OK)
+        return st;
     clear_stale_error();
-    return hip_status(red::launch_token_logprob(t, {m, targets, logp, lse, entropy}, info,
-                                                static_cast<hipStream_t>(stream)));
+    return hip_status(
+        red::launch_token_logprob(t, {m, targets, logp, lse, entropy}, info, ws, s));
 }
 
 int token_logprob_grad(LogitType t, const Logits& m, const int64_t* targets, const float* lse,

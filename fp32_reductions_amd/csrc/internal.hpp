@@ -16,10 +16,12 @@ enum class OpKind { Sum, Max, Min };
 struct Workspace {
     void* partials = nullptr;
     size_t partial_bytes = 0;
-    // A count of arrivals, zero between launches (null in scratch that has
-    // none).  A launch that counts leaves it at zero again.
-    unsigned* counter = nullptr;
+    // kCounterWords counts of arrivals, zero between launches (null in scratch
+    // that has none).  A launch that counts leaves them at zero again.
+    unsigned* counters = nullptr;
 };
+
+constexpr size_t kCounterWords = size_t(1) << 15;
 
 // Launch geometry chosen by the host from the device.
 struct DeviceInfo {

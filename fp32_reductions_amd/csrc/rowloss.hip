@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
         a.seq_logp[(uint64_t)a.pairs + p] = (float)seq[1].logp;
         a.join.put(p, w != 0.0 ? w * loss : 0.0);
     }
-    const unsigned before = threadIdx.x < kWave ? a.join.arrive() : 0;
+    const unsigned before = threadIdx.x < kWave ? a.join.arrive(p) : 0;
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const float mine = (float)((side ? -g : g) / seq[side].count);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
             a.row_slope[r] = mine;
     }
     if (threadIdx.x < kWave)
-        a.join.finish(before, a.pairs);
+        a.join.finish(before, p, a.pairs);
 }
 
 } // namespace
@@ -158,10 +158,11 @@ hipError_t launch_preference_pairs(const PreferenceCall& a, const double* row_lo
     default: return RowLoss<ElemBF16>::call;        \
     }
 
+bool token_logprob_shares(LogitType t, const Logits& m) { RED_BY_TYPE(t, logprob_shares(m)) }
 hipError_t launch_token_logprob(LogitType t, const LogprobCall& a, const DeviceInfo& dev,
-                                hipStream_t stream)
+                                const Workspace& ws, hipStream_t stream)
 {
-    RED_BY_TYPE(t, logprob(a, dev, stream))
+    RED_BY_TYPE(t, logprob(a, dev, ws, stream))
 }
 hipError_t launch_token_logprob_grad(LogitType t, const LogprobGradCall& a,
                                      const DeviceInfo& dev, hipStream_t stream)

@@ -79,8 +79,10 @@ struct PreferenceCall {
     int accum;
 };
 
+// Whether the call keeps something in the workspace.
+bool token_logprob_shares(LogitType t, const Logits& m);
 hipError_t launch_token_logprob(LogitType t, const LogprobCall& a, const DeviceInfo& dev,
-                                hipStream_t stream);
+                                const Workspace& ws, hipStream_t stream);
 hipError_t launch_token_logprob_grad(LogitType t, const LogprobGradCall& a,
                                      const DeviceInfo& dev, hipStream_t stream);
 hipError_t launch_distill_topk(LogitType t, const DistillCall& a, const DeviceInfo& dev,
@@ -93,7 +95,9 @@ hipError_t launch_preference_loss(LogitType t, const PreferenceCall& a, const De
 // The kernels of one element type (T: a trait of rowloss_kernels.hpp).
 template <class T>
 struct RowLoss {
-    static hipError_t logprob(const LogprobCall& a, const DeviceInfo& dev, hipStream_t stream);
+    static bool logprob_shares(const Logits& m);
+    static hipError_t logprob(const LogprobCall& a, const DeviceInfo& dev, const Workspace& ws,
+                              hipStream_t stream);
     static hipError_t logprob_grad(const LogprobGradCall& a, const DeviceInfo& dev,
                                    hipStream_t stream);
     static hipError_t distill(const DistillCall& a, const DeviceInfo& dev, const Workspace& ws,

@@ -10,78 +10,134 @@
 namespace red {
 
 // Each row's loss goes to the workspace, and the wave whose row is the last
-// to arrive adds them up, in the order of the rows.  A second kernel for the
-// sum took 3.2 us more of host time a call and 1.4 us and a gap on the GPU
-// (96 rows of 32768 bf16: 15.6 us a call against 10.6).  A row's loss is stored, has arrived where every compute die sees it
-// (a device-scope store, waited for), and only then is the row counted, so
-// the last one finds all.  A release fence would do as well, but would write
-// back the whole L2 with the gradient in it.  The last wave sets the count
-// back to zero for the next launch on the stream.  Past kJoinRows rows, whose
-// sum is too much for one wave, `count` is null and a kernel of its own
-// adds them up.
-constexpr uint32_t kJoinRows = 1024;
+// to arrive adds them up, in a fixed order.  A second kernel for the sum took
+// 3.2 us more of host time a call and 1.4 us and a gap on the GPU (96 rows of
+// 32768 bf16: 15.6 us a call against 10.6).  A row's loss is stored, has
+// arrived where every compute die sees it (a device-scope store, waited for),
+// and only then is the row counted, so the last one finds all.  A release
+// fence would do as well, but would write back the whole L2 with the gradient
+// in it.
+//
+// Arrivals at one address follow each other at 12 ns (1024 rows of 1000 bf16:
+// 17.1 us with one count, 4.3 us for one row), so every 64 rows have a count
+// of their own, on its own cache lines; the last of 64 adds up their losses
+// and arrives with the sum at the next level.  The last ones set the counts
+// back to zero for the next launch on the stream.  Past kJoinRows rows
+// `count` is null and a kernel of its own adds up.
+constexpr uint32_t kJoinGroup = kWave, kJoinGroups = 256;
+constexpr uint32_t kJoinRows = kJoinGroup * kJoinGroups;
+constexpr uint32_t kCountStride = 64; // words between counts
+
+// Words that workgroups on different compute dies share within a launch.
+__device__ __forceinline__ void store_shared(double* p, double v)
+{
+    __hip_atomic_store(reinterpret_cast<unsigned long long*>(p),
+                       __builtin_bit_cast(unsigned long long, v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void store_shared(float* p, float v)
+{
+    __hip_atomic_store(reinterpret_cast<unsigned*>(p), __float_as_uint(v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double load_shared(const double* p)
+{
+    return __builtin_bit_cast(
+        double, __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ float load_shared(const float* p)
+{
+    return __uint_as_float(__hip_atomic_load(reinterpret_cast<const unsigned*>(p),
+                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+// One more arrival, after everything this lane has stored; the count before.
+__device__ __forceinline__ unsigned count_shared(unsigned* p)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void clear_shared(unsigned* p)
+{
+    __hip_atomic_store(p, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 struct Join {
     double* row_loss;
-    unsigned* count;
+    double* group_sum;
+    unsigned* count; // [0]: of groups; [1 + g]: of the rows of group g
     float* loss;
     int accum;
-    __device__ __forceinline__ void put(size_t row, double v) const
-    {
-        __hip_atomic_store(reinterpret_cast<unsigned long long*>(row_loss + row),
-                           __builtin_bit_cast(unsigned long long, v), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-    }
+    __device__ __forceinline__ void put(size_t row, double v) const { store_shared(row_loss + row, v); }
     // By every lane of the wave whose lane 0 has put the row's loss.
-    __device__ __forceinline__ unsigned arrive() const
+    __device__ __forceinline__ unsigned arrive(uint32_t row) const
     {
-        unsigned before = 0;
-        if (count && (threadIdx.x & 63) == 0) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        return before;
+        return count ? arrive_at(count + (1 + row / kJoinGroup) * kCountStride) : 0;
     }
     // By the same wave with what arrive() gave lane 0.
-    __device__ __forceinline__ void finish(unsigned before, uint32_t rows) const
+    __device__ __forceinline__ void finish(unsigned before, uint32_t row, uint32_t rows) const
     {
-        if (!count || __builtin_amdgcn_readfirstlane(before) != rows - 1)
+        if (!count)
             return;
-        const uint32_t lane = threadIdx.x & 63;
-        const float old = accum ? loss[0] : 0.0f;
-        double sum = 0.0;
-        for (uint32_t i = lane; i < rows; i += 8 * kWave) {
-            unsigned long long v[8];
+        const uint32_t lane = threadIdx.x & 63, g = row / kJoinGroup;
+        const uint32_t first = g * kJoinGroup;
+        const uint32_t size = rows - first < kJoinGroup ? rows - first : kJoinGroup;
+        if (__builtin_amdgcn_readfirstlane(before) != size - 1)
+            return;
+        double sum = total(lane < size ? load_shared(row_loss + first + lane) : 0.0);
+        if (lane == 0)
+            clear_shared(count + (1 + g) * kCountStride);
+        const uint32_t groups = (rows + kJoinGroup - 1) / kJoinGroup;
+        if (groups > 1) {
+            if (lane == 0)
+                store_shared(group_sum + g, sum);
+            before = arrive_at(count);
+            if (__builtin_amdgcn_readfirstlane(before) != groups - 1)
+                return;
+            double v[kJoinGroups / kWave];
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k)
-                v[k] = i + k * kWave < rows
-                           ? __hip_atomic_load(reinterpret_cast<unsigned long long*>(row_loss) + i +
-                                                   k * kWave,
-                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                           : 0ull;
+            for (uint32_t k = 0; k < kJoinGroups / kWave; ++k)
+                v[k] = lane + k * kWave < groups ? load_shared(group_sum + lane + k * kWave) : 0.0;
+            sum = 0.0;
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k)
-                sum += __builtin_bit_cast(double, v[k]);
+            for (uint32_t k = 0; k < kJoinGroups / kWave; ++k)
+                sum += v[k];
+            sum = total(sum);
+            if (lane == 0)
+                clear_shared(count);
         }
+        if (lane == 0)
+            loss[0] = (float)((accum ? (double)loss[0] : 0.0) + sum);
+    }
+
+  private:
+    static __device__ __forceinline__ unsigned arrive_at(unsigned* p)
+    {
+        return (threadIdx.x & 63) == 0 ? count_shared(p) : 0;
+    }
+    static __device__ __forceinline__ double total(double v)
+    {
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1)
-            sum += __shfl_xor(sum, m);
-        if (lane == 0) {
-            loss[0] = (float)((double)old + sum);
-            __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
+            v += __shfl_xor(v, m);
+        return v;
     }
 };
+static_assert((1 + kJoinGroups) * kCountStride <= kCounterWords, "a count for each group");
 
 // For operators without a loss to join.
 struct NoJoin {
-    __device__ __forceinline__ unsigned arrive() const { return 0; }
-    __device__ __forceinline__ void finish(unsigned, uint32_t) const {}
+    __device__ __forceinline__ unsigned arrive(uint32_t) const { return 0; }
+    __device__ __forceinline__ void finish(unsigned, uint32_t, uint32_t) const {}
 };
 
 // The meeting place of `rows` losses at `row_loss` (in the workspace).
 inline Join join_of(const Workspace& ws, void* row_loss, size_t rows, float* loss, int accum)
 {
-    return {static_cast<double*>(row_loss), rows <= kJoinRows ? ws.counter : nullptr, loss, accum};
+    return {static_cast<double*>(row_loss),
+            reinterpret_cast<double*>(static_cast<char*>(ws.partials) + ws.partial_bytes) -
+                kJoinGroups,
+            rows <= kJoinRows ? ws.counters : nullptr, loss, accum};
 }
 
 // After the launch that puts them: the sum, where no wave of it adds them up.

@@ -376,20 +376,18 @@ __device__ __forceinline__ Stat combine(Stat st, float c, float* lds)
                 lds[2 * kParts + w] = st.u;
         }
         __syncthreads();
-        float m = lds[0];
-#pragma unroll
-        for (int k = 1; k < kParts; ++k)
-            m = fmaxf(m, lds[k]);
-        Stat all = {m, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-            Stat part = {lds[k], lds[kParts + k], ENT ? lds[2 * kParts + k] : 0.0f};
-            move_to<ENT>(part, m, c);
-            all.s += part.s;
+        const uint32_t lane = threadIdx.x & 63;
+        st = {-INFINITY, 0.0f, 0.0f};
+        if (lane < kParts) {
+            st.m = lds[lane];
+            st.s = lds[kParts + lane];
             if constexpr (ENT)
-                all.u += part.u;
+                st.u = lds[2 * kParts + lane];
         }
-        st = all;
+        move_to<ENT>(st, wave_reduce<OpMax>(st.m), c);
+        st.s = wave_reduce<OpSum>(st.s);
+        if constexpr (ENT)
+            st.u = wave_reduce<OpSum>(st.u);
     }
     return st;
 }
@@ -488,6 +486,13 @@ struct RowLogs {
     {
         return ln_s - kLn2 * ((double)st.u / (double)st.s);
     }
+};
+
+// What a row's gradient takes from its statistics, where another kernel
+// writes it: dz_v = 2^((z_v - ref) c) (a + b (z_v - ref) c), and fix more in the
+// target's column.  All zero for a row that does not count.
+struct RowSlope {
+    float ref, a, b, fix;
 };
 
 // Log-probability of the target, log-sum-exp and entropy.
@@ -858,11 +863,11 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const auto join = Op::join(args);
     auto dead_row = [&]() __attribute__((always_inline)) {
         Op::dead(args, row, leader);
-        const unsigned before = t < kWave ? join.arrive() : 0;
+        const unsigned before = t < kWave ? join.arrive(row) : 0;
         if constexpr (GRAD)
             write_zeros<T, GT>(dr, sp, t);
         if (t < kWave)
-            join.finish(before, rows);
+            join.finish(before, row, rows);
     };
     if (!r.live) {
         dead_row();
@@ -949,7 +954,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     } else {
         slope = Op::done(args, r, row, st, zy, leader, fix);
     }
-    const unsigned before = t < kWave ? join.arrive() : 0;
+    const unsigned before = t < kWave ? join.arrive(row) : 0;
 
     if constexpr (GRAD) {
         S* dvec = dr + sp.head;
@@ -983,7 +988,95 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         }
     }
     if (t < kWave)
-        join.finish(before, rows);
+        join.finish(before, row, rows);
+}
+
+// ---- few long rows ------------------------------------------------------------
+//
+// One workgroup for a row leaves most of the device idle when rows are few and
+// long, so a row is cut into segments of a workgroup each.  A segment's
+// statistics go to the workspace, and the workgroup that comes last in its row
+// joins them, in the order of the segments, and finishes the row.  (The same
+// protocol as for the losses' sum; the counts of the rows follow its counts.)
+// A gradient is written by a second kernel, grad_kernel, from the row's slope.
+constexpr uint32_t kSplitRows = 128, kSegmentsMost = kWave;
+constexpr uint32_t kSegmentVecs = 1024; // 16 KiB: four vectors for each thread
+constexpr uint32_t kRowCounts = (1 + kJoinGroups) * kCountStride;
+static_assert(kRowCounts + kSplitRows * kCountStride <= kCounterWords, "a count for each row");
+
+struct Split {
+    float* part;      // [row][3][kSegmentsMost]: maximum, sum, entropy sum
+    RowSlope* slope;  // [row]; null: no gradient
+    unsigned* counts; // [row * kCountStride]
+};
+
+template <class T, int NV, class Op>
+__global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint32_t rows,
+                                                    uint32_t V, uint32_t segs, uint32_t per,
+                                                    size_t ld, float c, Split split,
+                                                    typename Op::Args args)
+{
+    typedef typename T::S S;
+    constexpr int GT = 256;
+    __shared__ float parts[3 * (GT / kWave)];
+    const uint32_t t = threadIdx.x, row = blockIdx.x / segs, seg = blockIdx.x % segs;
+    const S* zr = z + (size_t)row * ld;
+    const Span sp = Span::of<T>(zr, V);
+    const typename Op::Row r = Op::begin(args, row, V);
+    const auto join = Op::join(args);
+    if (!r.live) {
+        if (seg == 0 && t < kWave) {
+            Op::dead(args, row, t == 0);
+            if (split.slope && t == 0)
+                split.slope[row] = {0.0f, 0.0f, 0.0f, 0.0f};
+            join.finish(join.arrive(row), row, rows);
+        }
+        return;
+    }
+    const u32x4_t* vec = reinterpret_cast<const u32x4_t*>(zr + sp.head);
+    const uint32_t first = seg * per;
+    const uint32_t last = first + per < sp.nvec ? first + per : sp.nvec;
+    u32x4_t v[NV];
+    load_chunk<T, GT, NV, false>(vec, first, last, t, v);
+    const bool has_one = seg == 0 && t < sp.singles;
+    const float one = has_one ? T::widen(zr[sp.single(t)]) : -INFINITY;
+    const float zy = T::widen(zr[r.y]);
+    Stat st = {-INFINITY, 0.0f, 0.0f};
+    fold_chunk<T, GT, NV, Op::kEntropy>(v, first, last, t, one, false, c, TakeAll{}, st);
+    for (uint32_t next = first + GT * NV; next < last; next += GT * NV) {
+        load_chunk<T, GT, NV, false>(vec, next, last, t, v);
+        fold_chunk<T, GT, NV, Op::kEntropy>(v, next, last, t, -INFINITY, true, c, TakeAll{}, st);
+    }
+    st = combine<GT, Op::kEntropy>(st, c, parts);
+    if (t >= kWave)
+        return;
+    float* mine = split.part + (size_t)row * 3 * kSegmentsMost;
+    unsigned before = 0;
+    if (t == 0) {
+        store_shared(mine + seg, st.m);
+        store_shared(mine + kSegmentsMost + seg, st.s);
+        if constexpr (Op::kEntropy)
+            store_shared(mine + 2 * kSegmentsMost + seg, st.u);
+        before = count_shared(split.counts + row * kCountStride);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) != segs - 1)
+        return;
+    st = {-INFINITY, 0.0f, 0.0f};
+    if (t < segs) {
+        st.m = load_shared(mine + t);
+        st.s = load_shared(mine + kSegmentsMost + t);
+        if constexpr (Op::kEntropy)
+            st.u = load_shared(mine + 2 * kSegmentsMost + t);
+    }
+    st = combine<kWave, Op::kEntropy>(st, c, parts);
+    float fix;
+    const Slope slope = Op::done(args, r, row, st, zy, t == 0, fix);
+    if (t == 0) {
+        clear_shared(split.counts + row * kCountStride);
+        if (split.slope)
+            split.slope[row] = {reference(st.m), slope.a, slope.b, fix};
+    }
+    join.finish(join.arrive(row), row, rows);
 }
 
 // ---- a gradient whose statistics are there already --------------------------
@@ -1058,6 +1151,35 @@ struct PreferenceGradOp {
         r.ref = reference(st.x);
         r.fix = g;
         r.slope = {-g / st.y, 0.0f};
+        return r;
+    }
+};
+
+// The gradient of a row split over several workgroups.
+template <bool ENT>
+struct SplitGradOp {
+    static constexpr bool kEntropy = ENT;
+    struct Args {
+        const int64_t* targets;
+        const RowSlope* slope;
+    };
+    struct Row {
+        bool live, hit;
+        uint32_t y;
+        float ref, fix;
+        Slope slope;
+    };
+    static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V, float)
+    {
+        Row r;
+        const int64_t y = a.targets[row];
+        const RowSlope s = a.slope[row];
+        r.hit = (uint64_t)y < V;
+        r.y = r.hit ? (uint32_t)y : 0u;
+        r.live = s.a != 0.0f || s.b != 0.0f || s.fix != 0.0f;
+        r.ref = s.ref;
+        r.fix = s.fix;
+        r.slope = {s.a, s.b};
         return r;
     }
 };
@@ -1139,11 +1261,57 @@ void launch_rows_as(const Logits& m, const Part& p, const typename Op::Args& arg
                        m.ldd, exponent_scale(m.scale), args);
 }
 
-// The threads and registers of a row by its length.  With a gradient the row
-// stays in registers, in the smallest group that holds it; without, rows
-// pass through a workgroup of 256.
+// Whether the rows of a launch are cut into segments.  us a call, whole rows
+// against segments, bf16:
+//   log-probability, V = 32768: 1 row 4.2 / 3.8, 128 rows 6.0 / 5.4;
+//     131072: 14.2 / 4.1 and 15.7 / 9.6; at 16384 whole rows win (3.5 / 3.7);
+//   policy loss and gradient, V = 65536: 1 row 10.6 / 8.8, 64 rows
+//     11.2 / 10.9, 128 rows 13 / 15; 131072: 16.3 / 8.9, 17.4 / 13.7 and
+//     20 / 20; 262144, which a workgroup cannot hold: 32 / 9.1 and, for 128
+//     rows, 41 / 36.
+template <class T>
+bool split_rows(const Logits& m, size_t rows, bool grad)
+{
+    const size_t nvec = m.V / T::W;
+    if (!grad)
+        return rows <= kSplitRows && nvec >= 4096;
+    return rows <= (nvec > 16384 ? kSplitRows : kSplitRows / 2) && nvec >= 8192;
+}
+
+// The workspace's last mebibyte (before the groups' sums) holds what split
+// rows share.
+inline Split split_of(const Workspace& ws, bool grad)
+{
+    char* base = static_cast<char*>(ws.partials) + ws.partial_bytes - (size_t(1) << 20);
+    float* part = reinterpret_cast<float*>(base);
+    return {part,
+            grad ? reinterpret_cast<RowSlope*>(part + kSplitRows * 3 * kSegmentsMost) : nullptr,
+            ws.counters + kRowCounts};
+}
+
 template <class T, class Op>
-void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds)
+void launch_split(const Logits& m, const Part& p, const typename Op::Args& args, const Split& split)
+{
+    const uint32_t nvec = (uint32_t)(m.V / T::W);
+    uint32_t segs = (nvec + kSegmentVecs - 1) / kSegmentVecs;
+    segs = segs < kSegmentsMost ? segs : kSegmentsMost;
+    const uint32_t per = ((nvec + segs - 1) / segs + 255) / 256 * 256;
+    hipLaunchKernelGGL((split_kernel<T, kSegmentVecs / 256, Op>), dim3(p.rows * segs), dim3(256), 0,
+                       p.stream, static_cast<const typename T::S*>(m.z) + p.row0 * m.ld, p.rows,
+                       (uint32_t)m.V, segs, per, m.ld, exponent_scale(m.scale), split, args);
+}
+
+// The threads and registers of a row by its length.  Without a gradient rows
+// pass through a wave or a workgroup of 256.  With one a row stays in
+// registers: of the smallest group that holds it, so that several rows share a
+// compute unit, or, where there are no more rows than compute units, of 256
+// or 1024 threads, which take their row through faster (policy loss, bf16, us
+// a call for 256 rows and for 1024 rows: V = 4096: 64 threads 8.2 and 9.1, 256
+// threads 7.1 and 9.7; V = 32768: 256 threads 12.4 and 26.5, 1024 threads 10.1
+// and 30.4; V = 65536: 512 threads 16.7 and 50, 1024 threads 15.7 and 59).
+template <class T, class Op>
+void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds,
+                    const DeviceInfo& dev)
 {
     const size_t nvec = m.V / T::W;
     if (!m.dz) {
@@ -1152,16 +1320,23 @@ void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& arg
         else
             launch_rows_as<T, 256, 8, true, false, Op>(m, p, args, lds);
     } else if constexpr (Op::kHasGrad) {
-        if (nvec <= 64 * 8)
+        const bool few = p.rows <= (uint32_t)dev.cus;
+        if (few && nvec > 256 && nvec <= 256 * 4)
+            launch_rows_as<T, 256, 4, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 64 * 8)
             launch_rows_as<T, 64, 8, false, true, Op>(m, p, args, lds);
+        else if (few && nvec <= 1024 * 4)
+            launch_rows_as<T, 1024, 4, false, true, Op>(m, p, args, lds);
         else if (nvec <= 256 * 8)
             launch_rows_as<T, 256, 8, false, true, Op>(m, p, args, lds);
         else if (nvec <= 256 * 16)
             launch_rows_as<T, 256, 16, false, true, Op>(m, p, args, lds);
+        else if (few && nvec <= 1024 * 8)
+            launch_rows_as<T, 1024, 8, false, true, Op>(m, p, args, lds);
         else if (nvec <= 512 * 16)
             launch_rows_as<T, 512, 16, false, true, Op>(m, p, args, lds);
-        else if (nvec <= 512 * 32)
-            launch_rows_as<T, 512, 32, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 1024 * 16)
+            launch_rows_as<T, 1024, 16, false, true, Op>(m, p, args, lds);
         else
             launch_rows_as<T, 512, 32, true, true, Op>(m, p, args, lds);
     }
@@ -1220,17 +1395,31 @@ void launch_grad(const Logits& m, const Part& p, const typename Op::Args& args)
 // ---- the calls of one element type -------------------------------------------
 
 template <class T>
-hipError_t RowLoss<T>::logprob(const LogprobCall& a, const DeviceInfo&, hipStream_t stream)
+bool RowLoss<T>::logprob_shares(const Logits& m)
+{
+    return rowloss::split_rows<T>(m, m.rows, false);
+}
+
+template <class T>
+hipError_t RowLoss<T>::logprob(const LogprobCall& a, const DeviceInfo& dev, const Workspace& ws,
+                               hipStream_t stream)
 {
     using namespace rowloss;
     return each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
         const size_t r = p.row0;
+        auto launch = [&](auto op) {
+            typedef decltype(op) Op;
+            const typename Op::Args args = {a.targets + r, a.logp + r, a.lse + r,
+                                            a.entropy ? a.entropy + r : nullptr, a.m.scale};
+            if (logprob_shares(a.m))
+                launch_split<T, Op>(a.m, p, args, split_of(ws, false));
+            else
+                launch_rows_op<T, Op>(a.m, p, args, 0, dev);
+        };
         if (a.entropy)
-            launch_rows_op<T, LogprobOp<true>>(
-                a.m, p, {a.targets + r, a.logp + r, a.lse + r, a.entropy + r, a.m.scale}, 0);
+            launch(LogprobOp<true>{});
         else
-            launch_rows_op<T, LogprobOp<false>>(
-                a.m, p, {a.targets + r, a.logp + r, a.lse + r, nullptr, a.m.scale}, 0);
+            launch(LogprobOp<false>{});
     });
 }
 
@@ -1254,7 +1443,7 @@ hipError_t RowLoss<T>::logprob_grad(const LogprobGradCall& a, const DeviceInfo&,
 }
 
 template <class T>
-hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Workspace& ws,
+hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo& dev, const Workspace& ws,
                                hipStream_t stream)
 {
     using namespace rowloss;
@@ -1272,12 +1461,12 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Wo
             launch_rows_op<T, DistillOp<true>>(a.m, p,
                                                {idx, val, a.teacher_lse + r, weight, (uint32_t)a.K,
                                                 a.ldk, a.m.scale, mean, out, join},
-                                               lds);
+                                               lds, dev);
         else
             launch_rows_op<T, DistillOp<false>>(a.m, p,
                                                 {idx, val, nullptr, weight, (uint32_t)a.K, a.ldk,
                                                  a.m.scale, mean, out, join},
-                                                lds);
+                                                lds, dev);
         const hipError_t s = sum_joined(join, p.rows, stream);
         e = e == hipSuccess ? s : e;
     });
@@ -1285,7 +1474,7 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo&, const Wo
 }
 
 template <class T>
-hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Workspace& ws,
+hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo& dev, const Workspace& ws,
                               hipStream_t stream)
 {
     using namespace rowloss;
@@ -1296,13 +1485,17 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Work
         const Join join = join_of(ws, ws.partials, p.rows, a.loss, a.accum || r);
         auto launch = [&](auto op) {
             typedef decltype(op) Op;
-            launch_rows_op<T, Op>(
-                a.m, p,
-                {a.targets + r, a.old_logp + r, a.ref_logp ? a.ref_logp + r : nullptr,
-                 a.advantage + r, a.weight ? a.weight + r : nullptr, 1.0 - (double)a.clip_low,
-                 1.0 + (double)a.clip_high, (double)a.kl_coef, (double)a.entropy_coef, a.m.scale,
-                 mean, a.logp + r, a.entropy ? a.entropy + r : nullptr, join},
-                0);
+            const typename Op::Args args = {
+                a.targets + r, a.old_logp + r, a.ref_logp ? a.ref_logp + r : nullptr,
+                a.advantage + r, a.weight ? a.weight + r : nullptr, 1.0 - (double)a.clip_low,
+                1.0 + (double)a.clip_high, (double)a.kl_coef, (double)a.entropy_coef, a.m.scale,
+                mean, a.logp + r, a.entropy ? a.entropy + r : nullptr, join};
+            if (!split_rows<T>(a.m, p.rows, a.m.dz != nullptr))
+                return launch_rows_op<T, Op>(a.m, p, args, 0, dev);
+            const Split split = split_of(ws, a.m.dz != nullptr);
+            launch_split<T, Op>(a.m, p, args, split);
+            if (a.m.dz)
+                launch_grad<T, SplitGradOp<Op::kEntropy>>(a.m, p, {a.targets + r, split.slope});
         };
         if (a.entropy || a.entropy_coef != 0.0f)
             launch(PolicyOp<true>{});
@@ -1315,7 +1508,7 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo&, const Work
 }
 
 template <class T>
-hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo&, const Workspace& ws,
+hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo& dev, const Workspace& ws,
                                   hipStream_t stream)
 {
     using namespace rowloss;
@@ -1324,13 +1517,17 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo&, co
     float2* stat = reinterpret_cast<float2*>(logp + kPrefRowsMax);
     double* pair_loss = reinterpret_cast<double*>(stat + kPrefRowsMax);
     float* slope = reinterpret_cast<float*>(pair_loss + kPrefPairsMax);
-    static_assert(kPrefRowsMax * (8 + 8 + 4) + kPrefPairsMax * 8 <= (size_t(16) << 20),
-                  "the statistics fit the workspace");
+    static_assert(kPrefRowsMax * (8 + 8 + 4) + kPrefPairsMax * 8 <= (size_t(15) << 20),
+                  "the statistics fit the workspace, below what split rows share");
     Logits read = a.m;
     read.dz = nullptr;
     hipError_t e = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
-        launch_rows_op<T, PreferenceOp>(
-            read, p, {a.targets + p.row0, stat + p.row0, logp + p.row0, slope + p.row0}, 0);
+        const PreferenceOp::Args args = {a.targets + p.row0, stat + p.row0, logp + p.row0,
+                                         slope + p.row0};
+        if (split_rows<T>(read, p.rows, false))
+            launch_split<T, PreferenceOp>(read, p, args, split_of(ws, false));
+        else
+            launch_rows_op<T, PreferenceOp>(read, p, args, 0, dev);
     });
     if (e == hipSuccess)
         e = launch_preference_pairs(a, logp, slope, join_of(ws, pair_loss, a.pairs, a.loss, a.accum),
