@@ -173,8 +173,10 @@ struct Span {
 // unaligned 16-byte vectors to global memory.
 typedef unsigned u32x4u_t __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef __attribute__((address_space(1))) const u32x4_t global_vec;
+
 template <bool STREAM>
-__device__ __forceinline__ u32x4_t load_vec(const u32x4_t* p)
+__device__ __forceinline__ u32x4_t load_vec(global_vec* p)
 {
     if constexpr (STREAM)
         return __builtin_nontemporal_load(p);
@@ -189,24 +191,25 @@ __device__ __forceinline__ void store_vec(void* p, const u32x4_t& v)
     __builtin_nontemporal_store(u, reinterpret_cast<u32x4u_t*>(p));
 }
 
-// The vectors j = first + k GT + t (k < NV) of a row; slots past the row's
-// end hold -inf, which adds nothing to any statistic.
+// Loads past a row's end go to a vector of -inf, which adds nothing to any
+// statistic, instead of being skipped.
+template <class T>
+__device__ const u32x4_t kNegInfVec = {T::kNegInf, T::kNegInf, T::kNegInf, T::kNegInf};
+
+// The vectors j = first + k GT + t (k < NV) of a row, in this order and
+// without a branch between them, so that the first can be used while the last
+// is on its way (with a branch around each load the compiler waits for all).
 template <class T, int GT, int NV, bool STREAM>
 __device__ __forceinline__ void load_chunk(const u32x4_t* base, uint32_t first, uint32_t nvec,
                                            uint32_t t, u32x4_t (&v)[NV])
 {
-    if (first + NV * GT <= nvec) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            v[k] = load_vec<STREAM>(base + first + k * GT + t);
-        return;
-    }
+    global_vec* none = (global_vec*)&kNegInfVec<T>;
+    asm volatile("" : "+v"(t)); // no offset is kept from here to the stores
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const uint32_t j = first + k * GT + t;
-        v[k] = u32x4_t{T::kNegInf, T::kNegInf, T::kNegInf, T::kNegInf};
-        if (j < nvec)
-            v[k] = load_vec<STREAM>(base + j);
+        v[k] = load_vec<STREAM>(j < nvec ? (global_vec*)base + j : none);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -274,6 +277,12 @@ __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t firs
             m1 = fmaxf(fmaxf(m1, f[i + 2]), f[i + 3]);
         }
     }
+    unsigned skips[NG];
+    if constexpr (Take::kSome) {
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+            skips[k] = take.skip(first + k * GT + t);
+    }
     const float m = fmaxf(m0, m1);
     const float ref = reference(m), mc = ref * c;
     // What was summed against the old maximum moves to the new one.
@@ -288,11 +297,11 @@ __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t firs
             float f[W];
             T::unpack(v[k], f);
             if constexpr (Take::kSome) {
-                const unsigned skip = take.skip(first + k * GT + t);
-                if (skip) {
+                if (__builtin_amdgcn_ballot_w64(skips[k] != 0)) {
+                    asm volatile(""); // a branch that few waves take, not selects for all
 #pragma unroll
                     for (int i = 0; i < W; ++i)
-                        if ((skip >> i) & 1)
+                        if ((skips[k] >> i) & 1)
                             f[i] = -INFINITY;
                 }
             }
@@ -473,6 +482,16 @@ __device__ __forceinline__ void write_zeros(typename T::S* row, const Span& sp, 
 //     and the slope of its gradient;
 //   fix: what is added to the gradient in the target's column.
 
+// values[row], or `other` without values; a branch around the load would put
+// one memory latency after another before the row's own loads, so then
+// something else that has a value for each row is read.
+__device__ __forceinline__ float value_or(const float* values, float other, const float* something,
+                                          size_t row)
+{
+    const float v = (values ? values : something)[row];
+    return values ? v : other;
+}
+
 // The fp64 part of a row: ln p of a logit, and the entropy.
 struct RowLogs {
     double ln_s, scale, ref;
@@ -596,10 +615,10 @@ struct PolicyOp {
     static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
     {
         const int64_t y = a.targets[row];
-        const float w = a.weight ? a.weight[row] : a.mean;
+        const float w = value_or(a.weight, a.mean, a.old_logp, row);
         const bool hit = (uint64_t)y < V;
         return {hit && w != 0.0f, hit ? (uint32_t)y : 0u, w, a.old_logp[row], a.advantage[row],
-                a.ref_logp ? a.ref_logp[row] : 0.0f};
+                value_or(a.ref_logp, 0.0f, a.old_logp, row)};
     }
     static __device__ __forceinline__ Slope done(const Args& a, const Row& r, size_t row,
                                                  const Stat& st, float zy, bool leader, float& fix)
@@ -674,12 +693,12 @@ struct DistillOp {
     };
     struct Row {
         bool live;
-        float weight;
+        float weight, teacher_lse;
     };
     static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t)
     {
-        const float w = a.weight ? a.weight[row] : a.mean;
-        return {w != 0.0f, w};
+        const float w = value_or(a.weight, a.mean, a.val, row);
+        return {w != 0.0f, w, TAIL ? a.teacher_lse[row] : 0.0f};
     }
     static __device__ __forceinline__ void dead(const Args& a, size_t row, bool leader)
     {
@@ -742,36 +761,81 @@ __device__ __forceinline__ void wave_lds_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// One wave reads the row's list and fills `l`.  fp64: a row's loss is a small
-// difference of these sums.
-template <class T, bool TAIL>
-__device__ __forceinline__ void read_teacher(const typename DistillOp<TAIL>::Args& a, size_t row,
-                                             const typename T::S* z, uint32_t V, uint32_t head,
-                                             uint32_t words, uint32_t lane, const TeacherLds& l)
+// One wave reads the row's list into `l`: columns, their logits, the
+// student's logits in them, and the bitmap.  It does so before its share of
+// the row's own loads, which would otherwise return first, and the other
+// waves fold the row while it weighs the teacher (4096 rows of 131072 bf16,
+// 64 entries and the rest: 428 us with the list read after the row, 413 so).
+struct ListFacts {
+    float val, z; // this lane's largest logits
+    int listed;   // columns that this lane was first to mark
+    bool again;   // this lane found a column marked already
+};
+
+template <class T>
+__device__ __forceinline__ ListFacts gather_list(const int64_t* idx, const float* val, uint32_t K,
+                                                 const typename T::S* z, uint32_t V,
+                                                 uint32_t head, uint32_t words, uint32_t lane,
+                                                 const TeacherLds& l)
 {
-    for (uint32_t i = lane; i < words; i += kWave)
-        l.bits[i] = 0;
-    const int64_t* idx = a.idx + row * a.ldk;
-    const float* val = a.val + row * a.ldk;
-    float top = -INFINITY, ref = -INFINITY;
-    for (uint32_t k = lane; k < a.K; k += kWave) {
-        const int64_t i = idx[k];
-        const float v = val[k];
-        const bool in = (uint64_t)i < V;
-        const float zk = in ? T::widen(z[i]) : -INFINITY;
-        l.col[k] = in ? (int)i : -1;
-        l.q[k] = in ? v : -INFINITY;
-        l.z[k] = zk;
-        top = fmaxf(top, in ? v : -INFINITY);
-        ref = fmaxf(ref, zk);
+    constexpr uint32_t kBatch = 2;
+    ListFacts facts = {-INFINITY, -INFINITY, 0, false};
+    for (uint32_t k0 = 0; k0 < K; k0 += kBatch * kWave) {
+        int64_t at[kBatch];
+        float v[kBatch], zk[kBatch];
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b) {
+            const uint32_t k = k0 + b * kWave + lane;
+            at[b] = k < K ? idx[k] : -1;
+            v[b] = k < K ? val[k] : -INFINITY;
+        }
+        if (k0 == 0)
+            for (uint32_t i = lane; i < words; i += kWave)
+                l.bits[i] = 0;
+        wave_lds_fence();
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b)
+            if ((uint64_t)at[b] < V) {
+                const uint32_t bit_at = (uint32_t)at[b] + T::W - head, bit = 1u << (bit_at & 31);
+                const bool seen = atomicOr(&l.bits[bit_at >> 5], bit) & bit;
+                facts.again |= seen;
+                facts.listed += !seen;
+            }
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b)
+            zk[b] = (uint64_t)at[b] < V ? T::widen(z[at[b]]) : -INFINITY;
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b) {
+            const uint32_t k = k0 + b * kWave + lane;
+            const bool in = (uint64_t)at[b] < V;
+            if (k < K) {
+                l.col[k] = in ? (int)at[b] : -1;
+                l.q[k] = in ? v[b] : -INFINITY;
+                l.z[k] = zk[b];
+            }
+            facts.val = fmaxf(facts.val, in ? v[b] : -INFINITY);
+            facts.z = fmaxf(facts.z, zk[b]);
+        }
     }
+    return facts;
+}
+
+// The same wave turns the list into the teacher's probabilities and the sums
+// of the row's loss.  fp64: a row's loss is a small difference of these sums.
+template <class T, bool TAIL>
+__device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Args& a,
+                                              const typename DistillOp<TAIL>::Row& r,
+                                              const ListFacts& facts, uint32_t lane,
+                                              const TeacherLds& l)
+{
+    float top = facts.val, ref = facts.z;
     top = wave_reduce<OpMax>(top);
     ref = reference(wave_reduce<OpMax>(ref));
     wave_lds_fence();
     const double scale = a.scale;
     double shift;
     if constexpr (TAIL) {
-        shift = a.teacher_lse[row];
+        shift = r.teacher_lse;
     } else {
         double s = 0.0;
         const double most = reference(top);
@@ -780,8 +844,7 @@ __device__ __forceinline__ void read_teacher(const typename DistillOp<TAIL>::Arg
         shift = most * scale + log(wave_sum64(s));
     }
     double sum = 0.0, cross = 0.0;
-    int listed = 0;
-    bool again = false;
+    int listed = facts.listed;
     for (uint32_t k = lane; k < a.K; k += kWave) {
         const double lq = (double)l.q[k] * scale - shift, q = exp(lq);
         const int col = l.col[k];
@@ -791,11 +854,6 @@ __device__ __forceinline__ void read_teacher(const typename DistillOp<TAIL>::Arg
         sum += q;
         if (q != 0.0) // an entry of no probability adds nothing, whatever its logit
             cross += q * (lq - ((double)l.z[k] - (double)ref) * scale);
-        const uint32_t at = (uint32_t)col + T::W - head;
-        const uint32_t bit = 1u << (at & 31);
-        const bool seen = atomicOr(&l.bits[at >> 5], bit) & bit;
-        again |= seen;
-        listed += !seen;
     }
     sum = wave_sum64(sum);
     cross = wave_sum64(cross);
@@ -803,7 +861,7 @@ __device__ __forceinline__ void read_teacher(const typename DistillOp<TAIL>::Arg
     for (int m = 32; m >= 1; m >>= 1)
         listed += __shfl_xor(listed, m);
     wave_lds_fence();
-    if (__any(again)) {
+    if (__any(facts.again)) {
         // A column listed more than once: its first entry takes the sum of
         // the probabilities, the others are marked.
         for (uint32_t k = lane; k < a.K; k += kWave) {
@@ -877,13 +935,26 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     constexpr uint32_t kChunk = GT * NV;
     const uint32_t chunks = MULTI ? (sp.nvec + kChunk - 1) / kChunk : 1;
     const uint32_t words = Op::kList ? bitmap_words<T>(V) : 0;
+    ListFacts facts;
+    if constexpr (Op::kList) {
+        if (t < kWave)
+            facts = gather_list<T>(
+                args.idx + row * args.ldk, args.val + row * args.ldk, args.K, zr, V, sp.head, words, t,
+                TeacherLds(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K));
+    }
+    // Loads return in the order of their issue: the single elements first, or
+    // the fold of the first vectors would wait for the last.
+    const bool has_one = t < sp.singles;
+    const uint32_t at_one = has_one ? sp.single(t) : 0;
+    const S raw_one = zr[at_one];
+    S raw_zy = 0;
+    if constexpr (!Op::kList)
+        raw_zy = zr[r.y];
     u32x4_t v[NV];
     // Every load of the row (of its first chunk) is under way before the
     // first is used.
     load_chunk<T, GT, NV, !(MULTI && GRAD)>(vec, 0, sp.nvec, t, v);
-    const bool has_one = t < sp.singles;
-    const uint32_t at_one = has_one ? sp.single(t) : 0;
-    const float one = has_one ? T::widen(zr[at_one]) : -INFINITY;
+    const float one = has_one ? T::widen(raw_one) : -INFINITY;
 
     Stat st = {-INFINITY, 0.0f, 0.0f};
     float zy = 0.0f;
@@ -898,10 +969,10 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     };
     if constexpr (Op::kList) {
         const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
-        if (t < kWave)
-            read_teacher<T, Op::kTail>(args, row, zr, V, sp.head, words, t, l);
         if constexpr (GT > kWave && Op::kTail)
             __syncthreads(); // the sums need the bitmap
+        if (t < kWave)
+            weigh_teacher<T, Op::kTail>(args, r, facts, t, l);
         if constexpr (Op::kTail) {
             const TakeUnmarked<T::W> take{l.bits, sp.head, sp.nvec};
             fold_row(has_one && take.skip_one(at_one), take);
@@ -909,7 +980,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             fold_row(false, TakeAll{});
         }
     } else {
-        zy = T::widen(zr[r.y]);
+        zy = T::widen(raw_zy);
         fold_row(false, TakeAll{});
     }
     st = combine<GT, Op::kEntropy>(st, c, parts);
@@ -935,15 +1006,19 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             if (l.state[1] < (int)V && Q < 1.0)
                 rest = 1.0 - Q;
         }
-        if (leader) {
-            const RowLogs logs(st, args.scale);
-            const double ref = __int_as_float(l.state[2]);
-            double loss = *l.cross + Q * ((logs.ref - ref) * logs.scale + logs.ln_s);
+        if (t < kWave) {
+            // Lanes 0, 1 and 2 take the three logarithms at once.
+            const double ln = log(t == 0 ? (double)st.s : t == 1 ? rest : outside);
+            const double ln_s = __shfl(ln, 0), ln_rest = __shfl(ln, 1), ln_out = __shfl(ln, 2);
+            const double ref = __int_as_float(l.state[2]), scale = args.scale;
+            double loss = *l.cross + Q * (((double)reference(st.m) - ref) * scale + ln_s);
             if (Op::kTail && rest > 0.0)
-                loss += rest * (log(rest) - log(outside) + logs.ln_s);
-            args.join.put(row, (double)r.weight * loss);
-            if (args.row_loss_out)
-                args.row_loss_out[row] = (float)loss;
+                loss += rest * (ln_rest - ln_out + ln_s);
+            if (leader) {
+                args.join.put(row, (double)r.weight * loss);
+                if (args.row_loss_out)
+                    args.row_loss_out[row] = (float)loss;
+            }
         }
         factor = r.weight * args.scale;
         mass = (float)(Q + rest);
@@ -1036,11 +1111,12 @@ __global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint
     const u32x4_t* vec = reinterpret_cast<const u32x4_t*>(zr + sp.head);
     const uint32_t first = seg * per;
     const uint32_t last = first + per < sp.nvec ? first + per : sp.nvec;
+    const bool has_one = seg == 0 && t < sp.singles;
+    const S raw_one = zr[has_one ? sp.single(t) : 0];
+    const S raw_zy = zr[r.y];
     u32x4_t v[NV];
     load_chunk<T, GT, NV, false>(vec, first, last, t, v);
-    const bool has_one = seg == 0 && t < sp.singles;
-    const float one = has_one ? T::widen(zr[sp.single(t)]) : -INFINITY;
-    const float zy = T::widen(zr[r.y]);
+    const float one = has_one ? T::widen(raw_one) : -INFINITY, zy = T::widen(raw_zy);
     Stat st = {-INFINITY, 0.0f, 0.0f};
     fold_chunk<T, GT, NV, Op::kEntropy>(v, first, last, t, one, false, c, TakeAll{}, st);
     for (uint32_t next = first + GT * NV; next < last; next += GT * NV) {
@@ -1214,10 +1290,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const typename T::S* z, typen
             dr[at_one] = 0;
         return;
     }
-    u32x4_t v[NV];
-    load_chunk<T, GT, NV, true>(reinterpret_cast<const u32x4_t*>(zr + sp.head), first, sp.nvec, t,
-                                v);
-    const float one = has_one ? T::widen(zr[at_one]) : 0.0f;
+    const S raw_one = zr[at_one];
     // The thread that writes the target's column reads it first: in place,
     // another thread's read could come after that write.
     bool mine = false;
@@ -1229,7 +1302,11 @@ __global__ __launch_bounds__(256) void grad_kernel(const typename T::S* z, typen
             mine = has_one && at_one == r.y;
         }
     }
-    const float zy = mine ? T::widen(zr[r.y]) : 0.0f;
+    const S raw_zy = zr[mine ? r.y : at_one];
+    u32x4_t v[NV];
+    load_chunk<T, GT, NV, true>(reinterpret_cast<const u32x4_t*>(zr + sp.head), first, sp.nvec, t,
+                                v);
+    const float one = T::widen(raw_one), zy = T::widen(raw_zy);
     const Exponent ex(r.ref, c);
     write_chunk<T, GT, NV, Op::kEntropy>(v, dr + sp.head, first, sp.nvec, t, ex, r.slope);
     if (has_one)
@@ -1302,7 +1379,11 @@ void launch_split(const Logits& m, const Part& p, const typename Op::Args& args,
 }
 
 // The threads and registers of a row by its length.  Without a gradient rows
-// pass through a wave or a workgroup of 256.  With one a row stays in
+// pass through a wave or, four vectors at a time, through a workgroup: of 256
+// threads, or of 512 where rows are few (log-probability, bf16, us a call for
+// 256 and 512 threads: 4096 rows of 8192 13.6 and 16.7, 256 rows of 32768 7.1
+// and 5.8, of 131072 20.5 and 14.4; eight vectors at a time and 256 threads:
+// 15.9, 6.9 and 17.2).  With one a row stays in
 // registers: of the smallest group that holds it, so that several rows share a
 // compute unit, or, where there are no more rows than compute units, of 256
 // or 1024 threads, which take their row through faster (policy loss, bf16, us
@@ -1317,8 +1398,10 @@ void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& arg
     if (!m.dz) {
         if (nvec <= 64 * 8)
             launch_rows_as<T, 64, 8, false, false, Op>(m, p, args, lds);
+        else if (nvec >= 4096 && p.rows <= 2u * (uint32_t)dev.cus)
+            launch_rows_as<T, 512, 4, true, false, Op>(m, p, args, lds);
         else
-            launch_rows_as<T, 256, 8, true, false, Op>(m, p, args, lds);
+            launch_rows_as<T, 256, 4, true, false, Op>(m, p, args, lds);
     } else if constexpr (Op::kHasGrad) {
         const bool few = p.rows <= (uint32_t)dev.cus;
         if (few && nvec > 256 && nvec <= 256 * 4)
