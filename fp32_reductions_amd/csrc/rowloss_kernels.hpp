@@ -1340,19 +1340,20 @@ void launch_rows_as(const Logits& m, const Part& p, const typename Op::Args& arg
 
 // Whether the rows of a launch are cut into segments.  us a call, whole rows
 // against segments, bf16:
-//   log-probability, V = 32768: 1 row 4.2 / 3.8, 128 rows 6.0 / 5.4;
-//     131072: 14.2 / 4.1 and 15.7 / 9.6; at 16384 whole rows win (3.5 / 3.7);
-//   policy loss and gradient, V = 65536: 1 row 10.6 / 8.8, 64 rows
-//     11.2 / 10.9, 128 rows 13 / 15; 131072: 16.3 / 8.9, 17.4 / 13.7 and
-//     20 / 20; 262144, which a workgroup cannot hold: 32 / 9.1 and, for 128
-//     rows, 41 / 36.
+//   log-probability, V = 32768: 1 row 3.6 / 3.6, 128 rows 5.0 / 5.6;
+//     49152: 5.3 / 4.1, 64 rows 5.9 / 5.4, 128 rows 6.2 / 6.5;
+//     65536: 6.4 / 4.2, 128 rows 7.4 / 7.3; 131072: 12.3 / 10.3 for 128 rows
+//     and 14.3 / 15.9 for 256;
+//   policy loss and gradient, V = 49152: 1 row 8.6 / 8.3, 64 rows 9.2 / 10.4;
+//     65536: 10.0 / 8.5 and 10.6 / 10.7; 131072: 15.6 / 8.6 and 16.6 / 13.7,
+//     128 rows 17.8 / 20.6; 262144, which a workgroup cannot hold: 32 / 9.1
+//     and, for 128 rows, 41 / 36.
 template <class T>
 bool split_rows(const Logits& m, size_t rows, bool grad)
 {
     const size_t nvec = m.V / T::W;
-    if (!grad)
-        return rows <= kSplitRows && nvec >= 4096;
-    return rows <= (nvec > 16384 ? kSplitRows : kSplitRows / 2) && nvec >= 8192;
+    const size_t many = grad ? 16385 : 8192;
+    return rows <= (nvec >= many ? kSplitRows : kSplitRows / 2) && nvec >= (grad ? 8192 : 6144);
 }
 
 // The workspace's last mebibyte (before the groups' sums) holds what split
