@@ -6,9 +6,8 @@
 // order: a sum of thousands of row losses of both signs keeps its last fp32
 // bits and is the same in every run.
 #include "device.hpp"
-#include "reduce.h"
 #include "rowloss.hpp"
-#include "rowloss_join.hpp"
+#include "rowloss_pairs.hpp"
 
 namespace red {
 namespace {
@@ -48,31 +47,15 @@ __global__ __launch_bounds__(1024) void loss_sum_kernel(const double* __restrict
         loss[0] = (float)((double)old + sum);
 }
 
-struct PairArgs {
-    const double* row_logp;
-    float* row_slope;
-    const int64_t *targets, *starts;
-    const float *ref_logp, *weight;
-    float* seq_logp;
-    Join join;
-    int64_t rows, V;
-    uint32_t pairs;
-    int kind, average;
-    double beta, margin, smoothing;
-};
-
-struct SequenceSum {
-    int64_t begin, end;
-    double logp, count;
-};
-
 // One workgroup per pair.  Sequence p is the chosen one and P + p the
 // rejected; bounds outside [0, rows] are moved into it.
 __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
 {
     __shared__ double lds[4][4];
     const uint32_t p = blockIdx.x;
-    SequenceSum seq[2];
+    const PairValues values(a, p);
+    int64_t begin[2], end[2];
+    double sum[2], count[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const uint64_t i = (uint64_t)side * a.pairs + p;
@@ -81,49 +64,22 @@ __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
         e = e < b ? b : e > a.rows ? a.rows : e;
         double s = 0.0, n = 0.0;
         for (int64_t r = b + threadIdx.x; r < e; r += 256) {
-            s += a.row_logp[r]; // 0 where the target is not a column
+            s += load_shared(a.row_logp + r); // 0 where the target is not a column
             n += (uint64_t)a.targets[r] < (uint64_t)a.V ? 1.0 : 0.0;
         }
-        s = block_sum64<4>(s, lds[2 * side]);
-        n = block_sum64<4>(n, lds[2 * side + 1]);
-        seq[side] = {b, e, a.average && n > 0.0 ? s / n : s, a.average && n > 0.0 ? n : 1.0};
+        begin[side] = b;
+        end[side] = e;
+        sum[side] = block_sum64<4>(s, lds[2 * side]);
+        count[side] = block_sum64<4>(n, lds[2 * side + 1]);
     }
-    const double w = a.weight ? (double)a.weight[p] : 1.0 / (double)a.pairs;
-    double delta = seq[0].logp - seq[1].logp;
-    if (a.ref_logp)
-        delta = (seq[0].logp - (double)a.ref_logp[p]) -
-                (seq[1].logp - (double)a.ref_logp[(uint64_t)a.pairs + p]);
-    const double h = a.beta * delta - a.margin;
-    double loss, slope; // slope: d loss / d h
-    if (a.kind == RED_PREF_SIGMOID) {
-        // softplus(x) = max(x, 0) + log1p(exp(-|x|))
-        const double t = exp(-fabs(h)), l = log1p(t);
-        const double pos = fmax(h, 0.0) + l, neg = fmax(-h, 0.0) + l; // of h and of -h
-        const double up = h >= 0.0 ? 1.0 / (1.0 + t) : t / (1.0 + t);  // sigmoid(h)
-        const double down = h >= 0.0 ? t / (1.0 + t) : 1.0 / (1.0 + t);
-        loss = (1.0 - a.smoothing) * neg + a.smoothing * pos;
-        slope = a.smoothing * up - (1.0 - a.smoothing) * down;
-    } else if (a.kind == RED_PREF_HINGE) {
-        loss = h >= 1.0 ? 0.0 : 1.0 - h;
-        slope = h >= 1.0 ? 0.0 : -1.0;
-    } else {
-        const double d = (h - 0.5) / a.beta;
-        loss = d * d;
-        slope = 2.0 * d / a.beta;
-    }
-    const double g = w != 0.0 ? w * slope * a.beta : 0.0;
-    if (threadIdx.x == 0) {
-        a.seq_logp[p] = (float)seq[0].logp;
-        a.seq_logp[(uint64_t)a.pairs + p] = (float)seq[1].logp;
-        a.join.put(p, w != 0.0 ? w * loss : 0.0);
-    }
+    const PairResult pair(a, values, sum, count);
+    if (threadIdx.x == 0)
+        pair.put(a, p);
     const unsigned before = threadIdx.x < kWave ? a.join.arrive(p) : 0;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const float mine = (float)((side ? -g : g) / seq[side].count);
-        for (int64_t r = seq[side].begin + threadIdx.x; r < seq[side].end; r += 256)
-            a.row_slope[r] = mine;
-    }
+    for (int side = 0; side < 2; ++side)
+        for (int64_t r = begin[side] + threadIdx.x; r < end[side]; r += 256)
+            a.row_slope[r] = pair.slope[side];
     if (threadIdx.x < kWave)
         a.join.finish(before, p, a.pairs);
 }
@@ -138,17 +94,11 @@ hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int ac
     return hipGetLastError();
 }
 
-hipError_t launch_preference_pairs(const PreferenceCall& a, const double* row_logp,
-                                   float* row_slope, const Join& join, hipStream_t stream)
+hipError_t launch_preference_pairs(const PairArgs& args, hipStream_t stream)
 {
-    const PairArgs args = {row_logp,     row_slope,  a.targets,         a.starts,
-                           a.ref_logp,   a.weight,   a.seq_logp,        join,
-                           (int64_t)a.m.rows, (int64_t)a.m.V, (uint32_t)a.pairs, a.kind,
-                           a.average,    a.beta,     a.margin,          a.smoothing};
-    hipLaunchKernelGGL(preference_pairs_kernel, dim3((uint32_t)a.pairs), dim3(256), 0, stream,
-                       args);
+    hipLaunchKernelGGL(preference_pairs_kernel, dim3(args.pairs), dim3(256), 0, stream, args);
     const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? sum_joined(join, a.pairs, stream) : e;
+    return e == hipSuccess ? sum_joined(args.join, args.pairs, stream) : e;
 }
 
 #define RED_BY_TYPE(t, call)                        \

@@ -117,10 +117,4 @@ extern template struct RowLoss<ElemBF16>;
 // loss[0] = [loss[0] +] sum of n row losses (rowloss.hip).
 hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int accum,
                            hipStream_t stream);
-// The pairs of a preference loss: from the log-probabilities of the rows to
-// the sequences', the rows' slopes and the loss (rowloss.hip).
-struct Join;
-hipError_t launch_preference_pairs(const PreferenceCall& a, const double* row_logp,
-                                   float* row_slope, const Join& join, hipStream_t stream);
-
 } // namespace red

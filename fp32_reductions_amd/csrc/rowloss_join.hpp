@@ -69,6 +69,14 @@ struct Join {
     float* loss;
     int accum;
     __device__ __forceinline__ void put(size_t row, double v) const { store_shared(row_loss + row, v); }
+    // Sum over a wave, in every lane.
+    static __device__ __forceinline__ double total(double v)
+    {
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1)
+            v += __shfl_xor(v, m);
+        return v;
+    }
     // By every lane of the wave whose lane 0 has put the row's loss.
     __device__ __forceinline__ unsigned arrive(uint32_t row) const
     {
@@ -114,13 +122,6 @@ struct Join {
     static __device__ __forceinline__ unsigned arrive_at(unsigned* p)
     {
         return (threadIdx.x & 63) == 0 ? count_shared(p) : 0;
-    }
-    static __device__ __forceinline__ double total(double v)
-    {
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1)
-            v += __shfl_xor(v, m);
-        return v;
     }
 };
 static_assert((1 + kJoinGroups) * kCountStride <= kCounterWords, "a count for each group");

@@ -30,7 +30,7 @@
 
 #include "device.hpp"
 #include "rowloss.hpp"
-#include "rowloss_join.hpp"
+#include "rowloss_pairs.hpp"
 
 namespace red {
 
@@ -547,27 +547,31 @@ struct LogprobOp {
         return {0.0f, 0.0f};
     }
     static __device__ __forceinline__ void dead(const Args&, size_t, bool) {}
-    static __device__ __forceinline__ NoJoin join(const Args&) { return {}; }
+    static __device__ __forceinline__ NoJoin join(const Args&, const Row&) { return {}; }
 };
 
 // First pass of the preference loss: maximum, sum and log-probability.
+// JOIN: the wave that comes last in a pair finishes the pair (PairJoin), which
+// takes twice the registers.
+template <bool JOIN>
 struct PreferenceOp {
     static constexpr bool kEntropy = false, kList = false, kHasGrad = false;
     struct Args {
-        const int64_t* targets;
         float2* stat;
-        double* logp;
-        float* slope;
+        PairArgs pair;
     };
     struct Row {
         bool live;
         uint32_t y;
+        int64_t start; // this lane's bound of a sequence
     };
     static __device__ __forceinline__ Row begin(const Args& a, size_t row, uint32_t V)
     {
-        const int64_t y = a.targets[row];
+        const uint32_t lane = threadIdx.x & 63, last = 2 * a.pair.pairs;
+        const int64_t y = a.pair.targets[row];
         const bool hit = (uint64_t)y < V;
-        return {hit, hit ? (uint32_t)y : 0u};
+        return {hit, hit ? (uint32_t)y : 0u,
+                JOIN ? a.pair.starts[lane < last ? lane : last] : 0};
     }
     static __device__ __forceinline__ Slope done(const Args& a, const Row&, size_t row,
                                                  const Stat& st, float zy, bool leader, float& fix)
@@ -575,8 +579,7 @@ struct PreferenceOp {
         if (leader) {
             const RowLogs l(st, 1.0f);
             a.stat[row] = make_float2(st.m, st.s);
-            a.logp[row] = l.logp(zy);
-            a.slope[row] = 0.0f;
+            put(a, row, l.logp(zy));
         }
         fix = 0.0f;
         return {0.0f, 0.0f};
@@ -585,11 +588,23 @@ struct PreferenceOp {
     {
         if (leader) {
             a.stat[row] = make_float2(0.0f, 1.0f);
-            a.logp[row] = 0.0;
-            a.slope[row] = 0.0f;
+            put(a, row, 0.0);
         }
     }
-    static __device__ __forceinline__ NoJoin join(const Args&) { return {}; }
+    // The slope of a row that no sequence has is 0.
+    static __device__ __forceinline__ void put(const Args& a, size_t row, double logp)
+    {
+        store_shared(a.pair.row_logp + row, logp);
+        if (!JOIN)
+            a.pair.row_slope[row] = 0.0f;
+    }
+    static __device__ __forceinline__ auto join(const Args& a, const Row& r)
+    {
+        if constexpr (JOIN)
+            return PairJoin(a.pair, r.start);
+        else
+            return NoJoin();
+    }
 };
 
 // Clipped policy loss.  With r = exp(logp - old), d = ref - logp:
@@ -625,7 +640,10 @@ struct PolicyOp {
     {
         const RowLogs l(st, a.scale);
         const double logp = l.logp(zy), adv = r.advantage, w = r.weight;
-        const double ratio = exp(logp - (double)r.old_logp);
+        // Even lanes take the ratio's exponential, odd ones the KL term's.
+        const double d = a.ref_logp ? (double)r.ref_logp - logp : 0.0;
+        const double e = exp(threadIdx.x & 1 ? d : logp - (double)r.old_logp);
+        const double ratio = __shfl(e, 0);
         const double free = ratio * adv;
         const double bound = ratio < a.clip_min   ? a.clip_min
                              : ratio > a.clip_max ? a.clip_max
@@ -635,7 +653,8 @@ struct PolicyOp {
         double loss = free > clipped ? -clipped : -free;
         double g = free > clipped ? 0.0 : -free;
         if (a.ref_logp) {
-            const double d = (double)r.ref_logp - logp, k = expm1(d);
+            // In fp64 the difference is off by 2^-53, below a loss's last bit.
+            const double k = __shfl(e, 1) - 1.0;
             loss += a.kl * (k - d);
             g -= a.kl * k;
         }
@@ -669,7 +688,7 @@ struct PolicyOp {
             a.join.put(row, 0.0);
         }
     }
-    static __device__ __forceinline__ const Join& join(const Args& a) { return a.join; }
+    static __device__ __forceinline__ Join join(const Args& a, const Row&) { return a.join; }
 };
 
 // Divergence from a teacher's largest logits.  S: the columns listed, q_k
@@ -708,7 +727,7 @@ struct DistillOp {
                 a.row_loss_out[row] = 0.0f;
         }
     }
-    static __device__ __forceinline__ const Join& join(const Args& a) { return a.join; }
+    static __device__ __forceinline__ Join join(const Args& a, const Row&) { return a.join; }
 };
 
 // A row's teacher in LDS: its columns (-1: padding; the high bit marks the
@@ -833,20 +852,26 @@ __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Ar
     ref = reference(wave_reduce<OpMax>(ref));
     wave_lds_fence();
     const double scale = a.scale;
-    double shift;
+    double shift, first_q = 0.0; // first_q: the probability of this lane's first entry
     if constexpr (TAIL) {
         shift = r.teacher_lse;
     } else {
         double s = 0.0;
         const double most = reference(top);
-        for (uint32_t k = lane; k < a.K; k += kWave)
-            s += exp(((double)l.q[k] - most) * scale);
-        shift = most * scale + log(wave_sum64(s));
+        for (uint32_t k = lane; k < a.K; k += kWave) {
+            const double e = exp(((double)l.q[k] - most) * scale);
+            first_q = k == lane ? e : first_q;
+            s += e;
+        }
+        s = wave_sum64(s);
+        shift = most * scale + log(s);
+        first_q /= s;
     }
     double sum = 0.0, cross = 0.0;
     int listed = facts.listed;
     for (uint32_t k = lane; k < a.K; k += kWave) {
-        const double lq = (double)l.q[k] * scale - shift, q = exp(lq);
+        const double lq = (double)l.q[k] * scale - shift;
+        const double q = !TAIL && k == lane ? first_q : exp(lq);
         const int col = l.col[k];
         l.q[k] = col >= 0 ? (float)q : 0.0f;
         if (col < 0)
@@ -918,7 +943,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const bool leader = t == 0;
     const Span sp = Span::of<T>(zr, V);
     const typename Op::Row r = Op::begin(args, row, V);
-    const auto join = Op::join(args);
+    auto join = Op::join(args, r);
     auto dead_row = [&]() __attribute__((always_inline)) {
         Op::dead(args, row, leader);
         const unsigned before = t < kWave ? join.arrive(row) : 0;
@@ -1077,7 +1102,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
 constexpr uint32_t kSplitRows = 128, kSegmentsMost = kWave;
 constexpr uint32_t kSegmentVecs = 1024; // 16 KiB: four vectors for each thread
 constexpr uint32_t kRowCounts = (1 + kJoinGroups) * kCountStride;
-static_assert(kRowCounts + kSplitRows * kCountStride <= kCounterWords, "a count for each row");
+static_assert(kRowCounts + kSplitRows * kCountStride <= kPairCounts, "a count for each row");
 
 struct Split {
     float* part;      // [row][3][kSegmentsMost]: maximum, sum, entropy sum
@@ -1098,7 +1123,7 @@ __global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint
     const S* zr = z + (size_t)row * ld;
     const Span sp = Span::of<T>(zr, V);
     const typename Op::Row r = Op::begin(args, row, V);
-    const auto join = Op::join(args);
+    auto join = Op::join(args, r);
     if (!r.live) {
         if (seg == 0 && t < kWave) {
             Op::dead(args, row, t == 0);
@@ -1605,17 +1630,32 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo& dev
                   "the statistics fit the workspace, below what split rows share");
     Logits read = a.m;
     read.dz = nullptr;
-    hipError_t e = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
-        const PreferenceOp::Args args = {a.targets + p.row0, stat + p.row0, logp + p.row0,
-                                         slope + p.row0};
-        if (split_rows<T>(read, p.rows, false))
-            launch_split<T, PreferenceOp>(read, p, args, split_of(ws, false));
+    // Few rows: many would queue at the pairs' counts and miss the registers
+    // that the pairs take (us a call with a kernel for the pairs and without, 2
+    // pairs, bf16: 4 rows of 1000 10.3 and 9.0, 64 of 32768 14.3 and 13.0, 256
+    // 19.4 and 18.9, 1024 of 1000 12.1 and 17.0).
+    const bool joined = a.pairs <= kJoinedPairs && a.m.rows <= (size_t)dev.cus;
+    const PairArgs pair = {logp, slope, a.targets, a.starts, a.ref_logp, a.weight, a.seq_logp,
+                           join_of(ws, pair_loss, a.pairs, a.loss, a.accum), (int64_t)a.m.rows,
+                           (int64_t)a.m.V, (uint32_t)a.pairs, a.kind, a.average, a.beta, a.margin,
+                           a.smoothing, ws.counters + kPairCounts};
+    // One part: there are at most kPrefRowsMax rows.
+    static_assert(kPrefRowsMax <= kRowsPerLaunch, "a row's number is its place in the launch");
+    const Part all = {0, (uint32_t)a.m.rows, stream};
+    auto launch = [&](auto op) {
+        typedef decltype(op) Op;
+        if (split_rows<T>(read, a.m.rows, false))
+            launch_split<T, Op>(read, all, {stat, pair}, split_of(ws, false));
         else
-            launch_rows_op<T, PreferenceOp>(read, p, args, 0, dev);
-    });
-    if (e == hipSuccess)
-        e = launch_preference_pairs(a, logp, slope, join_of(ws, pair_loss, a.pairs, a.loss, a.accum),
-                                    stream);
+            launch_rows_op<T, Op>(read, all, {stat, pair}, 0, dev);
+    };
+    if (joined)
+        launch(PreferenceOp<true>{});
+    else
+        launch(PreferenceOp<false>{});
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && !joined)
+        e = launch_preference_pairs(pair, stream);
     if (e == hipSuccess && a.m.dz)
         e = each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
             const size_t r = p.row0;
