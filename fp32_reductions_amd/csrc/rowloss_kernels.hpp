@@ -243,17 +243,13 @@ template <int W>
 struct TakeUnmarked {
     static constexpr bool kSome = true;
     const uint32_t* bits;
-    uint32_t head, nvec;
+    uint32_t nvec, singles; // singles: a bit for each element outside the vectors
     __device__ __forceinline__ unsigned skip(uint32_t j) const
     {
-        const uint32_t at = ((j < nvec ? j : nvec) + 1) * W; // no mark past the row's end
+        const uint32_t at = (j < nvec ? j : 0) * W; // past the row's end nothing is lost
         return (reinterpret_cast<const unsigned char*>(bits)[at >> 3] >> (at & 7)) & ((1u << W) - 1);
     }
-    __device__ __forceinline__ bool skip_one(uint32_t e) const
-    {
-        const uint32_t at = e - head + W;
-        return (bits[at >> 5] >> (at & 31)) & 1;
-    }
+    __device__ __forceinline__ bool skip_one(uint32_t t) const { return (singles >> t) & 1; }
 };
 
 // Folds the NG vectors first + k GT + t and the single element `one` into st:
@@ -740,30 +736,38 @@ struct TeacherLds {
     float* z;
     double* cross; // sum q (ln q - scale (z - ref)), ref the largest logit listed
     double* sum;   // Q
-    int* state;    // [0]: the row has a teacher; [1]: listed columns; [2]: ref
+    int* state;    // [0]: the row has a teacher; [1]: ref
+    uint32_t* marked; // of each wave: the columns it marked; the high bit: one of them twice
+    static constexpr size_t kHead = 32 + 16 * 4;
     static __host__ __device__ size_t bytes(size_t words, size_t K)
     {
-        return (32 + 4 * words + 12 * K + 15) / 16 * 16;
+        return (kHead + 4 * words + 12 * K + 15) / 16 * 16;
     }
     __device__ __forceinline__ TeacherLds(char* base, uint32_t words, uint32_t K)
     {
         cross = reinterpret_cast<double*>(base);
         sum = cross + 1;
         state = reinterpret_cast<int*>(base + 16);
-        bits = reinterpret_cast<uint32_t*>(base + 32);
+        marked = reinterpret_cast<uint32_t*>(base + 32);
+        bits = reinterpret_cast<uint32_t*>(base + kHead);
         col = reinterpret_cast<int*>(bits + words);
         q = reinterpret_cast<float*>(col + K);
         z = q + K;
     }
 };
 
-// Words of the bitmap of V columns: vectors start at bit W, so the columns
-// before the first vector (fewer than W) have bits of their own.
-template <class T>
-__host__ __device__ inline uint32_t bitmap_words(uint32_t V)
+template <class Op>
+__device__ __forceinline__ uint32_t list_length(const typename Op::Args& a)
 {
-    return (V + 2 * T::W) / 32 + 1;
+    if constexpr (Op::kList)
+        return a.K;
+    else
+        return 0;
 }
+
+// Words of the bitmap of V columns: a bit for each element of a vector, in the
+// order of the vectors, and one word for the elements outside.
+inline __host__ __device__ uint32_t bitmap_words(uint32_t V) { return (V + 31) / 32 + 1; }
 
 __device__ __forceinline__ double wave_sum64(double v)
 {
@@ -780,74 +784,125 @@ __device__ __forceinline__ void wave_lds_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// One wave reads the row's list into `l`: columns, their logits, the
-// student's logits in them, and the bitmap.  It does so before its share of
-// the row's own loads, which would otherwise return first, and the other
-// waves fold the row while it weighs the teacher (4096 rows of 131072 bf16,
-// 64 entries and the rest: 428 us with the list read after the row, 413 so).
-struct ListFacts {
-    float val, z; // this lane's largest logits
-    int listed;   // columns that this lane was first to mark
-    bool again;   // this lane found a column marked already
-};
+// Reads the row's list.  Every wave marks the columns in its own vectors, in
+// words of its own (64 vectors after one another are 64 W bits): so no wave
+// waits for another before it folds.  The first wave also keeps the list:
+// columns, their logits and the student's logits in them.  The columns are
+// loaded before the row's vectors, which would otherwise return first, and
+// used when the last of those is under way (4096 rows of 131072 bf16, 64
+// entries and the rest: 412 us with one wave that marks for all, 381 so).
+template <class T, int GT>
+struct ListReader {
+    typedef typename T::S S;
+    static constexpr uint32_t kBatch = 2, kStep = kBatch * kWave;
+    const TeacherLds& l;
+    const Span& sp;
+    const int64_t* idx;
+    const float* val;
+    const S* z;
+    uint32_t V, K, words, wave, lane;
+    uint32_t k0 = 0, listed = 0;
+    bool again = false;
+    float top_val = -INFINITY, top_z = -INFINITY; // first wave: this lane's largest
+    int64_t at[kBatch];
+    float v[kBatch];
+    S zk[kBatch];
 
-template <class T>
-__device__ __forceinline__ ListFacts gather_list(const int64_t* idx, const float* val, uint32_t K,
-                                                 const typename T::S* z, uint32_t V,
-                                                 uint32_t head, uint32_t words, uint32_t lane,
-                                                 const TeacherLds& l)
-{
-    constexpr uint32_t kBatch = 2;
-    ListFacts facts = {-INFINITY, -INFINITY, 0, false};
-    for (uint32_t k0 = 0; k0 < K; k0 += kBatch * kWave) {
-        int64_t at[kBatch];
-        float v[kBatch], zk[kBatch];
+    __device__ __forceinline__ void load()
+    {
 #pragma unroll
         for (uint32_t b = 0; b < kBatch; ++b) {
             const uint32_t k = k0 + b * kWave + lane;
-            at[b] = k < K ? idx[k] : -1;
-            v[b] = k < K ? val[k] : -INFINITY;
+            at[b] = idx[k < K ? k : 0];
+            v[b] = val[k < K && wave == 0 ? k : 0]; // no branch: it would wait for the load
         }
         if (k0 == 0)
-            for (uint32_t i = lane; i < words; i += kWave)
-                l.bits[i] = 0;
-        wave_lds_fence();
-#pragma unroll
-        for (uint32_t b = 0; b < kBatch; ++b)
-            if ((uint64_t)at[b] < V) {
-                const uint32_t bit_at = (uint32_t)at[b] + T::W - head, bit = 1u << (bit_at & 31);
-                const bool seen = atomicOr(&l.bits[bit_at >> 5], bit) & bit;
-                facts.again |= seen;
-                facts.listed += !seen;
-            }
-#pragma unroll
-        for (uint32_t b = 0; b < kBatch; ++b)
-            zk[b] = (uint64_t)at[b] < V ? T::widen(z[at[b]]) : -INFINITY;
+            clear();
 #pragma unroll
         for (uint32_t b = 0; b < kBatch; ++b) {
-            const uint32_t k = k0 + b * kWave + lane;
-            const bool in = (uint64_t)at[b] < V;
-            if (k < K) {
-                l.col[k] = in ? (int)at[b] : -1;
-                l.q[k] = in ? v[b] : -INFINITY;
-                l.z[k] = zk[b];
-            }
-            facts.val = fmaxf(facts.val, in ? v[b] : -INFINITY);
-            facts.z = fmaxf(facts.z, zk[b]);
+            at[b] = k0 + b * kWave + lane < K && (uint64_t)at[b] < V ? at[b] : -1;
+            zk[b] = z[at[b] < 0 || wave != 0 ? 0 : at[b]];
         }
     }
-    return facts;
-}
+    // The wave's words of the bitmap.
+    __device__ __forceinline__ void clear()
+    {
+        constexpr uint32_t kWords = kWave * T::W / 32; // of 64 vectors
+        const uint32_t rounds = (sp.nvec + GT - 1) / GT;
+        for (uint32_t i = lane; i < rounds * kWords; i += kWave) {
+            const uint32_t word = (i / kWords * GT + wave * kWave) * T::W / 32 + i % kWords;
+            if (word < words - 1)
+                l.bits[word] = 0;
+        }
+        if (wave == 0 && lane == 0)
+            l.bits[words - 1] = 0;
+        wave_lds_fence();
+    }
+    __device__ __forceinline__ void use()
+    {
+#pragma unroll
+        for (uint32_t b = 0; b < kBatch; ++b) {
+            if (wave == 0) {
+                const uint32_t k = k0 + b * kWave + lane;
+                const float logit = at[b] < 0 ? -INFINITY : T::widen(zk[b]);
+                const float value = at[b] < 0 ? -INFINITY : v[b];
+                if (k < K) {
+                    l.col[k] = (int)at[b];
+                    l.q[k] = value;
+                    l.z[k] = logit;
+                }
+                top_val = fmaxf(top_val, value);
+                top_z = fmaxf(top_z, logit);
+            }
+            if (at[b] < 0)
+                continue;
+            const uint32_t e = (uint32_t)at[b];
+            uint32_t place, owner = 0;
+            if (e >= sp.head && e < sp.tail) {
+                place = e - sp.head;
+                owner = place / T::W % GT / kWave;
+            } else {
+                place = (words - 1) * 32 + (e < sp.head ? e : e - sp.tail + sp.head);
+            }
+            if (owner == wave) {
+                const uint32_t bit = 1u << (place & 31);
+                const bool seen = atomicOr(&l.bits[place >> 5], bit) & bit;
+                again |= seen;
+                listed += !seen;
+            }
+        }
+    }
+    // All but the last entries, whose loads are left under way.
+    __device__ __forceinline__ void begin()
+    {
+        for (load(); k0 + kStep < K; load()) {
+            use();
+            k0 += kStep;
+        }
+    }
+    // The last, and what the wave has found.
+    __device__ __forceinline__ void end()
+    {
+        use();
+        uint32_t n = listed;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1)
+            n += __shfl_xor(n, m);
+        n |= __any(again) ? 0x80000000u : 0u;
+        if (lane == 0)
+            l.marked[wave] = n;
+        wave_lds_fence();
+    }
+};
 
 // The same wave turns the list into the teacher's probabilities and the sums
 // of the row's loss.  fp64: a row's loss is a small difference of these sums.
 template <class T, bool TAIL>
 __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Args& a,
                                               const typename DistillOp<TAIL>::Row& r,
-                                              const ListFacts& facts, uint32_t lane,
+                                              float top, float ref, uint32_t lane,
                                               const TeacherLds& l)
 {
-    float top = facts.val, ref = facts.z;
     top = wave_reduce<OpMax>(top);
     ref = reference(wave_reduce<OpMax>(ref));
     wave_lds_fence();
@@ -868,7 +923,6 @@ __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Ar
         first_q /= s;
     }
     double sum = 0.0, cross = 0.0;
-    int listed = facts.listed;
     for (uint32_t k = lane; k < a.K; k += kWave) {
         const double lq = (double)l.q[k] * scale - shift;
         const double q = !TAIL && k == lane ? first_q : exp(lq);
@@ -882,36 +936,34 @@ __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Ar
     }
     sum = wave_sum64(sum);
     cross = wave_sum64(cross);
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1)
-        listed += __shfl_xor(listed, m);
-    wave_lds_fence();
-    if (__any(facts.again)) {
-        // A column listed more than once: its first entry takes the sum of
-        // the probabilities, the others are marked.
-        for (uint32_t k = lane; k < a.K; k += kWave) {
-            const int col = l.col[k] & 0x7fffffff;
-            if (col == 0x7fffffff)
-                continue;
-            uint32_t first = k;
-            float q = 0.0f;
-            for (uint32_t j = 0; j < a.K; ++j)
-                if ((l.col[j] & 0x7fffffff) == col) {
-                    first = j < first ? j : first;
-                    q += l.q[j];
-                }
-            if (first == k)
-                l.q[k] = q;
-            else
-                l.col[k] = col | (int)0x80000000;
-        }
-    }
     if (lane == 0) {
         *l.sum = sum;
         *l.cross = cross;
         l.state[0] = TAIL || top != -INFINITY;
-        l.state[1] = listed;
-        l.state[2] = __float_as_int(ref);
+        l.state[1] = __float_as_int(ref);
+    }
+    wave_lds_fence();
+}
+
+// Where a column is listed more than once its first entry takes the sum of the
+// probabilities, and the others are marked.  One wave.
+__device__ __forceinline__ void merge_entries(uint32_t K, uint32_t lane, const TeacherLds& l)
+{
+    for (uint32_t k = lane; k < K; k += kWave) {
+        const int col = l.col[k] & 0x7fffffff;
+        if (col == 0x7fffffff)
+            continue;
+        uint32_t first = k;
+        float q = 0.0f;
+        for (uint32_t j = 0; j < K; ++j)
+            if ((l.col[j] & 0x7fffffff) == col) {
+                first = j < first ? j : first;
+                q += l.q[j];
+            }
+        if (first == k)
+            l.q[k] = q;
+        else
+            l.col[k] = col | (int)0x80000000;
     }
     wave_lds_fence();
 }
@@ -959,13 +1011,14 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const u32x4_t* vec = reinterpret_cast<const u32x4_t*>(zr + sp.head);
     constexpr uint32_t kChunk = GT * NV;
     const uint32_t chunks = MULTI ? (sp.nvec + kChunk - 1) / kChunk : 1;
-    const uint32_t words = Op::kList ? bitmap_words<T>(V) : 0;
-    ListFacts facts;
+    const uint32_t words = Op::kList ? bitmap_words(V) : 0;
+    const uint32_t K = list_length<Op>(args);
+    const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, K), words, K);
+    ListReader<T, GT> list = {l, sp, nullptr, nullptr, zr, V, K, words, t / kWave, t % kWave};
     if constexpr (Op::kList) {
-        if (t < kWave)
-            facts = gather_list<T>(
-                args.idx + row * args.ldk, args.val + row * args.ldk, args.K, zr, V, sp.head, words, t,
-                TeacherLds(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K));
+        list.idx = args.idx + row * args.ldk;
+        list.val = args.val + row * args.ldk;
+        list.begin();
     }
     // Loads return in the order of their issue: the single elements first, or
     // the fold of the first vectors would wait for the last.
@@ -993,14 +1046,12 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             }
     };
     if constexpr (Op::kList) {
-        const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
-        if constexpr (GT > kWave && Op::kTail)
-            __syncthreads(); // the sums need the bitmap
+        list.end();
         if (t < kWave)
-            weigh_teacher<T, Op::kTail>(args, r, facts, t, l);
+            weigh_teacher<T, Op::kTail>(args, r, list.top_val, list.top_z, t, l);
         if constexpr (Op::kTail) {
-            const TakeUnmarked<T::W> take{l.bits, sp.head, sp.nvec};
-            fold_row(has_one && take.skip_one(at_one), take);
+            const TakeUnmarked<T::W> take{l.bits, sp.nvec, has_one ? l.bits[words - 1] : 0u};
+            fold_row(has_one && take.skip_one(t), take);
         } else {
             fold_row(false, TakeAll{});
         }
@@ -1014,10 +1065,21 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     Slope slope;
     float fix = 0.0f, factor = 0.0f, mass = 0.0f;
     if constexpr (Op::kList) {
-        const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words, args.K);
         if (!l.state[0]) { // no teacher: the row does not count
             dead_row();
             return;
+        }
+        uint32_t listed = 0, again = 0;
+#pragma unroll
+        for (int w = 0; w < GT / kWave; ++w) {
+            listed += l.marked[w] & 0x7fffffffu;
+            again |= l.marked[w] & 0x80000000u;
+        }
+        if (__builtin_amdgcn_readfirstlane(again)) {
+            if (t < kWave)
+                merge_entries(args.K, t, l);
+            if constexpr (GT > kWave)
+                __syncthreads();
         }
         const double Q = *l.sum;
         double rest = 0.0, outside = st.s;
@@ -1028,14 +1090,14 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
                     in += exp2_fast(ex.at(l.z[k]));
             in = wave_reduce<OpSum>(in);
             st.s += in;
-            if (l.state[1] < (int)V && Q < 1.0)
+            if (listed < V && Q < 1.0)
                 rest = 1.0 - Q;
         }
         if (t < kWave) {
             // Lanes 0, 1 and 2 take the three logarithms at once.
             const double ln = log(t == 0 ? (double)st.s : t == 1 ? rest : outside);
             const double ln_s = __shfl(ln, 0), ln_rest = __shfl(ln, 1), ln_out = __shfl(ln, 2);
-            const double ref = __int_as_float(l.state[2]), scale = args.scale;
+            const double ref = __int_as_float(l.state[1]), scale = args.scale;
             double loss = *l.cross + Q * (((double)reference(st.m) - ref) * scale + ln_s);
             if (Op::kTail && rest > 0.0)
                 loss += rest * (ln_rest - ln_out + ln_s);
@@ -1069,8 +1131,6 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         // The few columns with more to them are written again, after the
         // stores above.
         if constexpr (Op::kList) {
-            const TeacherLds l(dynamic_lds + group * TeacherLds::bytes(words, args.K), words,
-                               args.K);
             if constexpr (GT > kWave)
                 __syncthreads();
             for (uint32_t k = t; k < args.K; k += GT)
@@ -1556,7 +1616,7 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo& dev, cons
                                hipStream_t stream)
 {
     using namespace rowloss;
-    const size_t lds = TeacherLds::bytes(bitmap_words<T>((uint32_t)a.m.V), a.K);
+    const size_t lds = TeacherLds::bytes(bitmap_words((uint32_t)a.m.V), a.K);
     const float mean = (float)(1.0 / (double)a.m.rows);
     hipError_t e = hipSuccess;
     const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
