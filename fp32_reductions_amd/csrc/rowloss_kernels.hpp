@@ -13,9 +13,10 @@
 //
 // with A and B from the loss of that row alone.  So a loss and its gradient
 // need one read of the row and one write: row_kernel keeps the row in the
-// registers of its workgroup between the two.  What bounds it is HBM; at 16
-// bits the exponentials come near it (two per element, each element unpacked
-// three times).
+// registers of its workgroup between the two.  What bounds it is HBM where
+// rows are many (the vector unit issues in half of the cycles at 16 bits: two
+// exponentials per element, each element unpacked three times), and the chain
+// of one row's latencies where they are few.
 //
 // Statistics are fp32 per thread (sums of at most a few hundred terms, then
 // a tree); what is computed once per row (logarithms, ratios, losses) is
@@ -976,6 +977,11 @@ __device__ __forceinline__ void merge_entries(uint32_t K, uint32_t lane, const T
 // is still there when the gradient is written and the others are read again
 // (from the caches: the rows in flight on 256 compute units fit there).
 // GRAD: the gradient is written.
+//
+// Measured (bf16, us a call): policy loss of 8192 rows of 131072, a quarter of
+// them masked, 655 (5.7 TB/s; 639 without arithmetic), of 1024 rows of 32768
+// 26, of 96 rows 8.7; log-probability and entropy of 4096 rows of 131072 168
+// (6.4 TB/s).
 template <class T, int GT, int NV, bool MULTI, bool GRAD, class Op>
 __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const typename T::S* z, typename T::S* dz, uint32_t rows, uint32_t V, size_t ld, size_t ldd,
@@ -1243,7 +1249,8 @@ __global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint
 // ---- a gradient whose statistics are there already --------------------------
 //
 // A segment of GT * NV vectors of a row per group of threads: nothing is
-// reduced, so rows are cut as finely as the device wants.
+// reduced, so rows are cut as finely as the device wants.  One read and one
+// write: 4096 rows of 131072 bf16 in 354 us, 6.1 TB/s.
 
 // Gradient of the log-probability (glogp) and the entropy (gentropy):
 //   dz = scale (g (delta_vy - p) - h p (ln p + H)),  ln p = scale z - lse.

@@ -61,7 +61,8 @@
  *   - Workspace.  The calls that combine per-workgroup partials in a second
  *     kernel (1-D, fused, column and column-product calls, row calls
  *     with very long rows or very few rows, and the losses) keep those partials in a
- *     16 MiB workspace the library allocates on the first such call for a
+ *     workspace (16 MiB and 128 KiB of counts, which are zero between
+ *     calls) the library allocates on the first such call for a
  *     (device, stream) pair and keeps until red_release_workspace.  For
  *     hipStreamPerThread, which names a different stream in every host
  *     thread, the workspace belongs to (device, calling thread).  A call
