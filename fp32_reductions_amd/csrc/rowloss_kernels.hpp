@@ -14,9 +14,10 @@
 // with A and B from the loss of that row alone.  So a loss and its gradient
 // need one read of the row and one write: row_kernel keeps the row in the
 // registers of its workgroup between the two.  What bounds it is HBM where
-// rows are many (the vector unit issues in half of the cycles at 16 bits: two
-// exponentials per element, each element unpacked three times), and the chain
-// of one row's latencies where they are few.
+// rows are many (at 16 bits the vector unit is busy in half of the cycles with a
+// gradient, where an element is unpacked three times and has two exponentials,
+// and in nine of ten where an entropy alone is wanted), and the chain of one
+// row's latencies where they are few.
 //
 // Statistics are fp32 per thread (sums of at most a few hundred terms, then
 // a tree); what is computed once per row (logarithms, ratios, losses) is
