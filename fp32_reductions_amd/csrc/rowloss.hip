@@ -17,9 +17,7 @@ namespace {
 template <int WAVES>
 __device__ __forceinline__ double block_sum64(double v, double* lds)
 {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1)
-        v += __shfl_xor(v, m);
+    v = wave_sum64(v);
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x / 64] = v;
     __syncthreads();

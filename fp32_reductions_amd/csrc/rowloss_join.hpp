@@ -28,6 +28,34 @@ constexpr uint32_t kJoinGroup = kWave, kJoinGroups = 256;
 constexpr uint32_t kJoinRows = kJoinGroup * kJoinGroups;
 constexpr uint32_t kCountStride = 64; // words between counts
 
+// Sum over a wave in fp64, in every lane: by DPP as in wave_reduce, a lane's
+// two halves at a time.  (With __shfl_xor, an LDS permute for each half and
+// step, a sum took three times as long: distillation of 1 row of 1000 with 32
+// entries and the rest 6.0 us a call, 5.6 so.)  All lanes take part.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_add64(double v)
+{
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)b, CTRL, ROW_MASK, 0xf, false);
+    const unsigned hi =
+        __builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), CTRL, ROW_MASK, 0xf, false);
+    return v + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double wave_sum64(double v)
+{
+    v = dpp_add64<0x111, 0xf>(v); // row_shr:1
+    v = dpp_add64<0x112, 0xf>(v); // row_shr:2
+    v = dpp_add64<0x114, 0xf>(v); // row_shr:4
+    v = dpp_add64<0x118, 0xf>(v); // row_shr:8
+    v = dpp_add64<0x142, 0xa>(v); // row_bcast:15 -> rows 1, 3
+    v = dpp_add64<0x143, 0xc>(v); // row_bcast:31 -> rows 2, 3
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)b, 63);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(b >> 32), 63);
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+
 // Words that workgroups on different compute dies share within a launch.
 __device__ __forceinline__ void store_shared(double* p, double v)
 {
@@ -69,14 +97,6 @@ struct Join {
     float* loss;
     int accum;
     __device__ __forceinline__ void put(size_t row, double v) const { store_shared(row_loss + row, v); }
-    // Sum over a wave, in every lane.
-    static __device__ __forceinline__ double total(double v)
-    {
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1)
-            v += __shfl_xor(v, m);
-        return v;
-    }
     // By every lane of the wave whose lane 0 has put the row's loss.
     __device__ __forceinline__ unsigned arrive(uint32_t row) const
     {
@@ -92,7 +112,7 @@ struct Join {
         const uint32_t size = rows - first < kJoinGroup ? rows - first : kJoinGroup;
         if (__builtin_amdgcn_readfirstlane(before) != size - 1)
             return;
-        double sum = total(lane < size ? load_shared(row_loss + first + lane) : 0.0);
+        double sum = wave_sum64(lane < size ? load_shared(row_loss + first + lane) : 0.0);
         if (lane == 0)
             clear_shared(count + (1 + g) * kCountStride);
         const uint32_t groups = (rows + kJoinGroup - 1) / kJoinGroup;
@@ -110,7 +130,7 @@ struct Join {
 #pragma unroll
             for (uint32_t k = 0; k < kJoinGroups / kWave; ++k)
                 sum += v[k];
-            sum = total(sum);
+            sum = wave_sum64(sum);
             if (lane == 0)
                 clear_shared(count);
         }

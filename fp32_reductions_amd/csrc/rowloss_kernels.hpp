@@ -771,14 +771,6 @@ __device__ __forceinline__ uint32_t list_length(const typename Op::Args& a)
 // order of the vectors, and one word for the elements outside.
 inline __host__ __device__ uint32_t bitmap_words(uint32_t V) { return (V + 31) / 32 + 1; }
 
-__device__ __forceinline__ double wave_sum64(double v)
-{
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1)
-        v += __shfl_xor(v, m);
-    return v;
-}
-
 // LDS written by one lane of a wave and read by another of the same wave.
 __device__ __forceinline__ void wave_lds_fence()
 {
@@ -886,10 +878,7 @@ struct ListReader {
     __device__ __forceinline__ void end()
     {
         use();
-        uint32_t n = listed;
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1)
-            n += __shfl_xor(n, m);
+        uint32_t n = (uint32_t)wave_reduce<OpSum>((float)listed);
         n |= __any(again) ? 0x80000000u : 0u;
         if (lane == 0)
             l.marked[wave] = n;

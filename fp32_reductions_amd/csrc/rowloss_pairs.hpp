@@ -180,8 +180,8 @@ struct PairJoin {
         }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            sum[side] = Join::total(sum[side]);
-            count[side] = Join::total(count[side]);
+            sum[side] = wave_sum64(sum[side]);
+            count[side] = wave_sum64(count[side]);
         }
         const PairResult result(a, values, sum, count);
         if (lane == 0)
