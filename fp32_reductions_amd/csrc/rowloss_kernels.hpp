@@ -1240,7 +1240,7 @@ __global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint
 //
 // A segment of GT * NV vectors of a row per group of threads: nothing is
 // reduced, so rows are cut as finely as the device wants.  One read and one
-// write: 4096 rows of 131072 bf16 in 354 us, 6.1 TB/s.
+// write: 4096 rows of 131072 bf16 in 337 us, 6.4 TB/s.
 
 // Gradient of the log-probability (glogp) and the entropy (gentropy):
 //   dz = scale (g (delta_vy - p) - h p (ln p + H)),  ln p = scale z - lse.
@@ -1248,6 +1248,7 @@ __global__ __launch_bounds__(256) void split_kernel(const typename T::S* z, uint
 template <bool ENT>
 struct LogprobGradOp {
     static constexpr bool kEntropy = ENT;
+    static constexpr int kPieceVecs = 2;
     struct Args {
         const int64_t* targets;
         const float *lse, *entropy, *glogp, *gentropy;
@@ -1286,6 +1287,7 @@ struct LogprobGradOp {
 // Second pass of the preference loss: the row's slope times d logp / dz.
 struct PreferenceGradOp {
     static constexpr bool kEntropy = false;
+    static constexpr int kPieceVecs = 2;
     struct Args {
         const int64_t* targets;
         const float2* stat;
@@ -1317,6 +1319,7 @@ struct PreferenceGradOp {
 template <bool ENT>
 struct SplitGradOp {
     static constexpr bool kEntropy = ENT;
+    static constexpr int kPieceVecs = 4;
     struct Args {
         const int64_t* targets;
         const RowSlope* slope;
@@ -1521,21 +1524,29 @@ hipError_t each_part(size_t rows, size_t most, hipStream_t stream, F f)
     return hipSuccess;
 }
 
-constexpr int kGradVecs = 4; // vectors per thread of the gradient kernel
+// Vectors per thread of the gradient kernel: four where a row fits a
+// workgroup so, two in the pieces of a longer one (us for 4096 rows, four and
+// two: bf16, V = 6598 21.0 and 23.0, 9802 35.4 and 29.4, 131072 348 and 334;
+// f32, 131072 725 and 701; eight lose at 20000, 56 and 74).  Of few rows, whose
+// slopes a kernel before has left, four (64 rows of 131072 bf16, policy loss:
+// 13.7 and 15.2).
+constexpr int kGradVecs = 4;
 
 // Workgroups per row of the gradient kernel; 0: several rows per workgroup.
-template <class T>
+template <class T, class Op>
 uint32_t grad_segments(const Logits& m)
 {
-    const size_t nvec = (m.V + T::W - 1) / T::W, per = 256 * kGradVecs;
-    return nvec <= 64 * kGradVecs ? 0 : (uint32_t)((nvec + per - 1) / per);
+    const size_t nvec = (m.V + T::W - 1) / T::W, per = 256 * Op::kPieceVecs;
+    if (nvec <= 64 * kGradVecs)
+        return 0;
+    return nvec <= 256 * kGradVecs ? 1 : (uint32_t)((nvec + per - 1) / per);
 }
 
 // Rows of one launch of the gradient kernel: at most 2^32 - 1 work-items.
-template <class T>
+template <class T, class Op>
 size_t grad_rows_per_launch(const Logits& m)
 {
-    const size_t segs = grad_segments<T>(m) ? grad_segments<T>(m) : 1;
+    const size_t segs = grad_segments<T, Op>(m) ? grad_segments<T, Op>(m) : 1;
     const size_t fit = ((size_t(1) << 24) - 1) / segs;
     return fit < kRowsPerLaunch ? fit : kRowsPerLaunch;
 }
@@ -1547,12 +1558,15 @@ void launch_grad(const Logits& m, const Part& p, const typename Op::Args& args)
     const S* z = static_cast<const S*>(m.z) + p.row0 * m.ld;
     S* dz = static_cast<S*>(m.dz) + p.row0 * m.ldd;
     const float c = exponent_scale(m.scale);
-    const uint32_t segs = grad_segments<T>(m);
+    const uint32_t segs = grad_segments<T, Op>(m);
     if (!segs)
         hipLaunchKernelGGL((grad_kernel<T, 64, kGradVecs, Op>), dim3((p.rows + 3) / 4), dim3(256),
                            0, p.stream, z, dz, p.rows, (uint32_t)m.V, 1u, m.ld, m.ldd, c, args);
+    else if (segs == 1)
+        hipLaunchKernelGGL((grad_kernel<T, 256, kGradVecs, Op>), dim3(p.rows), dim3(256), 0,
+                           p.stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
     else
-        hipLaunchKernelGGL((grad_kernel<T, 256, kGradVecs, Op>), dim3(p.rows * segs), dim3(256), 0,
+        hipLaunchKernelGGL((grad_kernel<T, 256, Op::kPieceVecs, Op>), dim3(p.rows * segs), dim3(256), 0,
                            p.stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
 }
 
@@ -1594,7 +1608,7 @@ hipError_t RowLoss<T>::logprob_grad(const LogprobGradCall& a, const DeviceInfo&,
                                     hipStream_t stream)
 {
     using namespace rowloss;
-    return each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
+    return each_part(a.m.rows, grad_rows_per_launch<T, LogprobGradOp<true>>(a.m), stream, [&](const Part& p) {
         const size_t r = p.row0;
         const double inverse = 1.0 / (double)a.m.scale;
         if (a.gentropy)
@@ -1714,7 +1728,7 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo& dev
     if (e == hipSuccess && !joined)
         e = launch_preference_pairs(pair, stream);
     if (e == hipSuccess && a.m.dz)
-        e = each_part(a.m.rows, grad_rows_per_launch<T>(a.m), stream, [&](const Part& p) {
+        e = each_part(a.m.rows, grad_rows_per_launch<T, PreferenceGradOp>(a.m), stream, [&](const Part& p) {
             const size_t r = p.row0;
             launch_grad<T, PreferenceGradOp>(a.m, p, {a.targets + r, stat + r, slope + r});
         });
