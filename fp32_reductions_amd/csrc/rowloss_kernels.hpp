@@ -1475,7 +1475,9 @@ void launch_split(const Logits& m, const Part& p, const typename Op::Args& args,
 // or 1024 threads, which take their row through faster (policy loss, bf16, us
 // a call for 256 rows and for 1024 rows: V = 4096: 64 threads 8.2 and 9.1, 256
 // threads 7.1 and 9.7; V = 32768: 256 threads 12.4 and 26.5, 1024 threads 10.1
-// and 30.4; V = 65536: 512 threads 16.7 and 50, 1024 threads 15.7 and 59).
+// and 30.4; V = 65536: 512 threads 16.7 and 50, 1024 threads 15.7 and 59).  Slots past the row's
+// end cost their loads, so short rows have half the slots (8000 rows of 1900
+// bf16, 64 threads: eight vectors 18.8, four 16.1).
 template <class T, class Op>
 void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& args, size_t lds,
                     const DeviceInfo& dev)
@@ -1490,10 +1492,12 @@ void launch_rows_op(const Logits& m, const Part& p, const typename Op::Args& arg
             launch_rows_as<T, 256, 4, true, false, Op>(m, p, args, lds);
     } else if constexpr (Op::kHasGrad) {
         const bool few = p.rows <= (uint32_t)dev.cus;
-        if (few && nvec > 256 && nvec <= 256 * 4)
-            launch_rows_as<T, 256, 4, false, true, Op>(m, p, args, lds);
-        else if (nvec <= 64 * 8)
+        if (nvec <= 64 * 4)
+            launch_rows_as<T, 64, 4, false, true, Op>(m, p, args, lds);
+        else if (!few && nvec <= 64 * 8)
             launch_rows_as<T, 64, 8, false, true, Op>(m, p, args, lds);
+        else if (nvec <= 256 * 4)
+            launch_rows_as<T, 256, 4, false, true, Op>(m, p, args, lds);
         else if (few && nvec <= 1024 * 4)
             launch_rows_as<T, 1024, 4, false, true, Op>(m, p, args, lds);
         else if (nvec <= 256 * 8)
