@@ -22,7 +22,9 @@
 // Statistics are fp32 per thread (sums of at most a few hundred terms, then
 // a tree); what is computed once per row (logarithms, ratios, losses) is
 // fp64, so that a sum of thousands of log-probabilities keeps its last bits.
-// Terms below 2^-126 of a row's largest count as zero (v_exp_f32).
+// Terms below 2^-126 of a row's largest count as zero (v_exp_f32); where a
+// result rests on some columns alone (distillation's rest) they are summed
+// against their own largest.
 //
 // Determinism: no atomics on results; every sum has a fixed order.
 #pragma once
@@ -233,8 +235,10 @@ __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.
 constexpr float kWideShift = 1048576.0f; // delta below 2^-4
 __device__ __forceinline__ bool is_wide(float shift) { return !(fabsf(shift) < kWideShift); }
 
-// What a term of the sums leaves out: nothing, or the columns of a bitmap
-// with one bit per element and W bits per vector.
+// What the statistics leave out: nothing, or the columns of a bitmap with one
+// bit per element and W bits per vector.  They are left out of the maximum
+// too: a listed logit 90 above all others would take every other term below
+// 2^-126 of itself, and the columns outside would have no sum of their own.
 struct TakeAll {
     static constexpr bool kSome = false;
     __device__ __forceinline__ unsigned skip(uint32_t) const { return 0; }
@@ -254,12 +258,25 @@ struct TakeUnmarked {
     __device__ __forceinline__ bool skip_one(uint32_t t) const { return (singles >> t) & 1; }
 };
 
-// Folds the NG vectors first + k GT + t and the single element `one` into st:
-// first the maximum, then the sums against it.
-template <class T, int GT, int NG, bool ENT, class Take>
+// Elements with a bit in `skip` become -inf, which adds nothing to any
+// statistic.
+template <class T>
+__device__ __forceinline__ void drop(u32x4_t& v, unsigned skip)
+{
+    constexpr int kPerWord = T::W / 4;
+#pragma unroll
+    for (int i = 0; i < T::W; ++i) {
+        const unsigned lanes = kPerWord == 1 ? 0xffffffffu : 0xffffu << (i % kPerWord * 16);
+        const unsigned mask = (skip >> i) & 1 ? lanes : 0u;
+        v[i / kPerWord] = (v[i / kPerWord] & ~mask) | (T::kNegInf & mask);
+    }
+}
+
+// Folds the NG vectors first + k GT + t and the single element `one` (-inf:
+// none) into st: first the maximum, then the sums against it.
+template <class T, int GT, int NG, bool ENT>
 __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t first, uint32_t nvec,
-                                           uint32_t t, float one, bool skip_one, float c,
-                                           const Take& take, Stat& st)
+                                           float one, bool skip_one, float c, Stat& st)
 {
     constexpr int W = T::W;
     float m0 = fmaxf(st.m, one), m1 = -INFINITY;
@@ -275,12 +292,6 @@ __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t firs
             m1 = fmaxf(fmaxf(m1, f[i + 2]), f[i + 3]);
         }
     }
-    unsigned skips[NG];
-    if constexpr (Take::kSome) {
-#pragma unroll
-        for (int k = 0; k < NG; ++k)
-            skips[k] = take.skip(first + k * GT + t);
-    }
     const float m = fmaxf(m0, m1);
     const float ref = reference(m), mc = ref * c;
     // What was summed against the old maximum moves to the new one.
@@ -294,15 +305,6 @@ __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t firs
                 break;
             float f[W];
             T::unpack(v[k], f);
-            if constexpr (Take::kSome) {
-                if (__builtin_amdgcn_ballot_w64(skips[k] != 0)) {
-                    asm volatile(""); // a branch that few waves take, not selects for all
-#pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        if ((skips[k] >> i) & 1)
-                            f[i] = -INFINITY;
-                }
-            }
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 const float x = exponent(f[i]), e = exp2_fast(x);
@@ -331,10 +333,12 @@ __device__ __forceinline__ void fold_group(const u32x4_t (&v)[NG], uint32_t firs
 }
 
 // Folds a chunk of NV vectors and one single element, kFold vectors at a
-// time: while the first are folded the others are still on their way.
+// time: while the first are folded the others are still on their way.  What
+// `take` leaves out is -inf in v afterwards: the gradient of those columns is
+// written from elsewhere.
 constexpr int kFold = 8;
 template <class T, int GT, int NV, bool ENT, class Take>
-__device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t first, uint32_t nvec,
+__device__ __forceinline__ void fold_chunk(u32x4_t (&v)[NV], uint32_t first, uint32_t nvec,
                                            uint32_t t, float one, bool skip_one, float c,
                                            const Take& take, Stat& st)
 {
@@ -344,12 +348,24 @@ __device__ __forceinline__ void fold_chunk(const u32x4_t (&v)[NV], uint32_t firs
     for (int g = 0; g < NV; g += NG) {
         if (g && first + g * GT >= nvec)
             break;
+        if constexpr (Take::kSome) {
+            unsigned skips[NG];
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+                skips[k] = take.skip(first + (g + k) * GT + t);
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+                if (__builtin_amdgcn_ballot_w64(skips[k] != 0)) {
+                    asm volatile(""); // a branch that few waves take, not selects for all
+                    drop<T>(v[g + k], skips[k]);
+                }
+        }
         u32x4_t part[NG];
 #pragma unroll
         for (int k = 0; k < NG; ++k)
             part[k] = v[g + k];
-        fold_group<T, GT, NG, ENT>(part, first + g * GT, nvec, t, g ? -INFINITY : one,
-                                   g ? true : skip_one, c, take, st);
+        fold_group<T, GT, NG, ENT>(part, first + g * GT, nvec, g || skip_one ? -INFINITY : one,
+                                   g ? true : skip_one, c, st);
     }
 }
 
@@ -736,9 +752,10 @@ struct TeacherLds {
     int* col;
     float* q;
     float* z;
-    double* cross; // sum q (ln q - scale (z - ref)), ref the largest logit listed
+    double* cross; // sum q (ln q - scale (z - ref)), ref the reference of the largest logit listed
     double* sum;   // Q
-    int* state;    // [0]: the row has a teacher; [1]: ref
+    int* state;    // [0]: the row has a teacher; [1]: the largest logit listed;
+                   // [2], [3]: the whole row's reference and sum
     uint32_t* marked; // of each wave: the columns it marked; the high bit: one of them twice
     static constexpr size_t kHead = 32 + 16 * 4;
     static __host__ __device__ size_t bytes(size_t words, size_t K)
@@ -891,11 +908,12 @@ struct ListReader {
 template <class T, bool TAIL>
 __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Args& a,
                                               const typename DistillOp<TAIL>::Row& r,
-                                              float top, float ref, uint32_t lane,
+                                              float top, float top_z, uint32_t lane,
                                               const TeacherLds& l)
 {
     top = wave_reduce<OpMax>(top);
-    ref = reference(wave_reduce<OpMax>(ref));
+    top_z = wave_reduce<OpMax>(top_z);
+    const float ref = reference(top_z);
     wave_lds_fence();
     const double scale = a.scale;
     double shift, first_q = 0.0; // first_q: the probability of this lane's first entry
@@ -931,7 +949,7 @@ __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Ar
         *l.sum = sum;
         *l.cross = cross;
         l.state[0] = TAIL || top != -INFINITY;
-        l.state[1] = __float_as_int(ref);
+        l.state[1] = __float_as_int(top_z);
     }
     wave_lds_fence();
 }
@@ -1078,25 +1096,33 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
                 __syncthreads();
         }
         const double Q = *l.sum;
-        double rest = 0.0, outside = st.s;
+        const float top_z = __int_as_float(l.state[1]);
+        // Of the whole row: the largest logit and the sum against it.  With the
+        // rest, st holds the columns outside alone, against their own maximum.
+        const float top = Op::kTail ? fmaxf(st.m, top_z) : st.m;
+        const Exponent whole(reference(top), c);
+        float total = st.s, shrink = 1.0f; // shrink: from their maximum to the row's
+        double rest = 0.0;
+        const double outside = st.s;
         if constexpr (Op::kTail) {
             float in = 0.0f;
             for (uint32_t k = t & 63; k < args.K; k += kWave)
                 if (l.col[k] >= 0)
-                    in += exp2_fast(ex.at(l.z[k]));
+                    in += exp2_fast(whole.at(l.z[k]));
             in = wave_reduce<OpSum>(in);
-            st.s += in;
+            shrink = exp2_fast(fmaxf(whole.at(st.m), kLowest));
+            total = fmaf(st.s, shrink, in);
             if (listed < V && Q < 1.0)
                 rest = 1.0 - Q;
         }
         if (t < kWave) {
             // Lanes 0, 1 and 2 take the three logarithms at once.
-            const double ln = log(t == 0 ? (double)st.s : t == 1 ? rest : outside);
+            const double ln = log(t == 0 ? (double)total : t == 1 ? rest : outside);
             const double ln_s = __shfl(ln, 0), ln_rest = __shfl(ln, 1), ln_out = __shfl(ln, 2);
-            const double ref = __int_as_float(l.state[1]), scale = args.scale;
-            double loss = *l.cross + Q * (((double)reference(st.m) - ref) * scale + ln_s);
-            if (Op::kTail && rest > 0.0)
-                loss += rest * (ln_rest - ln_out + ln_s);
+            const double ref = reference(top_z), scale = args.scale, most = reference(top);
+            double loss = *l.cross + Q * ((most - ref) * scale + ln_s);
+            if (Op::kTail && rest > 0.0) // ln p_r: by logits, however far below the row's largest
+                loss += rest * (ln_rest - (ln_out + ((double)st.m - most) * scale - ln_s));
             if (leader) {
                 args.join.put(row, (double)r.weight * loss);
                 if (args.row_loss_out)
@@ -1105,10 +1131,16 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         }
         factor = r.weight * args.scale;
         mass = (float)(Q + rest);
-        double a = (Q + rest) / (double)st.s;
+        // Against the maximum of st: the gradient of the columns outside is
+        // p_v (Q + q_r) less their share of q_r, which does not shrink with p_v.
+        double a = (Q + rest) * (double)shrink / (double)total;
         if (Op::kTail && outside > 0.0)
             a -= rest / outside;
         slope = {(float)((double)factor * a), 0.0f};
+        if (leader) { // for the columns listed, after the others are written
+            l.state[2] = __float_as_int(whole.ref);
+            l.state[3] = __float_as_int(total);
+        }
     } else {
         slope = Op::done(args, r, row, st, zy, leader, fix);
     }
@@ -1129,10 +1161,14 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         if constexpr (Op::kList) {
             if constexpr (GT > kWave)
                 __syncthreads();
+            else
+                wave_lds_fence();
+            const Exponent whole(__int_as_float(l.state[2]), c);
+            const float total = __int_as_float(l.state[3]);
             for (uint32_t k = t; k < args.K; k += GT)
                 if (l.col[k] >= 0)
                     dr[l.col[k]] = T::narrow(
-                        factor * (exp2_fast(ex.at(l.z[k])) / st.s * mass - l.q[k]));
+                        factor * (exp2_fast(whole.at(l.z[k])) / total * mass - l.q[k]));
         } else {
             uint32_t owner = 0;
             if (r.y >= sp.head && r.y < sp.tail)

@@ -309,7 +309,8 @@ int red_colprod_u32(const uint32_t* src, size_t R, size_t C, size_t ld,
  * Logits are widened exactly to fp32.  A thread's statistics are fp32, what
  * is computed once per row and the sums over rows are fp64, and every result
  * is rounded once to its type.  A term below 2^-126 of its row's largest
- * counts as 0.  Logits of -inf have probability 0.  A row with a NaN or +inf,
+ * counts as 0 (in the sum of a distilled row's columns that are not listed: of
+ * the largest among these).  Logits of -inf have probability 0.  A row with a NaN or +inf,
  * or with nothing but -inf, has NaN results unless it does not count; its
  * neighbours are not touched by it.  A row filled with one finite value is
  * uniform, the type's lowest value included.

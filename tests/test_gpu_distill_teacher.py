@@ -1,0 +1,93 @@
+"""Distillation where the teacher or the student is far from ordinary: a
+student whose listed logits lead all others so far that no other term is left
+beside them, and the columns not listed without any probability."""
+import math
+
+import pytest
+
+import rowloss_reference as ref
+from gpu_helpers import say
+from test_gpu_rowloss import DTYPES, draw, f32, run_distill
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+# Columns: a row held by a wave, by a workgroup, and one longer than that.
+COLUMNS = [9, 1200, 6000, 150000]
+
+
+@pytest.fixture(scope="module")
+def red():
+    import fp32_reductions_amd
+    return fp32_reductions_amd
+
+
+def lists(n, V, K, g):
+    return torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(n)])
+
+
+def teacher_with_rest(val, scale, rest):
+    """The log-sum-exp of a teacher whose entries leave `rest` to the others."""
+    return ((val.double() * scale).logsumexp(1) - torch.log1p(-rest.double())).float()
+
+
+@pytest.mark.parametrize("t", DTYPES)
+@pytest.mark.parametrize("V", COLUMNS)
+def test_listed_logits_far_above_the_rest(red, V, t):
+    """Every term outside the list is below 2^-126 of the row's largest; the
+    rest's loss and gradient are those among the columns outside."""
+    say("leading list V=%d %s" % (V, t))
+    n, K = 7, 4
+    g, z, _ = draw(n, V, t, V + 1, std=1.0)
+    idx = lists(n, V, K, g)
+    idx[4, 2] = -1
+    for r, lead in enumerate((100.0, 150.0, 600.0, 90.0, 200.0, 120.0)):
+        z[r, idx[r, 0]] = lead
+    z[2, idx[2, 1:3]] = 599.0
+    z[5, V // 2:] -= 150.0
+    z[5, idx[5, 0]] = 120.0
+    val = torch.randn(n, K, generator=g)
+    rest = torch.tensor([0.1, 0.5, 1e-3, 0.9, 0.25, 0.1, 0.3])
+    listed = torch.where(idx >= 0, val, torch.full_like(val, -math.inf))
+    w = torch.rand(n, generator=g) + 0.5
+    for scale in (1.0, 0.9):
+        lse = teacher_with_rest(listed, scale, rest)
+        run_distill(red, z, idx, val, t, scale, w, lse)
+        run_distill(red, z, idx, val, t, scale, w, lse, grad=False)
+        run_distill(red, z, idx, val, t, scale, w, lse, shift=1, pad=3, in_place=True)
+
+
+@pytest.mark.parametrize("t", DTYPES)
+@pytest.mark.parametrize("V", COLUMNS)
+def test_a_real_rest_without_columns(red, V, t):
+    """A rest that is more than rounding: infinite where the student has
+    masked the columns outside, and -ln p_r of it where it has them lowest."""
+    say("a rest of masked columns V=%d %s" % (V, t))
+    low = torch.finfo(DTYPES[t]).min
+    n, K = 4, 3
+    g, z, _ = draw(n, V, t, V + 3)
+    idx = lists(n, V, K, g)
+    keep = torch.zeros(n, V, dtype=torch.bool).scatter_(1, idx, True)
+    z[:2][~keep[:2]] = -math.inf
+    z[2:3][~keep[2:3]] = low
+    val = torch.randn(n, K, generator=g)
+    rest = torch.tensor([0.25, 1e-4, 0.25, 0.25])
+    lse = teacher_with_rest(val, 1.0, rest)
+    w = torch.ones(n)
+    loss, row_loss, dz = f32(1), f32(n), torch.full_like(z, 7.0).cuda()
+    getattr(red, "distill_topk_" + t)(z.cuda(), idx.cuda(), val.cuda(), loss, dlogits=dz,
+                                      teacher_lse=lse.cuda(), weight=w.cuda(), row_loss=row_loss)
+    want = ref.distill_topk(z, idx, val, 1.0, w, lse)
+    assert (want["row_loss"][0][:2] == math.inf).all() and loss.item() == math.inf
+    ref.check("row_loss", row_loss, *want["row_loss"])
+    some = torch.tensor([0, 1, 3])
+    ref.check("dlogits", dz.cpu()[some], want["dlogits"][0][some], want["dlogits"][1][some])
+    # Equal logits outside share the rest's gradient.  The sum of V equal terms
+    # and its reciprocal, and the rounding of the result.
+    d = dz.cpu()[2].double()
+    q = (val[2].double() - lse[2].double()).exp()
+    share = -(1 - q.sum()) / (V - K)
+    bound = share.abs() * ref.stat_error(V) + ref.round_bound(share, z.dtype)
+    assert (d[~keep[2]] - share).abs().max() <= bound
+    ref.check("listed", d[idx[2]], want["dlogits"][0][2][idx[2]], want["dlogits"][1][2][idx[2]])
