@@ -744,6 +744,14 @@ struct DistillOp {
     static __device__ __forceinline__ Join join(const Args& a, const Row&) { return a.join; }
 };
 
+// What rounding can leave of 1 - Q where the teacher has nothing outside its
+// list: teacher_lse is an fp32 number (2^-24 of itself) from a sum of up to V
+// exponentials, and comes in as sixteen such steps at most.  Where the student
+// has nothing there either (masked columns: e^x is 0 even in fp64, for the
+// largest of them against the row's largest), such a rest counts as 0, and not
+// as infinitely far from the student.
+constexpr double kRestRounding = 0x1p-20, kNoTerm = -745.2;
+
 // A row's teacher in LDS: its columns (-1: padding; the high bit marks the
 // later ones of a column listed more than once), probabilities, the logits
 // in those columns, and a bit for each listed column.
@@ -754,8 +762,7 @@ struct TeacherLds {
     float* z;
     double* cross; // sum q (ln q - scale (z - ref)), ref the reference of the largest logit listed
     double* sum;   // Q
-    int* state;    // [0]: the row has a teacher; [1]: the largest logit listed;
-                   // [2], [3]: the whole row's reference and sum
+    int* state;    // [0]: the row has a teacher; [1]: the largest logit listed
     uint32_t* marked; // of each wave: the columns it marked; the high bit: one of them twice
     static constexpr size_t kHead = 32 + 16 * 4;
     static __host__ __device__ size_t bytes(size_t words, size_t K)
@@ -787,6 +794,20 @@ __device__ __forceinline__ uint32_t list_length(const typename Op::Args& a)
 // Words of the bitmap of V columns: a bit for each element of a vector, in the
 // order of the vectors, and one word for the elements outside.
 inline __host__ __device__ uint32_t bitmap_words(uint32_t V) { return (V + 31) / 32 + 1; }
+
+// A value that is the same in all lanes of a wave, in scalar registers: a row's
+// few fp64 numbers beside its vectors would cost a wave per SIMD.
+__device__ __forceinline__ float uniform(float v)
+{
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
+__device__ __forceinline__ double uniform(double v)
+{
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((int)(unsigned)b);
+    const unsigned hi = __builtin_amdgcn_readfirstlane((int)(unsigned)(b >> 32));
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
 
 // LDS written by one lane of a wave and read by another of the same wave.
 __device__ __forceinline__ void wave_lds_fence()
@@ -1078,8 +1099,12 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
 
     Slope slope;
     float fix = 0.0f, factor = 0.0f, mass = 0.0f;
+    float listed_ref = 0.0f, listed_sum = 0.0f; // for the columns listed
     if constexpr (Op::kList) {
-        if (!l.state[0]) { // no teacher: the row does not count
+        const int taught = l.state[0];
+        const float top_z = __int_as_float(l.state[1]);
+        const double Q = uniform(*l.sum);
+        if (!taught) { // no teacher: the row does not count
             dead_row();
             return;
         }
@@ -1095,8 +1120,6 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             if constexpr (GT > kWave)
                 __syncthreads();
         }
-        const double Q = *l.sum;
-        const float top_z = __int_as_float(l.state[1]);
         // Of the whole row: the largest logit and the sum against it.  With the
         // rest, st holds the columns outside alone, against their own maximum.
         const float top = Op::kTail ? fmaxf(st.m, top_z) : st.m;
@@ -1114,6 +1137,10 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
             total = fmaf(st.s, shrink, in);
             if (listed < V && Q < 1.0)
                 rest = 1.0 - Q;
+            if (rest <= kRestRounding * (1.0 + fabs((double)r.teacher_lse)) &&
+                ((double)st.m - (double)reference(top)) * (double)args.scale < kNoTerm)
+                rest = 0.0;
+            rest = uniform(rest);
         }
         if (t < kWave) {
             // Lanes 0, 1 and 2 take the three logarithms at once.
@@ -1137,10 +1164,8 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         if (Op::kTail && outside > 0.0)
             a -= rest / outside;
         slope = {(float)((double)factor * a), 0.0f};
-        if (leader) { // for the columns listed, after the others are written
-            l.state[2] = __float_as_int(whole.ref);
-            l.state[3] = __float_as_int(total);
-        }
+        listed_ref = uniform(whole.ref);
+        listed_sum = uniform(total);
     } else {
         slope = Op::done(args, r, row, st, zy, leader, fix);
     }
@@ -1161,14 +1186,11 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         if constexpr (Op::kList) {
             if constexpr (GT > kWave)
                 __syncthreads();
-            else
-                wave_lds_fence();
-            const Exponent whole(__int_as_float(l.state[2]), c);
-            const float total = __int_as_float(l.state[3]);
+            const Exponent whole(listed_ref, c);
             for (uint32_t k = t; k < args.K; k += GT)
                 if (l.col[k] >= 0)
                     dr[l.col[k]] = T::narrow(
-                        factor * (exp2_fast(whole.at(l.z[k])) / total * mass - l.q[k]));
+                        factor * (exp2_fast(whole.at(l.z[k])) / listed_sum * mass - l.q[k]));
         } else {
             uint32_t owner = 0;
             if (r.y >= sp.head && r.y < sp.tail)

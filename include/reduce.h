@@ -363,7 +363,10 @@ int red_token_logprob_grad_bf16(const uint16_t* logits, size_t rows, size_t V, s
  * exp(s val_k - teacher_lse), and the columns not listed, with the teacher's
  * rest q_r = 1 - sum q and the student's p_r = their sum of p, count as one:
  *   row loss = sum_k q_k (ln q_k - ln p_{idx_k}) + q_r (ln q_r - ln p_r).
- * The rest is 0 where sum q >= 1 or every column is listed.
+ * The rest is 0 where sum q >= 1 or every column is listed, and where the
+ * columns outside are masked (s z more than 745.2 below the row's largest:
+ * nothing even in double precision) and 1 - sum q is no more than the rounding
+ * of teacher_lse, (1 + |teacher_lse|) 2^-20.
  *
  * An entry of probability 0 adds nothing.  Each entry of a column listed
  * more than once counts.  row_loss, where not NULL, takes the rows' losses

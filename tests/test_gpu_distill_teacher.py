@@ -58,6 +58,40 @@ def test_listed_logits_far_above_the_rest(red, V, t):
         run_distill(red, z, idx, val, t, scale, w, lse, shift=1, pad=3, in_place=True)
 
 
+def compact(z, idx):
+    """The listed columns of every row alone, with entry k in column k."""
+    return z.gather(1, idx), torch.arange(idx.shape[1]).repeat(z.shape[0], 1)
+
+
+@pytest.mark.parametrize("t", DTYPES)
+@pytest.mark.parametrize("V", COLUMNS)
+@pytest.mark.parametrize("lowest", [False, True])
+def test_rounding_of_a_rest_without_columns(red, V, t, lowest):
+    """The teacher lists every column that the student's mask leaves.  1 - Q is
+    then what rounding left of the teacher's log-sum-exp, and no rest."""
+    say("no columns outside V=%d %s %s" % (V, t, lowest))
+    n, K = 24, 5
+    mask = torch.finfo(DTYPES[t]).min if lowest else -math.inf
+    g, z, _ = draw(n, V, t, V + 2)
+    idx = lists(n, V, K, g)
+    keep = torch.zeros(n, V, dtype=torch.bool).scatter_(1, idx, True)
+    z[~keep] = mask
+    val = torch.randn(n, K, generator=g) * 3 + 9.0
+    lse = val.double().logsumexp(1).float()
+    missing = 1 - (val.double() - lse.double().unsqueeze(1)).exp().sum(1)
+    assert (missing > 0).sum() > 3 and (missing < 0).sum() > 3
+    w = torch.rand(n, generator=g) + 0.5
+    loss, row_loss, dz = f32(1), f32(n), torch.full_like(z, 7.0).cuda()
+    getattr(red, "distill_topk_" + t)(z.cuda(), idx.cuda(), val.cuda(), loss, dlogits=dz,
+                                      teacher_lse=lse.cuda(), weight=w.cuda(), row_loss=row_loss)
+    few, at = compact(z, idx)
+    want = ref.distill_topk(few, at, val, 1.0, w, lse)  # every column listed: no rest
+    ref.check("loss", loss, want["loss"][0].reshape(1), want["loss"][1])
+    ref.check("row_loss", row_loss, *want["row_loss"])
+    ref.check("dlogits", dz.cpu().gather(1, idx), *want["dlogits"])
+    assert not dz.cpu()[~keep].any()
+
+
 @pytest.mark.parametrize("t", DTYPES)
 @pytest.mark.parametrize("V", COLUMNS)
 def test_a_real_rest_without_columns(red, V, t):
