@@ -835,6 +835,7 @@ struct ListReader {
     uint32_t V, K, words, wave, lane;
     uint32_t k0 = 0, listed = 0;
     bool again = false;
+    bool taught = false; // first wave: this lane has an entry above -inf, or a NaN
     float top_val = -INFINITY, top_z = -INFINITY; // first wave: this lane's largest
     int64_t at[kBatch];
     float v[kBatch];
@@ -883,6 +884,7 @@ struct ListReader {
                     l.q[k] = value;
                     l.z[k] = logit;
                 }
+                taught |= !(value == -INFINITY);
                 top_val = fmaxf(top_val, value);
                 top_z = fmaxf(top_z, logit);
             }
@@ -929,9 +931,10 @@ struct ListReader {
 template <class T, bool TAIL>
 __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Args& a,
                                               const typename DistillOp<TAIL>::Row& r,
-                                              float top, float top_z, uint32_t lane,
-                                              const TeacherLds& l)
+                                              bool taught, float top, float top_z,
+                                              uint32_t lane, const TeacherLds& l)
 {
+    taught = __any(taught);
     top = wave_reduce<OpMax>(top);
     top_z = wave_reduce<OpMax>(top_z);
     const float ref = reference(top_z);
@@ -969,7 +972,7 @@ __device__ __forceinline__ void weigh_teacher(const typename DistillOp<TAIL>::Ar
     if (lane == 0) {
         *l.sum = sum;
         *l.cross = cross;
-        l.state[0] = TAIL || top != -INFINITY;
+        l.state[0] = TAIL || taught;
         l.state[1] = __float_as_int(top_z);
     }
     wave_lds_fence();
@@ -1083,7 +1086,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     if constexpr (Op::kList) {
         list.end();
         if (t < kWave)
-            weigh_teacher<T, Op::kTail>(args, r, list.top_val, list.top_z, t, l);
+            weigh_teacher<T, Op::kTail>(args, r, list.taught, list.top_val, list.top_z, t, l);
         if constexpr (Op::kTail) {
             const TakeUnmarked<T::W> take{l.bits, sp.nvec, has_one ? l.bits[words - 1] : 0u};
             fold_row(has_one && take.skip_one(t), take);

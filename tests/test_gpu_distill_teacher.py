@@ -1,6 +1,7 @@
 """Distillation where the teacher or the student is far from ordinary: a
 student whose listed logits lead all others so far that no other term is left
-beside them, and the columns not listed without any probability."""
+beside them, and the columns not listed without any probability; teachers with
+NaN among their entries."""
 import math
 
 import pytest
@@ -125,3 +126,34 @@ def test_a_real_rest_without_columns(red, V, t):
     bound = share.abs() * ref.stat_error(V) + ref.round_bound(share, z.dtype)
     assert (d[~keep[2]] - share).abs().max() <= bound
     ref.check("listed", d[idx[2]], want["dlogits"][0][2][idx[2]], want["dlogits"][1][2][idx[2]])
+
+
+@pytest.mark.parametrize("t", DTYPES)
+@pytest.mark.parametrize("V", COLUMNS)
+@pytest.mark.parametrize("tail", [False, True])
+def test_nan_among_the_teachers_entries(red, V, t, tail):
+    """A teacher that gives NaN makes NaN of its own row, however many of its
+    entries are NaN; padding is not looked at, and entries of -inf alone are
+    no teacher."""
+    say("NaN teachers V=%d %s tail=%s" % (V, t, tail))
+    n, K = 7, 4
+    g, z, _ = draw(n, V, t, V + 4)
+    idx = lists(n, V, K, g)
+    val = torch.randn(n, K, generator=g)
+    val[0, :] = math.nan
+    val[1, 2] = math.nan
+    val[2, :2], val[2, 2:] = math.nan, -math.inf
+    val[3, :] = -math.inf
+    val[4, 1], idx[4, 1] = math.nan, -1
+    val[5, :], idx[5, :] = math.nan, -1
+    lse = torch.full((n,), 2.5) if tail else None
+    w = torch.rand(n, generator=g) + 0.5
+    w[6] = 0.0
+    val[6, :] = math.nan
+    bad = torch.tensor([1, 1, 1, 0, 0, 0, 0], dtype=torch.bool)
+    _, row_loss, dz = run_distill(red, z, idx, val, t, 1.0, w, lse)
+    assert torch.equal(row_loss.cpu().isnan(), bad)
+    assert dz.cpu()[bad].isnan().all() and not dz.cpu()[~bad].isnan().any()
+    # and without those rows the loss is a number
+    loss, _, _ = run_distill(red, z, idx, val, t, 1.0, torch.where(bad, 0.0, w), lse)
+    assert loss.isfinite().all()
