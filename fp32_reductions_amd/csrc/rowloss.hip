@@ -30,10 +30,11 @@ __device__ __forceinline__ double block_sum64(double v, double* lds)
 
 // One workgroup: thread t adds terms t, t + 1024, ..., four loads in flight.
 __global__ __launch_bounds__(1024) void loss_sum_kernel(const double* __restrict__ v, uint32_t n,
-                                                        float* loss, int accum)
+                                                        float* loss, int accum,
+                                                        const double* before, double* after)
 {
     __shared__ double lds[16];
-    const float old = accum ? loss[0] : 0.0f;
+    const double old = before ? before[0] : accum ? (double)loss[0] : 0.0;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     for (uint32_t i = threadIdx.x; i < n; i += 4096) {
 #pragma unroll
@@ -41,8 +42,12 @@ __global__ __launch_bounds__(1024) void loss_sum_kernel(const double* __restrict
             s[k] += i + k * 1024 < n ? v[i + k * 1024] : 0.0;
     }
     const double sum = block_sum64<16>((s[0] + s[1]) + (s[2] + s[3]), lds);
-    if (threadIdx.x == 0)
-        loss[0] = (float)((double)old + sum);
+    if (threadIdx.x != 0)
+        return;
+    if (after)
+        after[0] = old + sum;
+    else
+        loss[0] = (float)(old + sum);
 }
 
 // One workgroup per pair.  Sequence p is the chosen one and P + p the
@@ -85,10 +90,10 @@ __global__ __launch_bounds__(256) void preference_pairs_kernel(PairArgs a)
 } // namespace
 
 hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int accum,
-                           hipStream_t stream)
+                           const double* before, double* after, hipStream_t stream)
 {
     hipLaunchKernelGGL(loss_sum_kernel, dim3(1), dim3(1024), 0, stream, row_loss, (uint32_t)n,
-                       loss, accum);
+                       loss, accum, before, after);
     return hipGetLastError();
 }
 

@@ -114,7 +114,9 @@ extern template struct RowLoss<ElemF32>;
 extern template struct RowLoss<ElemF16>;
 extern template struct RowLoss<ElemBF16>;
 
-// loss[0] = [loss[0] +] sum of n row losses (rowloss.hip).
+// loss[0] = [loss[0] +] sum of n row losses (rowloss.hip).  `before` (null: 0)
+// is added in fp64; where `after` is not null the sum goes there, and not to
+// loss: of several launches that make one loss only the last rounds it.
 hipError_t launch_loss_sum(const double* row_loss, size_t n, float* loss, int accum,
-                           hipStream_t stream);
+                           const double* before, double* after, hipStream_t stream);
 } // namespace red

@@ -145,6 +145,7 @@ struct Join {
     }
 };
 static_assert((1 + kJoinGroups) * kCountStride <= kCounterWords, "a count for each group");
+static_assert(kJoinRows < kRowsPerLaunch, "a loss of several launches has no count");
 
 // For operators without a loss to join.
 struct NoJoin {
@@ -152,7 +153,9 @@ struct NoJoin {
     __device__ __forceinline__ void finish(unsigned, uint32_t, uint32_t) const {}
 };
 
-// The meeting place of `rows` losses at `row_loss` (in the workspace).
+// The meeting place of `rows` losses at `row_loss` (in the workspace).  A loss of
+// several launches has no count (its rows are more than kJoinRows): its sum
+// passes from one to the next in fp64, in the word before the groups' sums.
 inline Join join_of(const Workspace& ws, void* row_loss, size_t rows, float* loss, int accum)
 {
     return {static_cast<double*>(row_loss),
@@ -162,9 +165,14 @@ inline Join join_of(const Workspace& ws, void* row_loss, size_t rows, float* los
 }
 
 // After the launch that puts them: the sum, where no wave of it adds them up.
-inline hipError_t sum_joined(const Join& j, size_t rows, hipStream_t stream)
+// first, last: of the launches that make the loss.
+inline hipError_t sum_joined(const Join& j, size_t rows, hipStream_t stream, bool first = true,
+                             bool last = true)
 {
-    return j.count ? hipSuccess : launch_loss_sum(j.row_loss, rows, j.loss, j.accum, stream);
+    double* passed = j.group_sum - 1;
+    return j.count ? hipSuccess
+                   : launch_loss_sum(j.row_loss, rows, j.loss, j.accum, first ? nullptr : passed,
+                                     last ? nullptr : passed, stream);
 }
 
 } // namespace red

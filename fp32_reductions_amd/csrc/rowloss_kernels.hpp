@@ -1463,10 +1463,13 @@ __global__ __launch_bounds__(256) void grad_kernel(const typename T::S* z, typen
 
 // ---- launches ----------------------------------------------------------------
 
-struct Part { // rows [row0, row0 + rows) of a call, on `stream`
+struct Part { // rows [row0, row0 + rows) of the `all` of a call, on `stream`
     size_t row0;
     uint32_t rows;
     hipStream_t stream;
+    size_t all;
+    bool first() const { return row0 == 0; }
+    bool last() const { return row0 + rows == all; }
 };
 
 inline float exponent_scale(float scale) { return (float)((double)scale * kLog2e); }
@@ -1581,7 +1584,7 @@ hipError_t each_part(size_t rows, size_t most, hipStream_t stream, F f)
 {
     for (size_t row0 = 0; row0 < rows; row0 += most) {
         const size_t n = rows - row0 < most ? rows - row0 : most;
-        f(Part{row0, (uint32_t)n, stream});
+        f(Part{row0, (uint32_t)n, stream, rows});
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -1697,7 +1700,7 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo& dev, cons
     hipError_t e = hipSuccess;
     const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
         const size_t r = p.row0;
-        const Join join = join_of(ws, ws.partials, p.rows, a.loss, a.accum || r);
+        const Join join = join_of(ws, ws.partials, p.all, a.loss, a.accum);
         const float* weight = a.weight ? a.weight + r : nullptr;
         float* out = a.row_loss ? a.row_loss + r : nullptr;
         const int64_t* idx = a.idx + r * a.ldk;
@@ -1712,7 +1715,7 @@ hipError_t RowLoss<T>::distill(const DistillCall& a, const DeviceInfo& dev, cons
                                                 {idx, val, nullptr, weight, (uint32_t)a.K, a.ldk,
                                                  a.m.scale, mean, out, join},
                                                 lds, dev);
-        const hipError_t s = sum_joined(join, p.rows, stream);
+        const hipError_t s = sum_joined(join, p.rows, stream, p.first(), p.last());
         e = e == hipSuccess ? s : e;
     });
     return f == hipSuccess ? e : f;
@@ -1727,7 +1730,7 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo& dev, const 
     hipError_t e = hipSuccess;
     const hipError_t f = each_part(a.m.rows, kRowsPerLaunch, stream, [&](const Part& p) {
         const size_t r = p.row0;
-        const Join join = join_of(ws, ws.partials, p.rows, a.loss, a.accum || r);
+        const Join join = join_of(ws, ws.partials, p.all, a.loss, a.accum);
         auto launch = [&](auto op) {
             typedef decltype(op) Op;
             const typename Op::Args args = {
@@ -1746,7 +1749,7 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo& dev, const 
             launch(PolicyOp<true>{});
         else
             launch(PolicyOp<false>{});
-        const hipError_t s = sum_joined(join, p.rows, stream);
+        const hipError_t s = sum_joined(join, p.rows, stream, p.first(), p.last());
         e = e == hipSuccess ? s : e;
     });
     return f == hipSuccess ? e : f;
@@ -1777,7 +1780,7 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo& dev
                            a.smoothing, ws.counters + kPairCounts};
     // One part: there are at most kPrefRowsMax rows.
     static_assert(kPrefRowsMax <= kRowsPerLaunch, "a row's number is its place in the launch");
-    const Part all = {0, (uint32_t)a.m.rows, stream};
+    const Part all = {0, (uint32_t)a.m.rows, stream, a.m.rows};
     auto launch = [&](auto op) {
         typedef decltype(op) Op;
         if (split_rows<T>(read, a.m.rows, false))
