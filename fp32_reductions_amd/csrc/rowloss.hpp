@@ -16,7 +16,8 @@ namespace red {
 enum class LogitType { F32, F16, BF16 };
 
 // Rows one launch covers.  A launch holds at most 2^32 - 1 work-items and a
-// row takes at most 512, and the row losses of a launch (8 bytes each) fill
+// row takes at most 1024 of a launch that keeps rows whole (those that cut rows
+// up have their own bounds), and the row losses of a launch (8 bytes each) fill
 // at most half of the workspace; more rows take several launches.
 constexpr size_t kRowsPerLaunch = size_t(1) << 20;
 // Rows and pairs of a preference loss, whose per-row statistics (20 bytes a

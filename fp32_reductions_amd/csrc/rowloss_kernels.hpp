@@ -1619,23 +1619,32 @@ size_t grad_rows_per_launch(const Logits& m)
     return fit < kRowsPerLaunch ? fit : kRowsPerLaunch;
 }
 
-template <class T, class Op>
-void launch_grad(const Logits& m, const Part& p, const typename Op::Args& args)
+// The gradient of rows [row0, row0 + rows), in as many launches as that takes;
+// args_from(row) gives the operator's arguments from a row on.
+template <class T, class Op, class ArgsFrom>
+hipError_t launch_grad(const Logits& m, size_t row0, size_t rows, hipStream_t stream,
+                       ArgsFrom args_from)
 {
     typedef typename T::S S;
-    const S* z = static_cast<const S*>(m.z) + p.row0 * m.ld;
-    S* dz = static_cast<S*>(m.dz) + p.row0 * m.ldd;
     const float c = exponent_scale(m.scale);
     const uint32_t segs = grad_segments<T, Op>(m);
-    if (!segs)
-        hipLaunchKernelGGL((grad_kernel<T, 64, kGradVecs, Op>), dim3((p.rows + 3) / 4), dim3(256),
-                           0, p.stream, z, dz, p.rows, (uint32_t)m.V, 1u, m.ld, m.ldd, c, args);
-    else if (segs == 1)
-        hipLaunchKernelGGL((grad_kernel<T, 256, kGradVecs, Op>), dim3(p.rows), dim3(256), 0,
-                           p.stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
-    else
-        hipLaunchKernelGGL((grad_kernel<T, 256, Op::kPieceVecs, Op>), dim3(p.rows * segs), dim3(256), 0,
-                           p.stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
+    return each_part(rows, grad_rows_per_launch<T, Op>(m), stream, [&](const Part& p) {
+        const size_t row = row0 + p.row0;
+        const S* z = static_cast<const S*>(m.z) + row * m.ld;
+        S* dz = static_cast<S*>(m.dz) + row * m.ldd;
+        const typename Op::Args args = args_from(row);
+        if (!segs)
+            hipLaunchKernelGGL((grad_kernel<T, 64, kGradVecs, Op>), dim3((p.rows + 3) / 4),
+                               dim3(256), 0, stream, z, dz, p.rows, (uint32_t)m.V, 1u, m.ld, m.ldd,
+                               c, args);
+        else if (segs == 1)
+            hipLaunchKernelGGL((grad_kernel<T, 256, kGradVecs, Op>), dim3(p.rows), dim3(256), 0,
+                               stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld, m.ldd, c, args);
+        else
+            hipLaunchKernelGGL((grad_kernel<T, 256, Op::kPieceVecs, Op>), dim3(p.rows * segs),
+                               dim3(256), 0, stream, z, dz, p.rows, (uint32_t)m.V, segs, m.ld,
+                               m.ldd, c, args);
+    });
 }
 
 } // namespace rowloss
@@ -1676,18 +1685,16 @@ hipError_t RowLoss<T>::logprob_grad(const LogprobGradCall& a, const DeviceInfo&,
                                     hipStream_t stream)
 {
     using namespace rowloss;
-    return each_part(a.m.rows, grad_rows_per_launch<T, LogprobGradOp<true>>(a.m), stream, [&](const Part& p) {
-        const size_t r = p.row0;
-        const double inverse = 1.0 / (double)a.m.scale;
-        if (a.gentropy)
-            launch_grad<T, LogprobGradOp<true>>(a.m, p,
-                                                {a.targets + r, a.lse + r, a.entropy + r,
-                                                 a.glogp + r, a.gentropy + r, a.m.scale, inverse});
-        else
-            launch_grad<T, LogprobGradOp<false>>(a.m, p,
-                                                 {a.targets + r, a.lse + r, nullptr, a.glogp + r,
-                                                  nullptr, a.m.scale, inverse});
-    });
+    auto launch = [&](auto op) {
+        typedef decltype(op) Op;
+        return launch_grad<T, Op>(a.m, 0, a.m.rows, stream, [&](size_t r) {
+            return typename Op::Args{a.targets + r, a.lse + r,
+                                     a.gentropy ? a.entropy + r : nullptr, a.glogp + r,
+                                     a.gentropy ? a.gentropy + r : nullptr, a.m.scale,
+                                     1.0 / (double)a.m.scale};
+        });
+    };
+    return a.gentropy ? launch(LogprobGradOp<true>{}) : launch(LogprobGradOp<false>{});
 }
 
 template <class T>
@@ -1742,8 +1749,13 @@ hipError_t RowLoss<T>::policy(const PolicyCall& a, const DeviceInfo& dev, const 
                 return launch_rows_op<T, Op>(a.m, p, args, 0, dev);
             const Split split = split_of(ws, a.m.dz != nullptr);
             launch_split<T, Op>(a.m, p, args, split);
-            if (a.m.dz)
-                launch_grad<T, SplitGradOp<Op::kEntropy>>(a.m, p, {a.targets + r, split.slope});
+            e = e == hipSuccess ? hipGetLastError() : e;
+            if (e != hipSuccess || !a.m.dz)
+                return;
+            typedef SplitGradOp<Op::kEntropy> GradOp;
+            e = launch_grad<T, GradOp>(a.m, r, p.rows, stream, [&](size_t row) {
+                return typename GradOp::Args{a.targets + row, split.slope + (row - r)};
+            });
         };
         if (a.entropy || a.entropy_coef != 0.0f)
             launch(PolicyOp<true>{});
@@ -1796,9 +1808,8 @@ hipError_t RowLoss<T>::preference(const PreferenceCall& a, const DeviceInfo& dev
     if (e == hipSuccess && !joined)
         e = launch_preference_pairs(pair, stream);
     if (e == hipSuccess && a.m.dz)
-        e = each_part(a.m.rows, grad_rows_per_launch<T, PreferenceGradOp>(a.m), stream, [&](const Part& p) {
-            const size_t r = p.row0;
-            launch_grad<T, PreferenceGradOp>(a.m, p, {a.targets + r, stat + r, slope + r});
+        e = launch_grad<T, PreferenceGradOp>(a.m, 0, a.m.rows, stream, [&](size_t r) {
+            return PreferenceGradOp::Args{a.targets + r, stat + r, slope + r};
         });
     return e;
 }
