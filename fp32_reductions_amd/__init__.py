@@ -6,7 +6,8 @@ passes their device pointers and the current HIP stream, and turns a
 non-zero status into ``ReduceError``.  Every step of the reduction runs in
 the HIP kernels of ``libreduce.so``; there is no CPU fallback.  Importing
 this package raises if the library has not been built
-(``python fp32_reductions_amd/build.py``).
+(``python fp32_reductions_amd/build.py``).  The losses over rows of logits
+also need the extension module ``_rowloss.so``, and raise where it is missing.
 
 Names follow the C ABI:
 
@@ -385,15 +386,30 @@ def colprod_u32(src, out, C=None, stream=None):
 
 # These calls take many tensors, and small ones take no longer on the GPU than
 # their checks would in Python: the functions are those of the extension
-# module built from csrc/rowloss_binding.cpp.
+# module built from csrc/rowloss_binding.cpp.  It is tied to the torch that it
+# was built against; where it is absent or does not load the rest of the package
+# works, and these functions raise.
 
-if not os.path.exists(os.path.join(_PKG, "_rowloss.so")):
-    raise ImportError("_rowloss.so is not built beside libreduce.so; run "
-                      "'python fp32_reductions_amd/build.py'")
+def _without_rowloss(name, why):
+    def call(*args, **kwargs):
+        raise ImportError("%s needs the extension module _rowloss.so beside libreduce.so, which "
+                          "cannot be loaded (%s); run 'python fp32_reductions_amd/build.py'"
+                          % (name, why))
 
-from . import _rowloss  # noqa: E402
+    call.__name__ = call.__qualname__ = name
+    return call
 
-globals().update(_rowloss.CALLS)
+
+try:
+    from ._rowloss import CALLS as _LOSSES, MARSHALS as _LOSS_MARSHAL
+except ImportError as _e:
+    _LOSSES = {_n: _without_rowloss(_n, _e)
+               for _n in ("%s_%s" % (_op, _t) for _op in (
+                   "token_logprob", "token_logprob_grad", "distill_topk", "policy_loss",
+                   "preference_loss") for _t in ("f32", "f16", "bf16"))}
+    _LOSS_MARSHAL = _LOSSES
+
+globals().update(_LOSSES)
 
 
 # ---------------------------------------------------------------------------
@@ -415,8 +431,8 @@ for _t in ("f32", "f16", "bf16", "i32", "i16", "u16", "u32"):
 def plan(name: str, *args, **kwargs) -> Plan:
     """Marshal the arguments of entry point ``name`` (e.g. "sum_f32") once;
     the returned Plan enqueues the call each time it is called."""
-    if name in _rowloss.MARSHALS:
-        cargs = _rowloss.MARSHALS[name](*args, **kwargs)
+    if name in _LOSS_MARSHAL:
+        cargs = _LOSS_MARSHAL[name](*args, **kwargs)
         return Plan("red_" + name, cargs, (args, kwargs))
     cname, marshal = _MARSHAL[name]
     cargs, keep = marshal(cname, *args, **kwargs)
