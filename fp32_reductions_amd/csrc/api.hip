@@ -14,6 +14,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <tuple>
 
 #include "internal.hpp"
@@ -143,12 +144,20 @@ int find_slot(int dev, hipStream_t stream, std::shared_ptr<Slot>* out)
     const char* fail = std::getenv("RED_TEST_FAIL_ALLOC");
     if (fail && fail[0] == '1')
         return RED_ERR_NOMEM;
+    // The entry first: what follows can then fail without an exception.
+    std::shared_ptr<Slot> slot;
+    try {
+        slot = std::make_shared<Slot>();
+        g_ws.emplace(key, slot);
+    } catch (const std::bad_alloc&) {
+        return RED_ERR_NOMEM;
+    }
     void* base = nullptr;
     if (hipMalloc(&base, kPartialBytes + kCounterBytes) != hipSuccess) {
         (void)hipGetLastError(); // clear the sticky allocation error
+        g_ws.erase(key);
         return RED_ERR_NOMEM;
     }
-    auto slot = std::make_shared<Slot>();
     slot->ws.partials = base;
     slot->ws.partial_bytes = kPartialBytes;
     slot->ws.counters = reinterpret_cast<unsigned*>(static_cast<char*>(base) + kPartialBytes);
@@ -156,9 +165,9 @@ int find_slot(int dev, hipStream_t stream, std::shared_ptr<Slot>* out)
     (void)hipGetLastError();
     if (red::launch_fill_u32(slot->ws.counters, red::kCounterWords, 0, stream) != hipSuccess) {
         (void)hipFree(base);
+        g_ws.erase(key);
         return RED_ERR_HIP;
     }
-    g_ws.emplace(key, slot);
     *out = slot;
     return RED_OK;
 }

@@ -85,3 +85,18 @@ def test_no_launch_passes_the_limit(run, op, t):
         rows, V, status, launches, largest = map(int, line.split())
         assert (status, launches > 0) == (0, True), line
         assert 0 < largest < 1 << 32, line
+
+
+@pytest.mark.parametrize("op", ["policy_loss", "preference_loss", "distill_topk"])
+def test_out_of_host_memory_is_a_status(run, op):
+    """No exception leaves a C entry point: the call returns the status of a
+    failed workspace, holds nothing, and the next one works."""
+    out = run("fake.set_out_of_host_memory(1)\n"
+              "first = call(%r, 'bf16', 3, 5000)\n"
+              "print(*first, fake.recorded_allocations() - fake.recorded_frees())\n"
+              "fake.set_out_of_host_memory(0)\n"
+              "print(*call(%r, 'bf16', 3, 5000), fake.recorded_allocations())\n" % (op, op))
+    status, launches, _, held = map(int, out[0].split())
+    assert (status, launches, held) == (3, 0, 0)  # RED_ERR_NOMEM
+    status, launches, _, allocated = map(int, out[1].split())
+    assert status == 0 and launches > 0 and allocated == 1
