@@ -16,7 +16,11 @@ namespace red {
 // arrived where every compute die sees it (a device-scope store, waited for),
 // and only then is the row counted, so the last one finds all.  A release
 // fence would do as well, but would write back the whole L2 with the gradient
-// in it.
+// in it.  This is gfx950's behaviour and not the language's memory model, by
+// which relaxed stores and a relaxed count order nothing: device-scope stores
+// write through to where every die reads, s_waitcnt vmcnt(0) returns once they
+// have, device-scope loads do not read an older copy, and they are issued after
+// a branch on the count that was returned.  Another target needs the fences.
 //
 // Arrivals at one address follow each other at 12 ns (1024 rows of 1000 bf16:
 // 17.1 us with one count, 4.3 us for one row), so every 64 rows have a count

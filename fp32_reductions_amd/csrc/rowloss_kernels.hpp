@@ -822,7 +822,7 @@ __device__ __forceinline__ void wave_lds_fence()
 // columns, their logits and the student's logits in them.  The columns are
 // loaded before the row's vectors, which would otherwise return first, and
 // used when the last of those is under way (4096 rows of 131072 bf16, 64
-// entries and the rest: 412 us with one wave that marks for all, 381 so).
+// entries and the rest: 412 us with one wave that marks for all, 382 so).
 template <class T, int GT>
 struct ListReader {
     typedef typename T::S S;
@@ -1593,8 +1593,8 @@ hipError_t each_part(size_t rows, size_t most, hipStream_t stream, F f)
 }
 
 // Vectors per thread of the gradient kernel: four where a row fits a
-// workgroup so, two in the pieces of a longer one (us for 4096 rows, four and
-// two: bf16, V = 6598 21.0 and 23.0, 9802 35.4 and 29.4, 131072 348 and 334;
+// workgroup so, two in the pieces of a longer one (kernel times of one run, us
+// for 4096 rows, four and two: bf16, V = 6598 21.0 and 23.0, 9802 35.4 and 29.4, 131072 348 and 334;
 // f32, 131072 725 and 701; eight lose at 20000, 56 and 74).  Of few rows, whose
 // slopes a kernel before has left, four (64 rows of 131072 bf16, policy loss:
 // 13.7 and 15.2).

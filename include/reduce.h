@@ -298,7 +298,9 @@ int red_colprod_u32(const uint32_t* src, size_t R, size_t C, size_t ld,
  * weight  : one fp32 factor per row (for the preference loss, per pair) in
  *           the sum that makes the loss; NULL: 1 / rows each (1 / pairs).  A
  *           row of weight 0 does not count: its outputs are 0 and its logits
- *           are not looked at.  A mask and a normaliser are both weights.
+ *           are not looked at.  (A pair of weight 0 adds nothing to the loss
+ *           and has a gradient of 0, whatever its logits; its seq_logp is
+ *           computed as any other.)  A mask and a normaliser are both weights.
  * loss    : one fp32 value, the weighted sum of row losses; accum != 0 adds
  *           it to the old value.
  *
@@ -310,9 +312,10 @@ int red_colprod_u32(const uint32_t* src, size_t R, size_t C, size_t ld,
  * is computed once per row and the sums over rows are fp64, and every result
  * is rounded once to its type.  A term below 2^-126 of its row's largest
  * counts as 0 (in the sum of a distilled row's columns that are not listed: of
- * the largest among these).  Logits of -inf have probability 0.  A row with a NaN or +inf,
- * or with nothing but -inf, has NaN results unless it does not count; its
- * neighbours are not touched by it.  A row filled with one finite value is
+ * the largest among these).  Logits of -inf have probability 0.  A row with a
+ * NaN or +inf, or with nothing but -inf, has NaN results unless it does not
+ * count (the lse of nothing but -inf is -inf); its neighbours are not touched
+ * by it.  A row filled with one finite value is
  * uniform, the type's lowest value included.
  * All results are deterministic.
  * ------------------------------------------------------------------- */
@@ -333,7 +336,9 @@ int red_token_logprob_bf16(const uint16_t* logits, size_t rows, size_t V, size_t
 /* The gradient of red_token_logprob: with g = glogp[r] and h = gentropy[r]
  * the gradients of the row's two outputs,
  *   dlogits[r, v] = s (g (delta_{v, target} - p_v) - h p_v (ln p_v + H)).
- * lse and entropy are what the forward call wrote.  gentropy and entropy
+ * lse and entropy are what the forward call wrote, and p_v = exp(s z_v - lse)
+ * with lse as it is: its fp32 rounding, |lse| 2^-24, is a relative error of
+ * every p_v.  gentropy and entropy
  * are both NULL where the entropy has no gradient.  Where g (or the target's
  * column) and h are 0 the row's logits are not looked at. */
 int red_token_logprob_grad_f32(const float* logits, size_t rows, size_t V, size_t ld,
@@ -357,7 +362,8 @@ int red_token_logprob_grad_bf16(const uint16_t* logits, size_t rows, size_t V, s
  * teacher_lse NULL: the teacher is the softmax of the row's entries,
  *   q_k = exp(s val_k) / sum_j exp(s val_j),
  *   row loss = sum_k q_k (ln q_k - ln p_{idx_k}).
- * A row of padding alone (or of -inf alone) does not count.
+ * A row of padding alone (or of -inf alone) does not count; a NaN among the
+ * entries makes NaN of the row.
  *
  * teacher_lse given (ln sum exp(s .) over the teacher's whole row): q_k =
  * exp(s val_k - teacher_lse), and the columns not listed, with the teacher's
@@ -419,7 +425,8 @@ int red_policy_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size_t l
  * rows [starts[i], starts[i + 1]); sequences 0 .. pairs - 1 are the chosen
  * ones and pairs .. 2 pairs - 1 the rejected ones of the same pairs (2 pairs
  * + 1 starts, nondecreasing; bounds outside [0, rows] are moved into it).
- * Rows of no sequence do not count.  With S_i the sum of ln p_target over
+ * Rows of no sequence have a gradient of 0.  pairs == 0 is empty input: nothing
+ * is written, dlogits neither.  With S_i the sum of ln p_target over
  * the sequence's rows that count (average != 0: their mean; an empty
  * sequence has 0), ref_logp[i] the same from a reference model (NULL: 0),
  *   D = (S_c - ref_c) - (S_r - ref_r),   h = beta D - margin,
