@@ -751,6 +751,7 @@ struct DistillOp {
 // largest of them against the row's largest), such a rest counts as 0, and not
 // as infinitely far from the student.
 constexpr double kRestRounding = 0x1p-20, kNoTerm = -745.2;
+constexpr float kFar = 0x1p-100f;
 
 // A row's teacher in LDS: its columns (-1: padding; the high bit marks the
 // later ones of a column listed more than once), probabilities, the logits
@@ -1127,8 +1128,8 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         // rest, st holds the columns outside alone, against their own maximum.
         const float top = Op::kTail ? fmaxf(st.m, top_z) : st.m;
         const Exponent whole(reference(top), c);
-        float total = st.s, shrink = 1.0f; // shrink: from their maximum to the row's
-        double rest = 0.0;
+        float shrink = 1.0f; // from their maximum to the row's
+        double rest = 0.0, total = st.s;
         const double outside = st.s;
         if constexpr (Op::kTail) {
             float in = 0.0f;
@@ -1137,7 +1138,7 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
                     in += exp2_fast(whole.at(l.z[k]));
             in = wave_reduce<OpSum>(in);
             shrink = exp2_fast(fmaxf(whole.at(st.m), kLowest));
-            total = fmaf(st.s, shrink, in);
+            total = (double)st.s * shrink + (double)in;
             if (listed < V && Q < 1.0)
                 rest = 1.0 - Q;
             if (rest <= kRestRounding * (1.0 + fabs((double)r.teacher_lse)) &&
@@ -1147,12 +1148,18 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         }
         if (t < kWave) {
             // Lanes 0, 1 and 2 take the three logarithms at once.
-            const double ln = log(t == 0 ? (double)total : t == 1 ? rest : outside);
+            // The columns outside as they are in the row's sum, so that what is
+            // off in both falls out of p_r; by logits where that may underflow.
+            const bool far = !(shrink > kFar);
+            const double ln = log(t == 0   ? total
+                                  : t == 1 ? rest
+                                           : outside * (far ? 1.0 : (double)shrink));
             const double ln_s = __shfl(ln, 0), ln_rest = __shfl(ln, 1), ln_out = __shfl(ln, 2);
             const double ref = reference(top_z), scale = args.scale, most = reference(top);
             double loss = *l.cross + Q * ((most - ref) * scale + ln_s);
-            if (Op::kTail && rest > 0.0) // ln p_r: by logits, however far below the row's largest
-                loss += rest * (ln_rest - (ln_out + ((double)st.m - most) * scale - ln_s));
+            if (Op::kTail && rest > 0.0)
+                loss += rest *
+                        (ln_rest - ln_out + ln_s - (far ? ((double)st.m - most) * scale : 0.0));
             if (leader) {
                 args.join.put(row, (double)r.weight * loss);
                 if (args.row_loss_out)
@@ -1163,12 +1170,12 @@ __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
         mass = (float)(Q + rest);
         // Against the maximum of st: the gradient of the columns outside is
         // p_v (Q + q_r) less their share of q_r, which does not shrink with p_v.
-        double a = (Q + rest) * (double)shrink / (double)total;
+        double a = (Q + rest) * (double)shrink / total;
         if (Op::kTail && outside > 0.0)
             a -= rest / outside;
         slope = {(float)((double)factor * a), 0.0f};
         listed_ref = uniform(whole.ref);
-        listed_sum = uniform(total);
+        listed_sum = uniform((float)total);
     } else {
         slope = Op::done(args, r, row, st, zy, leader, fix);
     }

@@ -157,3 +157,39 @@ def test_nan_among_the_teachers_entries(red, V, t, tail):
     # and without those rows the loss is a number
     loss, _, _ = run_distill(red, z, idx, val, t, 1.0, torch.where(bad, 0.0, w), lse)
     assert loss.isfinite().all()
+
+
+@pytest.mark.parametrize("t", DTYPES)
+@pytest.mark.parametrize("V", COLUMNS + [196088])
+def test_small_row_losses_with_a_rest(red, V, t):
+    """A student close to its teacher: row losses that are small differences of
+    large terms.  In the row loss, with S = S_out + S_in,
+
+        (Q + q_r) ln S - q_r ln S_out + (terms of exact logits),
+
+    Q + q_r = 1, so an error d of S_out makes d (p_r - q_r) of it and an error e
+    of S_in makes e p_in, p_in the student's listed probability.  d: the row's
+    sum and its move to the row's maximum; e: the exponents, of at most 40, and
+    K additions.  The loss itself is rounded once."""
+    say("small row losses V=%d %s" % (V, t))
+    n, K = 12, 8 if V > 9 else 3
+    g, z, _ = draw(n, V, t, V + 6, std=2.0)
+    idx = lists(n, V, K, g)
+    p = torch.softmax(z.double(), 1)
+    p_in = p.gather(1, idx).sum(1)
+    # a teacher that has the list 1 % more or less likely
+    val = z.gather(1, idx).float()
+    lse = (z.double().logsumexp(1) + 0.01 * torch.randn(n, generator=g).double()).float()
+    loss, row_loss = f32(1), f32(n)
+    getattr(red, "distill_topk_" + t)(z.cuda(), idx.cuda(), val.cuda(), loss, teacher_lse=lse.cuda(),
+                                      row_loss=row_loss)
+    lnq = val.double() - lse.double().unsqueeze(1)
+    q_r = 1 - lnq.exp().sum(1)
+    out = torch.ones(n, V, dtype=torch.bool).scatter_(1, idx, False)
+    p_r = (p * out).sum(1)
+    lnp = torch.log_softmax(z.double(), 1).gather(1, idx)
+    want = (lnq.exp() * (lnq - lnp)).sum(1) + q_r * (q_r.log() - p_r.log())
+    moved = ref.U * (2 * 40 + 2)
+    bound = ((ref.stat_error(V) + moved) * (p_r - q_r).abs() + (moved + K * ref.U) * p_in
+             + want.abs() * ref.U + 2.0 ** -46)
+    ref.check("row_loss", row_loss, want, bound)
