@@ -823,7 +823,7 @@ __device__ __forceinline__ void wave_lds_fence()
 // columns, their logits and the student's logits in them.  The columns are
 // loaded before the row's vectors, which would otherwise return first, and
 // used when the last of those is under way (4096 rows of 131072 bf16, 64
-// entries and the rest: 412 us with one wave that marks for all, 382 so).
+// entries and the rest: 412 us with one wave that marks for all, 384 so).
 template <class T, int GT>
 struct ListReader {
     typedef typename T::S S;
@@ -1012,9 +1012,9 @@ __device__ __forceinline__ void merge_entries(uint32_t K, uint32_t lane, const T
 // GRAD: the gradient is written.
 //
 // Measured (bf16, us a call): policy loss of 8192 rows of 131072, a quarter of
-// them masked, 655 (5.7 TB/s; 639 without arithmetic), of 1024 rows of 32768
-// 26, of 96 rows 8.7; log-probability and entropy of 4096 rows of 131072 168
-// (6.4 TB/s).
+// them masked, 653 (5.7 TB/s; 639 without arithmetic), of 1024 rows of 32768
+// 26, of 96 rows 8.7; log-probability and entropy of 4096 rows of 131072 166
+// (6.5 TB/s).
 template <class T, int GT, int NV, bool MULTI, bool GRAD, class Op>
 __global__ __launch_bounds__(GT < 256 ? 256 : GT) void row_kernel(
     const typename T::S* z, typename T::S* dz, uint32_t rows, uint32_t V, size_t ld, size_t ldd,
