@@ -7,7 +7,8 @@ non-zero status into ``ReduceError``.  Every step of the reduction runs in
 the HIP kernels of ``libreduce.so``; there is no CPU fallback.  Importing
 this package raises if the library has not been built
 (``python fp32_reductions_amd/build.py``).  The losses over rows of logits
-also need the extension module ``_rowloss.so``, and raise where it is missing.
+and the operators around the output layer also need the extension module
+``_rowloss.so``, and raise where it is missing.
 
 Names follow the C ABI:
 
@@ -26,6 +27,14 @@ and, for _f32, _f16 and _bf16 logits, the losses over rows of logits
     distill_topk_f32 (logits, idx, val, loss, ...)
     policy_loss_f32 (logits, targets, old_logp, advantage, loss, logp, ...)
     preference_loss_f32 (logits, targets, starts, loss, seq_logp, ...)
+
+and the operators around the output layer, the last for _f16 and _bf16
+
+    add_rmsnorm_f32 (x, weight, y, residual=None, sum=None, ...)
+    rmsnorm_grad_f32 (h, weight, rstd, dy, dx, ...)
+    router_balance_f32 (logits, experts, loss, counts, ...)
+    linear_ce_bf16 (hidden, weight, targets, loss, ...)
+    linear_ce_workspace (hidden, weight, ...): its bytes of workspace
 
 ``plan(name, *args, **kwargs)`` marshals the same arguments once and returns
 a ``Plan``; calling it enqueues the C entry point with the stored pointers,
@@ -93,6 +102,18 @@ for _t in ("f32", "f16", "bf16"):
                                   _I, _P, _P, _P, _SZ, _P],
         "red_preference_loss_" + _t: [_P, _SZ, _SZ, _SZ, _P, _P, _SZ, _P, _P, _I, _F, _F, _F, _I,
                                       _P, _I, _P, _P, _SZ, _P],
+        "red_add_rmsnorm_" + _t: [_P, _SZ, _SZ, _SZ, _P, _SZ, _P, _F, _P, _SZ, _P, _SZ, _P, _SZ,
+                                  _P, _P, _P],
+        "red_rmsnorm_grad_" + _t: [_P, _SZ, _SZ, _SZ, _P, _P, _P, _SZ, _P, _SZ, _P, _SZ, _P, _I,
+                                   _P],
+        "red_router_balance_" + _t: [_P, _SZ, _SZ, _SZ, _P, _SZ, _SZ, _P, _F, _F, _P, _I, _P, _P,
+                                     _P, _SZ, _P],
+    })
+for _t in ("f16", "bf16"):
+    _SIGS.update({
+        "red_linear_ce_" + _t: [_P, _SZ, _SZ, _SZ, _P, _SZ, _SZ, _P, _P, _F, _F, _P, _I, _P, _P,
+                                _P, _SZ, _P, _SZ, _P, _SZ, _P],
+        "red_linear_ce_workspace_" + _t: [_SZ, _SZ, _SZ, _I, _I, _P],
     })
 for _name, _args in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -381,7 +402,7 @@ def colprod_u32(src, out, C=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# losses over rows of logits
+# losses over rows of logits, and the operators around the output layer
 # ---------------------------------------------------------------------------
 
 # These calls take many tensors, and small ones take no longer on the GPU than
@@ -406,10 +427,27 @@ except ImportError as _e:
     _LOSSES = {_n: _without_rowloss(_n, _e)
                for _n in ("%s_%s" % (_op, _t) for _op in (
                    "token_logprob", "token_logprob_grad", "distill_topk", "policy_loss",
-                   "preference_loss") for _t in ("f32", "f16", "bf16"))}
+                   "preference_loss", "add_rmsnorm", "rmsnorm_grad", "router_balance",
+                   "linear_ce") for _t in ("f32", "f16", "bf16")
+                  if (_op, _t) != ("linear_ce", "f32"))}
     _LOSS_MARSHAL = _LOSSES
 
 globals().update(_LOSSES)
+
+
+def linear_ce_workspace(hidden, weight, dhidden=True, dweight=True) -> int:
+    """Bytes of workspace that linear_ce needs for these tensors on the current
+    device; dhidden, dweight: whether the gradients are wanted."""
+    name = {torch.float16: "red_linear_ce_workspace_f16",
+            torch.bfloat16: "red_linear_ce_workspace_bf16"}.get(hidden.dtype)
+    if name is None:
+        raise TypeError("hidden must be torch.float16 or torch.bfloat16, got %s" % hidden.dtype)
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden and weight must be 2-D")
+    size = ctypes.c_size_t()
+    _check(getattr(_lib, name)(hidden.shape[0], hidden.shape[1], weight.shape[0],
+                               int(bool(dhidden)), int(bool(dweight)), ctypes.byref(size)), name)
+    return size.value
 
 
 # ---------------------------------------------------------------------------

@@ -7,7 +7,8 @@ load the library being rebuilt.)
 
 Each translation unit under csrc/ compiles to an object in csrc/_build/
 (in parallel), and the objects link into fp32_reductions_amd/libreduce.so.
-csrc/rowloss_binding.cpp becomes the extension module _rowloss.so beside it.
+csrc/rowloss_binding.cpp and csrc/layer_binding.cpp become the extension module
+_rowloss.so beside it.
 The library is rebuilt on every call.
 """
 from __future__ import annotations
@@ -28,13 +29,15 @@ LIBRARY = os.path.join(PKG, "libreduce.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "reduce1d.hip", "rows.hip", "colprod.hip", "rowloss.hip",
-           "rowloss_f32.hip", "rowloss_f16.hip", "rowloss_bf16.hip"]
+           "rowloss_f32.hip", "rowloss_f16.hip", "rowloss_bf16.hip", "norm.hip", "router.hip",
+           "linear_ce.hip"]
 # Measurement only (the benchmark's read-only streaming ceiling): a library
 # of its own.
 CALIB_SOURCES = ["calib_read.hip"]
 CALIB_LIBRARY = os.path.join(PKG, "libreduce_calib.so")
-# The Python functions of the losses over rows of logits (host code).
-BINDING_SOURCE = "rowloss_binding.cpp"
+# The Python functions of the losses over rows of logits and of the operators
+# around the output layer (host code).
+BINDING_SOURCES = ["rowloss_binding.cpp", "layer_binding.cpp"]
 BINDING_LIBRARY = os.path.join(PKG, "_rowloss.so")
 
 ARCH = "gfx950"
@@ -82,29 +85,29 @@ def _link(objs, library: str) -> None:
     os.replace(tmp, library)
 
 
-def _compile_binding() -> str:
-    """The binding's object: host C++ against Python's and torch's headers."""
+def _compile_binding(src: str) -> str:
+    """An object of the binding: host C++ against Python's and torch's headers."""
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     rocm = os.path.dirname(os.path.dirname(HIPCC))
-    obj = os.path.join(OBJDIR, os.path.splitext(BINDING_SOURCE)[0] + ".o")
+    obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            "-Wall", "-Wno-attributes", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            "-I" + INCLUDE, "-I" + sysconfig.get_path("include"),
            "-isystem", os.path.join(torch_dir, "include"),
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(rocm, "include"),
-           "-c", os.path.join(CSRC, BINDING_SOURCE), "-o", obj]
+           "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("the compiler failed for %s:\n%s\n%s"
-                           % (BINDING_SOURCE, " ".join(cmd), res.stdout + res.stderr))
+                           % (src, " ".join(cmd), res.stdout + res.stderr))
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs) -> None:
     torch_lib = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
     tmp = BINDING_LIBRARY + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, "-L" + PKG, "-l:libreduce.so",
+    cmd = [os.environ.get("CXX", "g++"), "-shared", *objs, "-o", tmp, "-L" + PKG, "-l:libreduce.so",
            "-Wl,-rpath,$ORIGIN", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_hip"]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -118,12 +121,12 @@ def build(verbose: bool = False) -> str:
     library libreduce_calib.so and the extension module _rowloss.so."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = SOURCES + CALIB_SOURCES
-    with concurrent.futures.ThreadPoolExecutor(len(srcs) + 1) as pool:
-        binding = pool.submit(_compile_binding)
+    with concurrent.futures.ThreadPoolExecutor(len(srcs) + 2) as pool:
+        binding = [pool.submit(_compile_binding, src) for src in BINDING_SOURCES]
         objs = dict(zip(srcs, pool.map(_compile, srcs)))
     _link([objs[s] for s in SOURCES], LIBRARY)
     _link([objs[s] for s in CALIB_SOURCES], CALIB_LIBRARY)
-    _link_binding(binding.result())
+    _link_binding([b.result() for b in binding])
     if verbose:
         print("built %s, %s and %s" % (LIBRARY, CALIB_LIBRARY, BINDING_LIBRARY))
     return LIBRARY

@@ -18,7 +18,10 @@
 #include <tuple>
 
 #include "internal.hpp"
+#include "linear_ce.hpp"
+#include "norm.hpp"
 #include "reduce.h"
+#include "router.hpp"
 #include "rowloss.hpp"
 
 namespace {
@@ -618,6 +621,187 @@ int preference_loss(LogitType t, const red::PreferenceCall& a, red_stream_t stre
     });
 }
 
+// ---- around the output layer --------------------------------------------------
+
+size_t elem_size(LogitType t) { return t == LogitType::F32 ? 4 : 2; }
+
+// One matrix of a call: null only where it is not `needed`.
+struct MatrixArg {
+    const void* p;
+    size_t ld, elem;
+    bool needed;
+};
+
+// Invalid arguments first, alignment second.
+int check_matrices(size_t rows, size_t cols, std::initializer_list<MatrixArg> matrices)
+{
+    int worst = RED_OK;
+    for (const MatrixArg& m : matrices) {
+        if (!m.p) {
+            if (m.needed)
+                return RED_ERR_INVALID;
+            continue;
+        }
+        if ((rows > 1 && m.ld < cols) || !extent_ok(rows, rows > 1 ? m.ld : 0, cols, m.elem))
+            return RED_ERR_INVALID;
+        if (!aligned(m.p, m.elem))
+            worst = RED_ERR_ALIGN;
+    }
+    return worst;
+}
+
+// An output over an input: the same matrix, row for row.
+bool laid_over(const void* out, size_t ldo, const void* in, size_t ldi, size_t rows)
+{
+    return !out || out != in || ldo == ldi || rows <= 1;
+}
+
+int add_rmsnorm(LogitType t, const red::NormCall& a, red_stream_t stream)
+{
+    if (a.rows == 0 || a.D == 0)
+        return RED_OK;
+    const size_t es = elem_size(t);
+    if (a.D > red::kNormColsMax || (!a.y && !a.y8) || !a.y8 != !a.scale8 ||
+        !(a.eps >= 0.0f && std::isfinite(a.eps)) || (a.y && (a.y == a.sum || a.y == a.y8)) ||
+        (a.sum && a.sum == a.y8) || !laid_over(a.sum, a.lds, a.x, a.ldx, a.rows) ||
+        !laid_over(a.sum, a.lds, a.residual, a.ldr, a.rows) ||
+        !laid_over(a.y, a.ldy, a.x, a.ldx, a.rows) ||
+        !laid_over(a.y, a.ldy, a.residual, a.ldr, a.rows))
+        return RED_ERR_INVALID;
+    int st = check_matrices(a.rows, a.D, {{a.x, a.ldx, es, true}, {a.residual, a.ldr, es, false},
+                                          {a.sum, a.lds, es, false}, {a.y, a.ldy, es, false},
+                                          {a.y8, a.ldy8, 1, false}});
+    if (st == RED_ERR_INVALID)
+        return st;
+    for (const int v : {check_values(a.weight, a.D, es, true),
+                        check_values(a.scale8, a.rows, 4, false),
+                        check_values(a.rstd, a.rows, 4, false)}) {
+        if (v == RED_ERR_INVALID)
+            return v;
+        st = v == RED_OK ? st : v;
+    }
+    if (st != RED_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    clear_stale_error();
+    return hip_status(red::launch_add_rmsnorm(t, a, info, static_cast<hipStream_t>(stream)));
+}
+
+int rmsnorm_grad(LogitType t, const red::NormGradCall& a, red_stream_t stream)
+{
+    if (a.rows == 0 || a.D == 0)
+        return RED_OK;
+    const size_t es = elem_size(t);
+    if (a.D > red::kNormColsMax || !laid_over(a.dx, a.lddx, a.h, a.ldh, a.rows) ||
+        !laid_over(a.dx, a.lddx, a.dy, a.lddy, a.rows) ||
+        !laid_over(a.dx, a.lddx, a.dsum, a.ldds, a.rows))
+        return RED_ERR_INVALID;
+    int st = check_matrices(a.rows, a.D, {{a.h, a.ldh, es, true}, {a.dy, a.lddy, es, true},
+                                          {a.dsum, a.ldds, es, false}, {a.dx, a.lddx, es, true}});
+    if (st == RED_ERR_INVALID)
+        return st;
+    for (const int v : {check_values(a.weight, a.D, es, true),
+                        check_values(a.rstd, a.rows, 4, true),
+                        check_values(a.dweight, a.D, 4, false)}) {
+        if (v == RED_ERR_INVALID)
+            return v;
+        st = v == RED_OK ? st : v;
+    }
+    if (st != RED_OK)
+        return st;
+    return with_workspace(stream, [&](const DeviceInfo& d, const Workspace& ws, hipStream_t s) {
+        return red::launch_rmsnorm_grad(t, a, d, ws, s);
+    });
+}
+
+int router_balance(LogitType t, const red::RouterCall& a, red_stream_t stream)
+{
+    const Logits& m = a.m;
+    if (m.rows == 0 || m.V == 0)
+        return RED_OK;
+    if (m.V > red::kRouterExpertsMax || m.rows >= (size_t(1) << 31) || a.K < 1 ||
+        a.K > red::kTopkMax || a.ldk < a.K || !extent_ok(m.rows, a.ldk, a.K, 8) ||
+        !std::isfinite(a.balance) || !std::isfinite(a.z))
+        return RED_ERR_INVALID;
+    const int st = check_logits(t, m, false,
+                                {{a.experts, 0, 8, true}, {a.weight, m.rows, 4, false},
+                                 {a.loss, 1, 4, true}, {a.counts, m.V, 8, true},
+                                 {a.prob, m.V, 4, false}});
+    if (st != RED_OK)
+        return st;
+    return with_workspace(stream, [&](const DeviceInfo& d, const Workspace& ws, hipStream_t s) {
+        return red::launch_router_balance(t, a, d, ws, s);
+    });
+}
+
+bool linear_sizes_ok(size_t rows, size_t D, size_t V)
+{
+    return rows <= red::kLinearRowsMax && V <= red::kLinearVocabMax && D <= red::kLinearWidthMax &&
+           D % 8 == 0;
+}
+
+int linear_ce(LogitType t, const red::LinearCall& a, red_stream_t stream)
+{
+    if (a.rows == 0 || a.V == 0 || a.D == 0)
+        return RED_OK;
+    if (!linear_sizes_ok(a.rows, a.D, a.V) || a.ldw % 8 || a.ldw > red::kLinearStrideMax ||
+        !scale_ok(a.scale) || !std::isfinite(a.z) || !a.workspace ||
+        (a.dhidden && a.dhidden == a.hidden) || (a.dweight && a.dweight == a.weight))
+        return RED_ERR_INVALID;
+    int st = check_matrices(a.rows, a.D, {{a.hidden, a.ldh, 2, true}, {a.dhidden, a.lddh, 2, false}});
+    if (st == RED_ERR_INVALID)
+        return st;
+    for (const int v : {check_matrices(a.V, a.D, {{a.weight, a.ldw, 2, true},
+                                                  {a.dweight, a.lddw, 2, false}}),
+                        check_values(a.targets, a.rows, 8, true),
+                        check_values(a.row_weight, a.rows, 4, false),
+                        check_values(a.loss, 1, 4, true), check_values(a.logp, a.rows, 4, false),
+                        check_values(a.lse, a.rows, 4, false)}) {
+        if (v == RED_ERR_INVALID)
+            return v;
+        st = v == RED_OK ? st : v;
+    }
+    if (!aligned(a.weight, 16) || !aligned(a.workspace, 256))
+        st = RED_ERR_ALIGN;
+    if (st != RED_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    if (red::linear_ce_workspace(t, a, info) > a.workspace_bytes)
+        return RED_ERR_SCRATCH;
+    clear_stale_error();
+    return hip_status(red::launch_linear_ce(t, a, info, static_cast<hipStream_t>(stream)));
+}
+
+int linear_ce_workspace(LogitType t, size_t rows, size_t D, size_t V, int dhidden, int dweight,
+                        size_t* bytes)
+{
+    if (!bytes)
+        return RED_ERR_INVALID;
+    *bytes = 0;
+    if (rows == 0 || V == 0 || D == 0)
+        return RED_OK;
+    if (!linear_sizes_ok(rows, D, V))
+        return RED_ERR_INVALID;
+    int dev, st;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != RED_OK)
+        return st;
+    red::LinearCall a = {};
+    a.rows = rows;
+    a.D = D;
+    a.V = V;
+    a.dhidden = dhidden ? bytes : nullptr;
+    a.dweight = dweight ? bytes : nullptr;
+    *bytes = red::linear_ce_workspace(t, a, info);
+    return RED_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -876,6 +1060,116 @@ int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size
                             ref_logp, weight, kind, average, beta, margin, smoothing, loss,
                             seq_logp, accum},
                            stream);
+}
+
+int red_add_rmsnorm_f32(const float* x, size_t rows, size_t D, size_t ldx, const float* residual,
+                        size_t ldr, const float* weight, float eps, float* sum, size_t lds, float* y,
+                        size_t ldy, uint8_t* y8, size_t ldy8, float* scale8, float* rstd,
+                        red_stream_t stream)
+{
+    return add_rmsnorm(LogitType::F32, {x, residual, weight, sum, y, y8, scale8, rstd, rows, D, ldx, ldr, lds,
+                                        ldy, ldy8, eps}, stream);
+}
+int red_rmsnorm_grad_f32(const float* h, size_t rows, size_t D, size_t ldh, const float* weight,
+                         const float* rstd, const float* dy, size_t lddy, const float* dsum,
+                         size_t ldds, float* dx, size_t lddx, float* dweight, int accum,
+                         red_stream_t stream)
+{
+    return rmsnorm_grad(LogitType::F32, {h, weight, rstd, dy, dsum, dx, dweight, rows, D, ldh, lddy, ldds, lddx,
+                                         accum}, stream);
+}
+int red_router_balance_f32(const float* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, float* dlogits, size_t ldd,
+                           red_stream_t stream)
+{
+    return router_balance(LogitType::F32, {{logits, dlogits, rows, E, ld, ldd, 1.0f}, experts, K, ldk, weight,
+                                           balance_coef, z_coef, loss, counts, prob, accum}, stream);
+}
+
+int red_add_rmsnorm_f16(const uint16_t* x, size_t rows, size_t D, size_t ldx, const uint16_t* residual,
+                        size_t ldr, const uint16_t* weight, float eps, uint16_t* sum, size_t lds, uint16_t* y,
+                        size_t ldy, uint8_t* y8, size_t ldy8, float* scale8, float* rstd,
+                        red_stream_t stream)
+{
+    return add_rmsnorm(LogitType::F16, {x, residual, weight, sum, y, y8, scale8, rstd, rows, D, ldx, ldr, lds,
+                                        ldy, ldy8, eps}, stream);
+}
+int red_rmsnorm_grad_f16(const uint16_t* h, size_t rows, size_t D, size_t ldh, const uint16_t* weight,
+                         const float* rstd, const uint16_t* dy, size_t lddy, const uint16_t* dsum,
+                         size_t ldds, uint16_t* dx, size_t lddx, float* dweight, int accum,
+                         red_stream_t stream)
+{
+    return rmsnorm_grad(LogitType::F16, {h, weight, rstd, dy, dsum, dx, dweight, rows, D, ldh, lddy, ldds, lddx,
+                                         accum}, stream);
+}
+int red_router_balance_f16(const uint16_t* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, uint16_t* dlogits, size_t ldd,
+                           red_stream_t stream)
+{
+    return router_balance(LogitType::F16, {{logits, dlogits, rows, E, ld, ldd, 1.0f}, experts, K, ldk, weight,
+                                           balance_coef, z_coef, loss, counts, prob, accum}, stream);
+}
+
+int red_add_rmsnorm_bf16(const uint16_t* x, size_t rows, size_t D, size_t ldx, const uint16_t* residual,
+                        size_t ldr, const uint16_t* weight, float eps, uint16_t* sum, size_t lds, uint16_t* y,
+                        size_t ldy, uint8_t* y8, size_t ldy8, float* scale8, float* rstd,
+                        red_stream_t stream)
+{
+    return add_rmsnorm(LogitType::BF16, {x, residual, weight, sum, y, y8, scale8, rstd, rows, D, ldx, ldr, lds,
+                                        ldy, ldy8, eps}, stream);
+}
+int red_rmsnorm_grad_bf16(const uint16_t* h, size_t rows, size_t D, size_t ldh, const uint16_t* weight,
+                         const float* rstd, const uint16_t* dy, size_t lddy, const uint16_t* dsum,
+                         size_t ldds, uint16_t* dx, size_t lddx, float* dweight, int accum,
+                         red_stream_t stream)
+{
+    return rmsnorm_grad(LogitType::BF16, {h, weight, rstd, dy, dsum, dx, dweight, rows, D, ldh, lddy, ldds, lddx,
+                                         accum}, stream);
+}
+int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, uint16_t* dlogits, size_t ldd,
+                           red_stream_t stream)
+{
+    return router_balance(LogitType::BF16, {{logits, dlogits, rows, E, ld, ldd, 1.0f}, experts, K, ldk, weight,
+                                           balance_coef, z_coef, loss, counts, prob, accum}, stream);
+}
+
+int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
+                      const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
+                      const float* row_weight, float scale, float z_coef, float* loss, int accum,
+                      float* logp, float* lse, uint16_t* dhidden, size_t lddh, uint16_t* dweight,
+                      size_t lddw, void* workspace, size_t workspace_bytes, red_stream_t stream)
+{
+    return linear_ce(LogitType::F16, {hidden, weight, rows, D, ldh, V, ldw, targets, row_weight, scale,
+                                      z_coef, loss, logp, lse, accum, dhidden, dweight, lddh, lddw,
+                                      workspace, workspace_bytes}, stream);
+}
+int red_linear_ce_workspace_f16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
+                                size_t* bytes)
+{
+    return linear_ce_workspace(LogitType::F16, rows, D, V, dhidden, dweight, bytes);
+}
+
+int red_linear_ce_bf16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
+                      const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
+                      const float* row_weight, float scale, float z_coef, float* loss, int accum,
+                      float* logp, float* lse, uint16_t* dhidden, size_t lddh, uint16_t* dweight,
+                      size_t lddw, void* workspace, size_t workspace_bytes, red_stream_t stream)
+{
+    return linear_ce(LogitType::BF16, {hidden, weight, rows, D, ldh, V, ldw, targets, row_weight, scale,
+                                      z_coef, loss, logp, lse, accum, dhidden, dweight, lddh, lddw,
+                                      workspace, workspace_bytes}, stream);
+}
+int red_linear_ce_workspace_bf16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
+                                size_t* bytes)
+{
+    return linear_ce_workspace(LogitType::BF16, rows, D, V, dhidden, dweight, bytes);
 }
 
 int red_release_workspace(red_stream_t stream)

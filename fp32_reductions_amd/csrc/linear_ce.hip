@@ -1,0 +1,624 @@
+// linear_ce.hip -- the cross entropy of hidden rows against an output layer,
+// without keeping the logits, and its gradients.
+//
+//     z = s h W^T,  lse = ln sum_v exp z_v,  row loss = lse - z_t + c lse^2
+//     d_v = w s ((1 + 2 c lse) p_v - [v = t]),  dh = d W,  dW = d^T h
+//
+// The products run on the matrix cores (mfma_tile.hpp).  Forward, a workgroup's
+// tile of logits stays in its registers and leaves one maximum and one sum of
+// exponentials for each of its rows, which a second kernel joins.  The
+// gradients need the whole row's sum before the first of them, so the logits are
+// computed a second time, a piece of the vocabulary at a time: the piece's d,
+// rounded to the inputs' type, goes to the workspace (it is an operand of both
+// further products), dh gathers d W over the pieces in fp32, and the piece's
+// rows of dW are finished at once.  So 8 rows V D operations where keeping the
+// logits would take 6, and a workspace that does not grow with V.
+//
+// Rows that do not count are left out first: the others' hidden rows are copied
+// together (rows D elements, nothing beside rows V D), which also keeps a NaN in
+// a masked row out of dW, and makes the products' operand aligned and padded.
+//
+// In half precision d would lose its small values: it is kept as d 2^(8 - e), e
+// the exponent of its row's factors, put back exactly in fp32 behind the
+// products (for dW, whose sum runs over rows, on a copy of the hidden rows).
+#include <algorithm>
+#include <cmath>
+
+#include "linear_ce.hpp"
+#include "mfma_tile.hpp"
+#include "rowloss_join.hpp"
+
+namespace red {
+namespace {
+
+constexpr float kLog2ef = 1.4426950408889634f;
+constexpr double kLog2e64 = 1.4426950408889634074;
+constexpr int kHalfShift = 8; // exponent of the largest factors of d in half precision
+
+typedef TileShape<256, 256, 2, 4, 2> BigTile;
+typedef TileShape<128, 128, 2, 2, 2> MidTile;
+typedef TileShape<128, 32, 4, 1, 4> FewTile;
+
+// What the kernels share.  Pointers into the workspace, except those of the call.
+struct Lce {
+    LinearCall c;
+    uint32_t* count;   // [0]: rows that count; [1]: largest exponent (int, half precision)
+    int32_t* where;    // of each row of the call: its place among those that count, or -1
+    int32_t *row, *target; // of each row that counts: its number, its target
+    float *w, *zt, *lse2, *fa, *fb, *fs; // weight, target's product, lse log2 e, factors, 2^(e - 8)
+    int32_t* e;
+    double* row_loss;
+    char *h, *hs;      // hidden rows, and in half precision a scaled copy
+    size_t ldh;        // bytes
+    float2* stat;      // maximum and sum of each row and vocabulary tile
+    uint32_t tiles_v;
+    char* d;           // rows x piece
+    uint32_t piece;
+    float* dh;         // splits x padded rows x padded width, in tile order
+    uint32_t splits;
+};
+
+// ---- rows that count --------------------------------------------------------
+
+__global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
+{
+    __shared__ uint32_t lds[1024 / kWave];
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint32_t before = 0;
+    for (size_t first = 0; first < a.c.rows; first += 1024) {
+        const size_t r = first + threadIdx.x;
+        int64_t t = -1;
+        float w = 0.0f;
+        if (r < a.c.rows) {
+            t = a.c.targets[r];
+            w = a.c.row_weight ? a.c.row_weight[r] : 1.0f / (float)a.c.rows;
+        }
+        const bool counts = w != 0.0f && t >= 0 && t < (int64_t)a.c.V;
+        const uint64_t all = __ballot(counts);
+        if (lane == 0)
+            lds[wave] = __popcll(all);
+        __syncthreads();
+        uint32_t at = before, total = 0;
+        for (uint32_t k = 0; k < 1024 / kWave; ++k) {
+            at += k < wave ? lds[k] : 0;
+            total += lds[k];
+        }
+        at += __popcll(all & ((1ull << lane) - 1));
+        if (r < a.c.rows)
+            a.where[r] = counts ? (int32_t)at : -1;
+        if (counts) {
+            a.row[at] = (int32_t)r;
+            a.target[at] = (int32_t)t;
+            a.w[at] = w;
+        }
+        before += total;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        a.count[0] = before;
+        a.count[1] = (uint32_t)INT32_MIN;
+    }
+}
+
+// One workgroup a row of the call, and kStepK more for the zeros after the last
+// row that counts.
+__global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
+{
+    const size_t r = blockIdx.x;
+    const uint32_t D = (uint32_t)a.c.D, chunks = (uint32_t)(a.ldh / 16);
+    const uint16_t* from = nullptr;
+    uint32_t to;
+    if (r < a.c.rows) {
+        const int32_t at = a.where[r];
+        if (at < 0) {
+            if (threadIdx.x == 0) {
+                if (a.c.logp)
+                    a.c.logp[r] = 0.0f;
+                if (a.c.lse)
+                    a.c.lse[r] = 0.0f;
+            }
+            if (a.c.dhidden) {
+                uint16_t* out = static_cast<uint16_t*>(a.c.dhidden) + r * a.c.lddh;
+                for (uint32_t i = threadIdx.x; i < D; i += 256)
+                    out[i] = 0;
+            }
+            return;
+        }
+        to = (uint32_t)at;
+        from = static_cast<const uint16_t*>(a.c.hidden) + r * a.c.ldh;
+    } else {
+        const uint32_t n = a.count[0];
+        to = n + (uint32_t)(r - a.c.rows);
+        if (to >= (n + kStepK - 1) / kStepK * kStepK)
+            return;
+    }
+    u32x4_t* out = reinterpret_cast<u32x4_t*>(a.h + to * a.ldh);
+    for (uint32_t i = threadIdx.x; i < chunks; i += 256) {
+        u32x4_t v = {0, 0, 0, 0};
+        if (from && i * 8 < D) { // D is a multiple of 8
+            const u32x4u_t u = reinterpret_cast<const u32x4u_t*>(from)[i];
+            v = u32x4_t{u.x, u.y, u.z, u.w};
+        }
+        out[i] = v;
+    }
+}
+
+// ---- tiles ------------------------------------------------------------------
+
+// The tile of workgroup `id`: each XCD takes a run of the order, in which 8
+// tiles along m go with every tile along n, so that what one XCD's compute units
+// read at a time is few operand rows, from its own L2.
+struct TileAt {
+    uint32_t m, n;
+};
+__device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tiles_m, uint32_t tiles_n)
+{
+    const uint32_t total = tiles_m * tiles_n, x = id % kXcds, i = id / kXcds;
+    const uint32_t per = total / kXcds, rest = total % kXcds;
+    const uint32_t o = x * per + (x < rest ? x : rest) + i;
+    const uint32_t group = o / (8 * tiles_n), in = o % (8 * tiles_n);
+    const uint32_t left = tiles_m - group * 8, height = left < 8 ? left : 8;
+    return {group * 8 + in % height, in / height};
+}
+
+template <class S>
+__device__ __forceinline__ uint32_t lds_of(char (&lds)[S::kLds])
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+}
+
+// ---- forward ------------------------------------------------------------------
+
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t first,
+                                                               uint32_t tiles_m, uint32_t tiles_n)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    const uint32_t lds = lds_of<S>(buffer);
+    TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
+    t.m += first;
+    const uint32_t v0 = t.m * S::M, n0 = t.n * S::N, rows = a.count[0];
+    if (n0 >= rows)
+        return;
+    const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
+    const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
+    TileAcc<S> acc;
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds);
+
+    const float c = a.c.scale * kLog2ef;
+    const uint32_t left = (uint32_t)a.c.V - v0; // columns of this tile
+    float2* part = reinterpret_cast<float2*>(buffer); // [WM][N]
+#pragma unroll
+    for (int j = 0; j < S::NS; ++j) {
+        const uint32_t n = acc.n(j);
+        if (left < (uint32_t)S::M) {
+#pragma unroll
+            for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (acc.m(i, e) >= left)
+                        acc.c[i][j][e] = -INFINITY;
+        }
+        // The target's product, where it is in this tile.
+        const uint32_t at = n0 + n < rows ? (uint32_t)a.target[n0 + n] - v0 : ~0u;
+        if (__any(at < (uint32_t)S::M)) {
+#pragma unroll
+            for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (acc.m(i, e) == at)
+                        a.zt[n0 + n] = acc.c[i][j][e];
+        }
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                m = fmaxf(m, acc.c[i][j][e]);
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s += __builtin_amdgcn_exp2f((acc.c[i][j][e] - ref) * c);
+        s += __shfl_xor(s, 32);
+        if (threadIdx.x % kWave < 32)
+            part[threadIdx.x / kWave / S::WN * S::N + n] = make_float2(m, s);
+    }
+    barrier();
+    for (uint32_t n = threadIdx.x; n < (uint32_t)S::N; n += S::kThreads) {
+        if (n0 + n >= rows)
+            continue;
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < S::WM; ++k)
+            m = fmaxf(m, part[k * S::N + n].x);
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int k = 0; k < S::WM; ++k) {
+            const float2 p = part[k * S::N + n];
+            s += p.y * __builtin_amdgcn_exp2f((p.x - ref) * c);
+        }
+        a.stat[(size_t)(n0 + n) * a.tiles_v + t.m] = make_float2(m, s);
+    }
+}
+
+// One wave a row: its tiles' sums, its loss and the factors of its gradient.
+template <class T>
+__global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
+{
+    const uint32_t n = blockIdx.x * kWaves + threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    if (n >= a.c.rows)
+        return;
+    if (n >= a.count[0]) {
+        if (lane == 0)
+            a.row_loss[n] = 0.0;
+        return;
+    }
+    const float2* stat = a.stat + (size_t)n * a.tiles_v;
+    const float c = a.c.scale * kLog2ef;
+    float m = -INFINITY;
+    for (uint32_t k = lane; k < a.tiles_v; k += kWave)
+        m = fmaxf(m, stat[k].x);
+    m = wave_reduce<OpMax>(m);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    double s = 0.0;
+    for (uint32_t k = lane; k < a.tiles_v; k += kWave) {
+        const float2 p = stat[k];
+        s += (double)(p.y * __builtin_amdgcn_exp2f((p.x - ref) * c));
+    }
+    s = wave_sum64(s);
+    if (lane)
+        return;
+    const double scale = a.c.scale, w = a.w[n];
+    const double ln = log(s), lse = scale * (double)ref + ln;
+    const double logp = scale * ((double)a.zt[n] - (double)ref) - ln;
+    const uint32_t r = (uint32_t)a.row[n];
+    if (a.c.logp)
+        a.c.logp[r] = (float)logp;
+    if (a.c.lse)
+        a.c.lse[r] = (float)lse;
+    a.row_loss[n] = w * ((double)a.c.z * lse * lse - logp);
+    a.lse2[n] = (float)(lse * kLog2e64);
+    double fa = w * scale * (1.0 + 2.0 * (double)a.c.z * lse), fb = w * scale;
+    if constexpr (__is_same(T, ElemF16)) {
+        const double most = fmax(fabs(fa), fabs(fb));
+        int e = most > 0.0 && most < 1e38 ? ilogb(most) : 0;
+        e = e < -100 ? -100 : e > 100 ? 100 : e;
+        fa = ldexp(fa, kHalfShift - e);
+        fb = ldexp(fb, kHalfShift - e);
+        a.e[n] = e;
+        a.fs[n] = ldexpf(1.0f, e - kHalfShift);
+        atomicMax(reinterpret_cast<int*>(a.count + 1), e); // of integers: in any order
+    }
+    a.fa[n] = (float)fa;
+    a.fb[n] = (float)fb;
+}
+
+// ---- gradients --------------------------------------------------------------
+
+// Half precision: the hidden rows times 2^(e - the largest e).
+__global__ __launch_bounds__(256) void lce_scale_kernel(Lce a)
+{
+    const uint32_t n = blockIdx.x, rows = a.count[0];
+    if (n >= (rows + kStepK - 1) / kStepK * kStepK)
+        return;
+    const float f = n < rows ? ldexpf(1.0f, a.e[n] - (int)a.count[1]) : 0.0f;
+    const u32x4_t* from = reinterpret_cast<const u32x4_t*>(a.h + n * a.ldh);
+    u32x4_t* to = reinterpret_cast<u32x4_t*>(a.hs + n * a.ldh);
+    for (uint32_t i = threadIdx.x; i < a.ldh / 16; i += 256) {
+        float v[8];
+        ElemF16::unpack(from[i], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] *= f;
+        to[i] = ElemF16::pack(v);
+    }
+}
+
+// d of the piece that starts at column `first`, rows of a.piece elements.
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t first, uint32_t tiles_n)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    const uint32_t lds = lds_of<S>(buffer);
+    const uint32_t rows = a.count[0];
+    const TileAt t = tile_at(blockIdx.x, a.piece / S::M, tiles_n);
+    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N, v0 = first + m0;
+    if (n0 >= rows || v0 >= (uint32_t)a.c.V)
+        return;
+    const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
+    const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
+    TileAcc<S> acc;
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds);
+
+    const float c = a.c.scale * kLog2ef;
+    const uint32_t left = (uint32_t)a.c.V - v0;
+    float lse2[S::NS], fa[S::NS], fb[S::NS];
+    uint32_t at[S::NS];
+#pragma unroll
+    for (int j = 0; j < S::NS; ++j) {
+        const uint32_t n = n0 + acc.n(j);
+        const bool in = n < rows;
+        lse2[j] = in ? a.lse2[n] : 0.0f;
+        fa[j] = in ? a.fa[n] : 0.0f;
+        fb[j] = in ? a.fb[n] : 0.0f;
+        at[j] = in ? (uint32_t)a.target[n] - v0 : ~0u;
+    }
+    store_tile<T>(acc, lds, S::M, [&](float z, int i, int j, int e) {
+        const uint32_t m = acc.m(i, e);
+        float d = fa[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -lse2[j]));
+        d = m == at[j] ? d - fb[j] : d;
+        return m < left ? d : 0.0f;
+    }, [&](uint32_t n) {
+        return reinterpret_cast<uint16_t*>(a.d) + (size_t)(n0 + n) * a.piece + m0;
+    });
+}
+
+// dh [+]= d W over the steps of k of split blockIdx.y.
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_dh_kernel(Lce a, uint32_t first, uint32_t tiles_m,
+                                                             uint32_t tiles_n)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    const uint32_t lds = lds_of<S>(buffer);
+    const uint32_t rows = a.count[0];
+    const TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
+    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
+    if (n0 >= rows)
+        return;
+    const uint32_t left = (uint32_t)a.c.V - first, k = left < a.piece ? left : a.piece;
+    const uint32_t stages = (k + kStepK - 1) / kStepK;
+    const uint32_t per = (stages + a.splits - 1) / a.splits * kStepK;
+    const uint32_t begin = blockIdx.y * per < k ? blockIdx.y * per : k;
+    const uint32_t end = begin + per < k ? begin + per : k;
+    const Operand W = {static_cast<const char*>(a.c.weight) + (size_t)first * a.c.ldw * 2,
+                       a.c.ldw * 2, (uint32_t)a.c.D, k};
+    const Operand d = {a.d, (size_t)a.piece * 2, rows, k};
+    TileAcc<S> acc;
+    multiply<T, S, false, true>(acc, W, d, m0, n0, begin, end, lds);
+    // In the order of the tile's lanes: 16 bytes a lane, 1 KiB a wave.
+    const size_t tile = ((size_t)blockIdx.y * tiles_m + t.m) * tiles_n + t.n;
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(a.dh) + tile * (S::M * S::N / 4) +
+                  threadIdx.x / kWave * (S::MS * S::NS * 4 * kWave) + threadIdx.x % kWave;
+#pragma unroll
+    for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+        for (int j = 0; j < S::NS; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4_t* p = to + ((i * S::NS + j) * 4 + q) * kWave;
+                f32x4_t v = {acc.c[i][j][4 * q], acc.c[i][j][4 * q + 1], acc.c[i][j][4 * q + 2],
+                             acc.c[i][j][4 * q + 3]};
+                if (first)
+                    v += *p;
+                *p = v;
+            }
+}
+
+// The rows of dh, one a workgroup: their splits' sums, in order, rounded once.
+template <class T, class S>
+__global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t tiles_m, uint32_t tiles_n)
+{
+    const uint32_t n = blockIdx.x;
+    if (n >= a.count[0])
+        return;
+    for (uint32_t m = threadIdx.x * 4; m < a.c.D; m += kBlock * 4) {
+        const uint32_t in_m = m % S::M, in_n = n % S::N;
+        const uint32_t wave = in_m / (S::MS * 32) * S::WN + in_n / (S::NS * 32);
+        const uint32_t i = in_m / 32 % S::MS, j = in_n / 32 % S::NS;
+        const uint32_t lane = in_m / 4 % 2 * 32 + in_n % 32, q = in_m / 8 % 4;
+        const size_t tile = (size_t)(m / S::M) * tiles_n + n / S::N;
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.dh) + tile * (S::M * S::N / 4) +
+                           ((wave * S::MS * S::NS + i * S::NS + j) * 4 + q) * kWave + lane;
+        const size_t split = (size_t)tiles_m * tiles_n * (S::M * S::N / 4);
+        f32x4_t v = *p;
+#pragma unroll 4
+        for (uint32_t k = 1; k < a.splits; ++k)
+            v += p[k * split];
+        if constexpr (__is_same(T, ElemF16))
+            v *= a.fs[n];
+        uint16_t* out = static_cast<uint16_t*>(a.c.dhidden) + (size_t)a.row[n] * a.c.lddh + m;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            out[x] = T::narrow(v[x]);
+    }
+}
+
+// The piece's rows of dW.
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t first, uint32_t tiles_m,
+                                                             uint32_t tiles_n)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    const uint32_t lds = lds_of<S>(buffer);
+    const uint32_t rows = a.count[0];
+    const TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
+    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
+    const uint32_t left = (uint32_t)a.c.V - first;
+    const Operand H = {__is_same(T, ElemF16) ? a.hs : a.h, a.ldh, (uint32_t)(a.ldh / 2), rows};
+    const Operand d = {a.d, (size_t)a.piece * 2, a.piece, rows};
+    TileAcc<S> acc;
+    multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
+    const float f = __is_same(T, ElemF16) && rows ? ldexpf(1.0f, (int)a.count[1] - kHalfShift) : 1.0f;
+    store_tile<T>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
+                  [&](uint32_t n) -> uint16_t* {
+                      return n0 + n < left ? static_cast<uint16_t*>(a.c.dweight) +
+                                                 (size_t)(first + n0 + n) * a.c.lddw + m0
+                                           : nullptr;
+                  });
+}
+
+// ---- plan -------------------------------------------------------------------
+
+constexpr size_t kPieceBytes = size_t(256) << 20; // of d, where that is 2048 columns or more
+constexpr size_t kRowPad = 256, kColPad = 256;
+// A launch holds at most 2^32 - 1 work-items, of which a tile takes up to 512.
+constexpr uint32_t kTilesPerLaunch = 1u << 22;
+
+size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+enum class Kind { Few, Mid, Big };
+
+// Tiles by the work: 32 rows by 128 columns where there are few rows, whose
+// product only reads the layer; 256 x 256, the fastest, where there are enough of
+// them to give every compute unit one; 128 x 128 in between.
+struct LcePlan {
+    Kind kind, kind_w; // of the products over rows; of the layer's gradient
+    uint32_t tile_m, tile_n, tile_w;
+    uint32_t tiles_v, tiles_n, tiles_d;
+    size_t rows, piece, splits, bytes;
+};
+
+template <class F>
+auto with_shape(Kind k, F f)
+{
+    switch (k) {
+    case Kind::Few: return f(FewTile());
+    case Kind::Mid: return f(MidTile());
+    default: return f(BigTile());
+    }
+}
+
+// Places in the workspace, 256 bytes apart at least; with base null it only adds
+// up.
+struct Places {
+    char* base;
+    size_t used = 0;
+    template <class P>
+    void take(P*& p, size_t bytes)
+    {
+        p = base ? reinterpret_cast<P*>(base + used) : nullptr;
+        used += round_up(bytes, 256);
+    }
+};
+
+LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
+{
+    LcePlan p;
+    const bool grad = c.dhidden || c.dweight;
+    p.rows = round_up(c.rows, kRowPad);
+    const size_t big = round_up(c.V, 256) / 256 * (p.rows / 256);
+    p.kind = c.rows <= 32 ? Kind::Few : c.rows > 128 && big >= (size_t)dev.cus ? Kind::Big : Kind::Mid;
+    with_shape(p.kind, [&](auto s) {
+        p.tile_m = s.M;
+        p.tile_n = s.N;
+        return 0;
+    });
+    p.tiles_v = (uint32_t)((c.V + p.tile_m - 1) / p.tile_m);
+    p.tiles_n = (uint32_t)((c.rows + p.tile_n - 1) / p.tile_n);
+    p.tiles_d = (uint32_t)((c.D + p.tile_m - 1) / p.tile_m);
+    p.kind_w = c.rows <= 128 || p.kind != Kind::Big ? Kind::Mid : Kind::Big;
+    p.tile_w = p.kind_w == Kind::Mid ? 128 : 256;
+    p.piece = std::min(round_up(c.V, kColPad),
+                       std::max<size_t>(2048, kPieceBytes / 2 / p.rows / kColPad * kColPad));
+    const size_t tiles = (size_t)p.tiles_d * p.tiles_n, stages = p.piece / kStepK;
+    p.splits = std::max<size_t>(1, std::min((size_t)dev.cus / std::max<size_t>(1, tiles), stages / 8));
+
+    Places w = {static_cast<char*>(c.workspace)};
+    Lce dummy;
+    Lce& o = a ? *a : dummy;
+    o.c = c;
+    const size_t n = p.rows;
+    o.ldh = round_up(c.D, kStepK) * 2;
+    w.take(o.count, 8);
+    w.take(o.where, 4 * n);
+    w.take(o.row, 4 * n);
+    w.take(o.target, 4 * n);
+    for (float** f : {&o.w, &o.zt, &o.lse2, &o.fa, &o.fb, &o.fs})
+        w.take(*f, 4 * n);
+    w.take(o.e, 4 * n);
+    w.take(o.row_loss, 8 * n);
+    w.take(o.h, o.ldh * n);
+    o.hs = nullptr;
+    if (t == LogitType::F16 && c.dweight)
+        w.take(o.hs, o.ldh * n);
+    o.tiles_v = p.tiles_v;
+    w.take(o.stat, sizeof(float2) * p.tiles_v * c.rows);
+    o.piece = (uint32_t)p.piece;
+    o.splits = (uint32_t)p.splits;
+    if (grad)
+        w.take(o.d, 2 * p.piece * n);
+    if (c.dhidden)
+        w.take(o.dh, 4 * p.splits * p.tiles_d * p.tile_m * p.tiles_n * p.tile_n);
+    p.bytes = w.used;
+    return p;
+}
+
+template <class T>
+hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStream_t s)
+{
+    Lce a;
+    const LcePlan p = plan_of(t, c, dev, &a);
+    hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(lce_gather_kernel, dim3((unsigned)c.rows + kStepK), dim3(256), 0, s, a);
+    with_shape(p.kind, [&](auto shape) {
+        typedef decltype(shape) S;
+        const uint32_t most = std::max(8u, kTilesPerLaunch / p.tiles_n);
+        for (uint32_t first = 0; first < p.tiles_v; first += most) {
+            const uint32_t tiles_m = std::min(most, p.tiles_v - first);
+            hipLaunchKernelGGL((lce_stat_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads),
+                               0, s, a, first, tiles_m, p.tiles_n);
+        }
+        return 0;
+    });
+    hipLaunchKernelGGL(lce_join_kernel<T>, dim3((unsigned)((c.rows + kWaves - 1) / kWaves)),
+                       dim3(kBlock), 0, s, a);
+    hipError_t e = launch_loss_sum(a.row_loss, c.rows, c.loss, c.accum, nullptr, nullptr, s);
+    if (e != hipSuccess || (!c.dhidden && !c.dweight))
+        return e;
+    if (a.hs)
+        hipLaunchKernelGGL(lce_scale_kernel, dim3((unsigned)p.rows), dim3(256), 0, s, a);
+    for (size_t first = 0; first < c.V; first += p.piece) {
+        const uint32_t f = (uint32_t)first;
+        with_shape(p.kind, [&](auto shape) {
+            typedef decltype(shape) S;
+            const uint32_t tiles_m = (uint32_t)p.piece / S::M;
+            hipLaunchKernelGGL((lce_d_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads), 0,
+                               s, a, f, p.tiles_n);
+            if (c.dhidden)
+                hipLaunchKernelGGL((lce_dh_kernel<T, S>),
+                                   dim3(p.tiles_d * p.tiles_n, (unsigned)p.splits),
+                                   dim3(S::kThreads), 0, s, a, f, p.tiles_d, p.tiles_n);
+            return 0;
+        });
+        if (c.dweight) {
+            const uint32_t cols = (uint32_t)std::min(p.piece, c.V - first);
+            const auto dw = [&](auto shape) {
+                typedef decltype(shape) S;
+                const uint32_t tiles_m = (uint32_t)((c.D + S::M - 1) / S::M);
+                const uint32_t tiles_n = (cols + S::N - 1) / S::N;
+                hipLaunchKernelGGL((lce_dw_kernel<T, S>), dim3(tiles_m * tiles_n),
+                                   dim3(S::kThreads), 0, s, a, f, tiles_m, tiles_n);
+            };
+            if (p.kind_w == Kind::Mid)
+                dw(MidTile());
+            else
+                dw(BigTile());
+        }
+    }
+    if (c.dhidden)
+        with_shape(p.kind, [&](auto shape) {
+            typedef decltype(shape) S;
+            hipLaunchKernelGGL((lce_dh_finish_kernel<T, S>),
+                               dim3((unsigned)c.rows), dim3(kBlock), 0, s, a, p.tiles_d, p.tiles_n);
+            return 0;
+        });
+    return hipGetLastError();
+}
+
+} // namespace
+
+size_t linear_ce_workspace(LogitType t, const LinearCall& a, const DeviceInfo& dev)
+{
+    return plan_of(t, a, dev, nullptr).bytes;
+}
+
+hipError_t launch_linear_ce(LogitType t, const LinearCall& a, const DeviceInfo& dev,
+                            hipStream_t stream)
+{
+    return t == LogitType::F16 ? run<ElemF16>(t, a, dev, stream) : run<ElemBF16>(t, a, dev, stream);
+}
+
+} // namespace red

@@ -2,7 +2,7 @@
  * reduce.h -- C ABI of libreduce: dense-array reduction on AMD Instinct
  * MI355X (gfx950).
  *
- * Three families of operations:
+ * Four families of operations:
  *
  *   1. A 1-D fp32 vector reduced to one scalar by sum, max or min, with an
  *      accum mode that folds the old destination value into the result
@@ -24,6 +24,12 @@
  *      loss's gradient with respect to the matrix: token log-probabilities,
  *      distillation from a teacher's largest logits, a clipped policy loss
  *      and a preference loss.
+ *
+ *   4. The operators around the output layer whose logits those are: the
+ *      root-mean-square norm of its rows with the residual's addition and an
+ *      8-bit output, the balance loss of a router of experts, and the cross
+ *      entropy of hidden rows against the layer without keeping the logits,
+ *      each with its gradient.
  *
  * Conventions shared by every entry point:
  *
@@ -60,7 +66,8 @@
  *     between runs.
  *   - Workspace.  The calls that combine per-workgroup partials in a second
  *     kernel (1-D, fused, column and column-product calls, row calls
- *     with very long rows or very few rows, and the losses) keep those partials in a
+ *     with very long rows or very few rows, the losses, the norm's gradient
+ *     and the balance loss) keep those partials in a
  *     workspace (16 MiB and 128 KiB of counts, which are zero between
  *     calls) the library allocates on the first such call for a
  *     (device, stream) pair and keeps until red_release_workspace.  For
@@ -108,7 +115,8 @@ enum red_status {
     RED_ERR_NOMEM = 3,   /* the per-stream workspace could not be allocated */
     RED_ERR_HIP = 4,     /* the HIP runtime reported an error */
     RED_ERR_SCRATCH = 5  /* red_sum_max_min_f32_noalloc: the grid would need
-                            more than the static scratch buffer holds */
+                            more than the static scratch buffer holds;
+                            red_linear_ce_*: the workspace is too small */
 };
 
 /* ---------------------------------------------------------------------
@@ -454,6 +462,139 @@ int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size
                              float margin, float smoothing, int average, float* loss, int accum,
                              float* seq_logp, uint16_t* dlogits, size_t ldd,
                              red_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * Around the output layer
+ *
+ * Matrices are row-major f32, f16 or bf16 (16-bit types as uint16_t bit
+ * patterns), aligned to their element size, with a row stride of at least
+ * their columns (where there is one row the stride is not looked at).
+ * Elements between the columns and the stride are neither read nor written.
+ * Values are widened exactly to fp32; every result is rounded once to its
+ * type.  A row with a NaN or an infinity has NaN results and touches no other
+ * row's (it does touch what is summed over rows).  All results are
+ * deterministic.
+ * ------------------------------------------------------------------- */
+
+/* Root-mean-square norm of rows of D values, D <= 16384, with the residual's
+ * addition before it:
+ *   h = x + residual (NULL: x),   rstd = (mean h^2 + eps)^(-1/2),
+ *   y = h rstd weight.
+ * sum (NULL: not wanted) takes h, y the norm, both rounded once from the exact
+ * sum's fp32 value: y does not start from the rounded h.  y8 with scale8 (both
+ * or neither; y or y8 or both must be given) takes the row in 8 bits, OCP
+ * e4m3: scale8[r] = max |y| / 448 and y8 = round(y / scale8[r]), to nearest even; a row
+ * whose largest |y| is below 1e-35 has scale 0 and zeros, and a NaN in y is a
+ * NaN in y8 and does not count for the scale.  rstd (NULL: not wanted) is what
+ * the gradient needs.  The sum of squares is fp64: no finite row overflows.
+ * weight has D values.  eps >= 0 and finite; with eps 0 a row of zeros has NaN.
+ * sum and y may each be x or residual themselves, with the same stride (two
+ * outputs never the same). */
+int red_add_rmsnorm_f32(const float* x, size_t rows, size_t D, size_t ldx,
+                        const float* residual, size_t ldr, const float* weight, float eps,
+                        float* sum, size_t lds, float* y, size_t ldy, uint8_t* y8, size_t ldy8,
+                        float* scale8, float* rstd, red_stream_t stream);
+int red_add_rmsnorm_f16(const uint16_t* x, size_t rows, size_t D, size_t ldx,
+                        const uint16_t* residual, size_t ldr, const uint16_t* weight, float eps,
+                        uint16_t* sum, size_t lds, uint16_t* y, size_t ldy, uint8_t* y8, size_t ldy8,
+                        float* scale8, float* rstd, red_stream_t stream);
+int red_add_rmsnorm_bf16(const uint16_t* x, size_t rows, size_t D, size_t ldx,
+                        const uint16_t* residual, size_t ldr, const uint16_t* weight, float eps,
+                        uint16_t* sum, size_t lds, uint16_t* y, size_t ldy, uint8_t* y8, size_t ldy8,
+                        float* scale8, float* rstd, red_stream_t stream);
+
+/* The gradient of red_add_rmsnorm: with n = h rstd and g = dy weight,
+ *   dx = (g - n mean(g n)) rstd + dsum,   dweight = sum over rows of dy n,
+ * dx being the gradient of x and of the residual alike, dsum (NULL: none) the
+ * gradient that arrives at h past the norm.  h and rstd are the forward call's.
+ * dweight (NULL: not wanted) is fp32; accum != 0 adds to its old values.  dx
+ * may be h, dy or dsum itself, with the same stride.  Uses the stream's
+ * workspace. */
+int red_rmsnorm_grad_f32(const float* h, size_t rows, size_t D, size_t ldh,
+                         const float* weight, const float* rstd, const float* dy, size_t lddy,
+                         const float* dsum, size_t ldds, float* dx, size_t lddx, float* dweight,
+                         int accum, red_stream_t stream);
+int red_rmsnorm_grad_f16(const uint16_t* h, size_t rows, size_t D, size_t ldh,
+                         const uint16_t* weight, const float* rstd, const uint16_t* dy, size_t lddy,
+                         const uint16_t* dsum, size_t ldds, uint16_t* dx, size_t lddx, float* dweight,
+                         int accum, red_stream_t stream);
+int red_rmsnorm_grad_bf16(const uint16_t* h, size_t rows, size_t D, size_t ldh,
+                         const uint16_t* weight, const float* rstd, const uint16_t* dy, size_t lddy,
+                         const uint16_t* dsum, size_t ldds, uint16_t* dx, size_t lddx, float* dweight,
+                         int accum, red_stream_t stream);
+
+/* Balance loss of a router of E experts, E <= 2048, over rows of logits, of
+ * which each row has chosen the K experts experts[r * ldk + k] (one that is
+ * not in [0, E) is padding; one listed twice counts twice; 1 <= K <= 1024,
+ * ldk >= K).  With p_r the softmax of row r and n_e the number of choices of
+ * expert e among the rows that count,
+ *   P_e = sum_r weight[r] p_re,   f_e = n_e / sum n,
+ *   loss = balance_coef E sum_e f_e P_e + z_coef sum_r weight[r] lse_r^2.
+ * weight: one factor per row (NULL: 1 / rows each); a row of weight 0 does not
+ * count: its logits and choices are not looked at and its gradient is 0.
+ * counts takes the n_e, prob (NULL: not wanted) the P_e.  dlogits (NULL: the
+ * loss alone) takes the gradient, for which the counts are constants; it may be
+ * logits itself, with the same stride.  Where nothing was chosen the first term
+ * is 0.  A row with a NaN makes the loss a NaN, and not the other rows'
+ * gradients.  balance_coef and z_coef finite, rows < 2^31.  accum != 0 adds to
+ * the old loss.  Uses the stream's workspace. */
+int red_router_balance_f32(const float* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, float* dlogits, size_t ldd,
+                           red_stream_t stream);
+int red_router_balance_f16(const uint16_t* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, uint16_t* dlogits, size_t ldd,
+                           red_stream_t stream);
+int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_t ld,
+                           const int64_t* experts, size_t K, size_t ldk, const float* weight,
+                           float balance_coef, float z_coef, float* loss, int accum,
+                           int64_t* counts, float* prob, uint16_t* dlogits, size_t ldd,
+                           red_stream_t stream);
+
+/* Cross entropy of hidden rows (rows x D) against an output layer weight
+ * (V x D) and targets, without logits in memory:
+ *   z_v = scale hidden[r] . weight[v],  lse = ln sum_v exp z_v,
+ *   loss = sum_r row_weight[r] (lse - z_target + z_coef lse^2).
+ * row_weight: one factor per row (NULL: 1 / rows each).  A row of weight 0, or
+ * whose target is not in [0, V) (-100, say), does not count: its outputs are 0
+ * and its hidden values are not looked at.  logp takes z_target - lse, lse the
+ * log-sum-exp (NULL: not wanted).  dhidden and dweight (NULL: not wanted) take
+ * the gradients, of the inputs' type; every element of their rows is written.
+ * accum != 0 adds to the old loss.
+ *
+ * Products are of the 16-bit values, summed in fp32.  The gradient of each
+ * logit is rounded to the inputs' type before it is multiplied by weight or
+ * hidden rows: an error of half a step, 2^-9 (bf16) or 2^-12 (f16) of each term
+ * in relative terms.  The logits are computed once for the loss and again, a
+ * piece of the vocabulary at a time, for the gradients.
+ *
+ * D a multiple of 8 and at most 65536; the rows of weight aligned to 16 bytes
+ * (RED_ERR_ALIGN, or RED_ERR_INVALID where ldw is no multiple of 8);
+ * rows <= 2^20, V <= 2^24, ldw <= 2^21; scale positive, z_coef finite.
+ *
+ * workspace: device memory of the caller's, aligned to 256 bytes, whose needed
+ * size red_linear_ce_workspace_* gives (on the device of the call; dhidden,
+ * dweight: whether they are wanted).  It holds nothing between calls; calls
+ * that share one must be ordered.  RED_ERR_SCRATCH where it is too small.  Its
+ * size is about rows D 2 bytes, 8 rows V / 128 or less, and for gradients up to
+ * 256 MiB (more past 65536 rows) and rows D 4. */
+int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
+                      const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
+                      const float* row_weight, float scale, float z_coef, float* loss, int accum,
+                      float* logp, float* lse, uint16_t* dhidden, size_t lddh, uint16_t* dweight,
+                      size_t lddw, void* workspace, size_t workspace_bytes, red_stream_t stream);
+int red_linear_ce_workspace_f16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
+                                size_t* bytes);
+int red_linear_ce_bf16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
+                      const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
+                      const float* row_weight, float scale, float z_coef, float* loss, int accum,
+                      float* logp, float* lse, uint16_t* dhidden, size_t lddh, uint16_t* dweight,
+                      size_t lddw, void* workspace, size_t workspace_bytes, red_stream_t stream);
+int red_linear_ce_workspace_bf16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
+                                size_t* bytes);
 
 /* ---------------------------------------------------------------------
  * Utilities
