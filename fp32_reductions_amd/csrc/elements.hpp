@@ -119,4 +119,41 @@ __device__ __forceinline__ void store_vec(void* p, const u32x4_t& v)
     __builtin_nontemporal_store(u, reinterpret_cast<u32x4u_t*>(p));
 }
 
+// The last `rest` elements of a row (fewer than a vector), packed from its first
+// byte on, zeros behind them: p is the first of them.  Where the row is at least a
+// vector long (`whole`), one load that ends with the row, shifted; elements one by
+// one otherwise.
+template <class T>
+__device__ __forceinline__ u32x4_t load_rest(const typename T::S* p, uint32_t rest, bool whole)
+{
+    typedef unsigned __int128 u128;
+    if (whole) {
+        const u32x4u_t u = *reinterpret_cast<const u32x4u_t*>(p + rest - T::W);
+        const u128 v = __builtin_bit_cast(u128, u32x4_t{u.x, u.y, u.z, u.w});
+        return __builtin_bit_cast(u32x4_t, v >> (8 * sizeof(typename T::S) * (T::W - rest)));
+    }
+    float f[T::W];
+#pragma unroll
+    for (int i = 0; i < T::W; ++i)
+        f[i] = i < (int)rest ? T::widen(p[i]) : 0.0f;
+    return T::pack(f);
+}
+
+// Stores the first `rest` elements of v at p, in pieces of 8, 4 and 2 bytes.
+template <class T>
+__device__ __forceinline__ void store_rest(typename T::S* p, const u32x4_t& v, uint32_t rest)
+{
+    typedef unsigned u32x2u_t __attribute__((ext_vector_type(2), aligned(2)));
+    typedef unsigned u32u_t __attribute__((aligned(2)));
+    const uint32_t bytes = rest * (uint32_t)sizeof(typename T::S);
+    char* q = reinterpret_cast<char*>(p);
+    if (bytes & 8)
+        *reinterpret_cast<u32x2u_t*>(q) = u32x2u_t{v.x, v.y};
+    if (bytes & 4)
+        *reinterpret_cast<u32u_t*>(q + (bytes & 8)) = bytes & 8 ? v.z : v.x;
+    if (bytes & 2)
+        *reinterpret_cast<uint16_t*>(q + (bytes & 12)) =
+            (uint16_t)((bytes & 8) ? ((bytes & 4) ? v.w : v.z) : ((bytes & 4) ? v.y : v.x));
+}
+
 } // namespace red

@@ -33,61 +33,86 @@ constexpr float kTiny8 = 1.0e-35f;
 
 __device__ const u32x4_t kZeroVec = {0, 0, 0, 0};
 
-// Row elements of GT threads with NV vectors each: vector k of thread t is
-// number k GT + t.  Loads past the row's end go to a vector of zeros, without a
-// branch, so that all are in flight at once.
-template <class T, int GT, int NV>
+// A row's threads: 16 or 64 of a wave, or (GT 0) the whole workgroup, whose size
+// the launch chooses.  Each holds NV vectors: vector k of thread t is number
+// k threads + t.  Loads past the row's end go to a vector of zeros, without a
+// branch, so that all are in flight at once; the elements after the last whole
+// vector (`rest`) belong to the thread whose turn it is.
+//
+// STREAM: the rows are aligned to 16 bytes and pass the caches by.  (8192 x 8192
+// bf16 with a residual and 8 bits out 72.5 us so, 81.1 otherwise, 80 with either
+// loads or stores alone; unaligned rows, whose lines two loads share, were slower:
+// 1531 x 5003 f32 20.8 against 16.9.)
+template <class T, int GT, int NV, bool STREAM>
 struct Row {
     static constexpr int W = T::W;
-    uint32_t t, nvec, rest; // rest: elements after the whole vectors
-    __device__ __forceinline__ Row(uint32_t D) : t(threadIdx.x % GT), nvec(D / W), rest(D % W) {}
+    uint32_t threads, t, nvec, rest;
+    __device__ __forceinline__ Row(uint32_t D)
+        : threads(GT ? GT : blockDim.x), t(GT ? threadIdx.x % GT : threadIdx.x), nvec(D / W),
+          rest(D % W)
+    {
+    }
 
     __device__ __forceinline__ void load(const void* row, u32x4_t (&v)[NV]) const
+    {
+        load_as<STREAM>(row, v);
+    }
+    // What other workgroups read too.
+    __device__ __forceinline__ void load_again(const void* row, u32x4_t (&v)[NV]) const
+    {
+        load_as<false>(row, v);
+    }
+    template <bool PASS>
+    __device__ __forceinline__ void load_as(const void* row, u32x4_t (&v)[NV]) const
     {
         const typename T::S* p = static_cast<const typename T::S*>(row);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const uint32_t j = k * GT + t;
+            const uint32_t j = k * threads + t;
             const u32x4u_t* at = j < nvec ? reinterpret_cast<const u32x4u_t*>(p) + j
                                           : reinterpret_cast<const u32x4u_t*>(&kZeroVec);
-            const u32x4u_t u = *at;
+            u32x4u_t u;
+            if constexpr (PASS)
+                u = __builtin_nontemporal_load(at);
+            else
+                u = *at;
             v[k] = u32x4_t{u.x, u.y, u.z, u.w};
         }
         if (rest) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (k * GT + t == nvec) {
-                    float f[W];
-#pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        f[i] = i < (int)rest ? T::widen(p[(size_t)nvec * W + i]) : 0.0f;
-                    v[k] = T::pack(f);
-                }
+                if (k * threads + t == nvec)
+                    v[k] = load_rest<T>(p + (size_t)nvec * W, rest, nvec > 0);
+        }
+    }
+    // Vector k of the row.
+    __device__ __forceinline__ void store(void* row, int k, const float (&f)[W]) const
+    {
+        typename T::S* p = static_cast<typename T::S*>(row);
+        const uint32_t j = k * threads + t;
+        const u32x4_t v = T::pack(f);
+        if (j < nvec) {
+            u32x4u_t* to = reinterpret_cast<u32x4u_t*>(p) + j;
+            if constexpr (STREAM)
+                __builtin_nontemporal_store(u32x4u_t{v.x, v.y, v.z, v.w}, to);
+            else
+                *to = u32x4u_t{v.x, v.y, v.z, v.w};
+        } else if (rest && j == nvec) {
+            store_rest<T>(p + (size_t)nvec * W, v, rest);
         }
     }
     __device__ __forceinline__ void store(void* row, const float (&f)[NV][W]) const
     {
-        typename T::S* p = static_cast<typename T::S*>(row);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const uint32_t j = k * GT + t;
-            if (j < nvec) {
-                const u32x4_t v = T::pack(f[k]);
-                *(reinterpret_cast<u32x4u_t*>(p) + j) = u32x4u_t{v.x, v.y, v.z, v.w};
-            } else if (rest && j == nvec) {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (i < (int)rest)
-                        p[(size_t)nvec * W + i] = T::narrow(f[k][i]);
-            }
-        }
+        for (int k = 0; k < NV; ++k)
+            store(row, k, f[k]);
     }
     __device__ __forceinline__ void store8(uint8_t* p, const float (&f)[NV][W]) const
     {
         typedef unsigned word_t __attribute__((aligned(1)));
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const uint32_t j = k * GT + t;
+            const uint32_t j = k * threads + t;
             unsigned q[W / 4];
 #pragma unroll
             for (int i = 0; i < W / 4; ++i) {
@@ -108,25 +133,25 @@ struct Row {
     }
 };
 
-// Sums and maxima over the GT threads of a row, in every one of them.  `lds`
-// holds a value per wave; a use is followed by a barrier before the next.
+// Sums and maxima over the threads of a row, in every one of them.  `lds` holds a
+// value per wave; a use is followed by a barrier before the next.
+constexpr int kMostWaves = 16;
 template <int GT>
 __device__ __forceinline__ double row_sum(double v, double* lds)
 {
-    if constexpr (GT < kWave) {
+    if constexpr (GT && GT < kWave) {
 #pragma unroll
         for (int d = GT / 2; d > 0; d /= 2)
             v += __shfl_xor(v, d);
         return v;
     } else {
         v = wave_sum64(v);
-        if constexpr (GT > kWave) {
+        if constexpr (GT == 0) {
             if (threadIdx.x % kWave == 0)
                 lds[threadIdx.x / kWave] = v;
             __syncthreads();
             v = 0.0;
-#pragma unroll
-            for (int k = 0; k < GT / kWave; ++k)
+            for (uint32_t k = 0; k < blockDim.x / kWave; ++k)
                 v += lds[k];
         }
         return v;
@@ -136,48 +161,60 @@ __device__ __forceinline__ double row_sum(double v, double* lds)
 template <int GT>
 __device__ __forceinline__ float row_max(float v, float* lds)
 {
-    if constexpr (GT < kWave) {
+    if constexpr (GT && GT < kWave) {
 #pragma unroll
         for (int d = GT / 2; d > 0; d /= 2)
             v = fmaxf(v, __shfl_xor(v, d));
         return v;
     } else {
         v = wave_reduce<OpMax>(v);
-        if constexpr (GT > kWave) {
+        if constexpr (GT == 0) {
             if (threadIdx.x % kWave == 0)
                 lds[threadIdx.x / kWave] = v;
             __syncthreads();
             v = lds[0];
-#pragma unroll
-            for (int k = 1; k < GT / kWave; ++k)
+            for (uint32_t k = 1; k < blockDim.x / kWave; ++k)
                 v = fmaxf(v, lds[k]);
         }
         return v;
     }
 }
 
+// Whether a matrix's rows are all aligned to 16 bytes (ld: bytes).
+struct Aligned {
+    size_t rows;
+    bool operator()(const void* p, size_t ld) const
+    {
+        return !p || ((uintptr_t)p % 16 == 0 && (rows == 1 || ld % 16 == 0));
+    }
+};
+
 __device__ __forceinline__ float reciprocal_root(double ms) { return (float)(1.0 / sqrt(ms)); }
 
 template <int GT>
-constexpr int rows_per_block() { return GT < kBlock ? kBlock / GT : 1; }
+constexpr int rows_per_block() { return GT ? kBlock / GT : 1; }
+template <int GT>
+constexpr int most_threads() { return GT ? kBlock : 1024; }
 
-template <class T, int GT, int NV>
-__global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void add_rmsnorm_kernel(NormCall a)
+template <class T, int GT, int NV, bool STREAM>
+__global__ __launch_bounds__(NV == 4 && T::W == 8 ? 512 : most_threads<GT>()) void
+add_rmsnorm_kernel(NormCall a)
 {
-    constexpr int W = T::W, RB = rows_per_block<GT>(), WAVES = GT > kWave ? GT / kWave : 1;
+    constexpr int W = T::W, RB = rows_per_block<GT>();
     typedef typename T::S S;
-    __shared__ double lds_sum[WAVES];
-    __shared__ float lds_max[WAVES];
-    const Row<T, GT, NV> at((uint32_t)a.D);
+    __shared__ double lds_sum[kMostWaves];
+    __shared__ float lds_max[kMostWaves];
+    const Row<T, GT, NV, STREAM> at((uint32_t)a.D);
     const size_t step = (size_t)gridDim.x * RB;
-    for (size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT; r < a.rows; r += step) {
+    for (size_t r = (size_t)blockIdx.x * RB + (GT ? threadIdx.x / (GT ? GT : 1) : 0); r < a.rows;
+         r += step) {
         u32x4_t v[NV], w[NV];
         float f[NV][W];
         at.load(static_cast<const S*>(a.x) + r * a.ldx, v);
         if (a.residual) {
             u32x4_t u[NV];
             at.load(static_cast<const S*>(a.residual) + r * a.ldr, u);
-            at.load(a.weight, w);
+            at.load_again(a.weight, w);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float e[W];
@@ -188,7 +225,7 @@ __global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void add_rmsnorm_kernel(
                     f[k][i] += e[i];
             }
         } else {
-            at.load(a.weight, w);
+            at.load_again(a.weight, w);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 T::unpack(v[k], f[k]);
@@ -236,7 +273,7 @@ __global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void add_rmsnorm_kernel(
                     f[k][i] *= inverse;
             at.store8(a.y8 + r * a.ldy8, f);
         }
-        if constexpr (GT > kWave)
+        if constexpr (GT == 0)
             __syncthreads(); // before lds_sum and lds_max are written again
     }
 }
@@ -247,24 +284,31 @@ struct GradArgs {
     int last;       // one workgroup: it writes the gradient itself
 };
 
-template <class T, int GT, int NV>
-__global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void rmsnorm_grad_kernel(GradArgs args)
+template <class T, int GT, int NV, bool STREAM>
+__global__ __launch_bounds__((most_threads<GT>())) void rmsnorm_grad_kernel(GradArgs args)
 {
-    constexpr int W = T::W, RB = rows_per_block<GT>(), WAVES = GT > kWave ? GT / kWave : 1;
+    constexpr int W = T::W, RB = rows_per_block<GT>();
     typedef typename T::S S;
     const NormGradCall& a = args.c;
-    __shared__ double lds_sum[2][WAVES];
-    const Row<T, GT, NV> at((uint32_t)a.D);
+    __shared__ double lds_sum[2][kMostWaves];
+    const Row<T, GT, NV, STREAM> at((uint32_t)a.D);
     const size_t step = (size_t)gridDim.x * RB;
+    // Four vectors a thread leave no registers for the weight between rows, nor for
+    // the third input while a row's sum is waited for.
+    constexpr bool kFull = NV == 4;
     u32x4_t w[NV];
-    at.load(a.weight, w);
+    if (!kFull)
+        at.load_again(a.weight, w);
     float acc[NV][W] = {};
     int turn = 0;
-    for (size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT; r < a.rows; r += step) {
+    for (size_t r = (size_t)blockIdx.x * RB + (GT ? threadIdx.x / (GT ? GT : 1) : 0); r < a.rows;
+         r += step) {
         u32x4_t hv[NV], gv[NV], sv[NV];
         at.load(static_cast<const S*>(a.h) + r * a.ldh, hv);
         at.load(static_cast<const S*>(a.dy) + r * a.lddy, gv);
-        if (a.dsum)
+        if (kFull)
+            at.load_again(a.weight, w);
+        if (!kFull && a.dsum)
             at.load(static_cast<const S*>(a.dsum) + r * a.ldds, sv);
         const float rstd = a.rstd[r];
         double c = 0.0;
@@ -284,24 +328,25 @@ __global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void rmsnorm_grad_kernel
         c = row_sum<GT>(c, lds_sum[turn]);
         turn ^= 1; // the next row's sums go elsewhere: no second barrier
         const float mean = (float)(c / (double)a.D);
-        float d[NV][W];
+        if (kFull && a.dsum)
+            at.load(static_cast<const S*>(a.dsum) + r * a.ldds, sv);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float n[W], g[W], e[W];
+            float n[W], g[W], e[W], d[W];
             T::unpack(hv[k], n);
             T::unpack(gv[k], g);
             T::unpack(w[k], e);
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                d[k][i] = (g[i] * e[i] - n[i] * rstd * mean) * rstd;
+                d[i] = (g[i] * e[i] - n[i] * rstd * mean) * rstd;
             if (a.dsum) {
                 T::unpack(sv[k], e);
 #pragma unroll
                 for (int i = 0; i < W; ++i)
-                    d[k][i] += e[i];
+                    d[i] += e[i];
             }
+            at.store(static_cast<S*>(a.dx) + r * a.lddx, k, d);
         }
-        at.store(static_cast<S*>(a.dx) + r * a.lddx, d);
     }
     if (!args.partial)
         return;
@@ -328,7 +373,7 @@ __global__ __launch_bounds__(GT < kBlock ? kBlock : GT) void rmsnorm_grad_kernel
     float* out = args.last ? a.dweight : args.partial + (size_t)blockIdx.x * a.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const uint32_t first = (k * GT + at.t) * W;
+        const uint32_t first = (k * at.threads + at.t) * W;
 #pragma unroll
         for (int i = 0; i < W; ++i)
             if (first + i < a.D)
@@ -363,27 +408,40 @@ column_finish_kernel(const float* __restrict__ partial, uint32_t n, uint32_t D, 
     dweight[j] = (float)((accum ? (double)dweight[j] : 0.0) + v);
 }
 
-// Workgroups of the gradient kernel: enough to fill the device twice over, and
-// no more, since each leaves a row of column sums.
-constexpr unsigned kGradGroupsPerCu = 2;
+// Waves of the gradient kernel for each compute unit: about what fits at once, and
+// no more, since each workgroup leaves a row of column sums.  (16384 x 4096 bf16:
+// 95.7 us with 16, 108 with 32.  Fewer, with the next row requested ahead, took 97.8
+// and needed twice the registers.)
+constexpr unsigned kGradWavesPerCu = 16;
 
 template <class T, int GT, int NV>
 struct Shape {
-    static constexpr int kThreads = GT < kBlock ? kBlock : GT;
-    static hipError_t norm(const NormCall& a, const DeviceInfo&, hipStream_t s)
+    // Threads of a workgroup for rows of `vecs` vectors.
+    static unsigned threads(size_t vecs)
+    {
+        return GT ? (unsigned)kBlock : (unsigned)(((vecs + NV - 1) / NV + kWave - 1) / kWave * kWave);
+    }
+    static hipError_t norm(const NormCall& a, size_t vecs, hipStream_t s)
     {
         constexpr size_t RB = rows_per_block<GT>();
-        const size_t groups = std::min((a.rows + RB - 1) / RB, size_t(1) << 20);
-        hipLaunchKernelGGL((add_rmsnorm_kernel<T, GT, NV>), dim3((unsigned)groups),
-                           dim3(kThreads), 0, s, a);
+        const unsigned groups = (unsigned)std::min((a.rows + RB - 1) / RB, size_t(1) << 20);
+        const Aligned al = {a.rows};
+        if (al(a.x, a.ldx * sizeof(typename T::S)) && al(a.residual, a.ldr * sizeof(typename T::S)) &&
+            al(a.sum, a.lds * sizeof(typename T::S)) && al(a.y, a.ldy * sizeof(typename T::S)))
+            hipLaunchKernelGGL((add_rmsnorm_kernel<T, GT, NV, true>), dim3(groups),
+                               dim3(threads(vecs)), 0, s, a);
+        else
+            hipLaunchKernelGGL((add_rmsnorm_kernel<T, GT, NV, false>), dim3(groups),
+                               dim3(threads(vecs)), 0, s, a);
         return hipGetLastError();
     }
-    static hipError_t grad(const NormGradCall& a, const DeviceInfo& dev, const Workspace& ws,
-                           hipStream_t s)
+    static hipError_t grad(const NormGradCall& a, size_t vecs, const DeviceInfo& dev,
+                           const Workspace& ws, hipStream_t s)
     {
         constexpr size_t RB = rows_per_block<GT>();
         size_t groups = (a.rows + RB - 1) / RB;
-        groups = std::min(groups, (size_t)dev.cus * kGradGroupsPerCu * (1024 / kThreads));
+        groups = std::min(groups, (size_t)dev.cus *
+                                      std::max(1u, kGradWavesPerCu * kWave / threads(vecs)));
         if (a.dweight)
             groups = std::min(groups, ws.partial_bytes / (a.D * sizeof(float)));
         GradArgs args = {a, a.dweight ? static_cast<float*>(ws.partials) : nullptr, 0};
@@ -391,8 +449,14 @@ struct Shape {
             args.last = 1;
             args.partial = a.dweight;
         }
-        hipLaunchKernelGGL((rmsnorm_grad_kernel<T, GT, NV>), dim3((unsigned)groups),
-                           dim3(kThreads), 0, s, args);
+        const Aligned al = {a.rows};
+        if (al(a.h, a.ldh * sizeof(typename T::S)) && al(a.dy, a.lddy * sizeof(typename T::S)) &&
+            al(a.dsum, a.ldds * sizeof(typename T::S)) && al(a.dx, a.lddx * sizeof(typename T::S)))
+            hipLaunchKernelGGL((rmsnorm_grad_kernel<T, GT, NV, true>), dim3((unsigned)groups),
+                               dim3(threads(vecs)), 0, s, args);
+        else
+            hipLaunchKernelGGL((rmsnorm_grad_kernel<T, GT, NV, false>), dim3((unsigned)groups),
+                               dim3(threads(vecs)), 0, s, args);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !a.dweight || groups == 1)
             return e;
@@ -404,58 +468,68 @@ struct Shape {
     }
 };
 
-// The threads that share a row: up to four vectors each.  Few rows get one
-// vector a thread, as far as that goes: what counts then is one row's time.
+// The threads that share a row and the vectors of each.  The gradient, and the norm
+// of few rows, whose time is that of one row, take one vector a thread as far as
+// that goes ("wide"); the norm of many two, or four where a row is long (8192 x 8192
+// bf16: 1024 threads with one 134 us, 512 with two 75.7, 256 with four 72.5).
 template <class T, class F>
-hipError_t by_shape(size_t rows, size_t D, const DeviceInfo& dev, F f)
+hipError_t by_wide_shape(size_t vecs, F f)
+{
+    if (vecs <= 16)
+        return f(Shape<T, 16, 1>(), vecs);
+    if (vecs <= 64)
+        return f(Shape<T, 64, 1>(), vecs);
+    if (vecs <= 1024)
+        return f(Shape<T, 0, 1>(), vecs);
+    if constexpr (T::W == 4)
+        if (vecs > 2048)
+            return f(Shape<T, 0, 4>(), vecs);
+    return f(Shape<T, 0, 2>(), vecs);
+}
+template <class T, class F>
+hipError_t by_shape(bool wide, size_t D, F f)
 {
     const size_t vecs = (D + T::W - 1) / T::W;
-    const bool few = rows <= (size_t)dev.cus;
-    if (vecs <= 16)
-        return f(Shape<T, 16, 1>());
-    if (vecs <= 64)
-        return f(Shape<T, 64, 1>());
-    if (vecs <= 128 && !few)
-        return f(Shape<T, 64, 2>());
-    if (vecs <= 256)
-        return f(Shape<T, 256, 1>());
-    if (few && vecs <= 1024)
-        return f(Shape<T, 1024, 1>());
-    if (vecs <= 512)
-        return f(Shape<T, 256, 2>());
-    if (vecs <= 1024)
-        return f(Shape<T, 256, 4>());
-    if (few && vecs <= 2048)
-        return f(Shape<T, 1024, 2>());
-    if (vecs <= 2048)
-        return f(Shape<T, 512, 4>());
-    if constexpr (T::W == 4)
-        return f(Shape<T, 1024, 4>());
-    return hipErrorInvalidValue; // not reached: D <= kNormColsMax
+    if (wide || vecs <= 64)
+        return by_wide_shape<T>(vecs, f);
+    if (vecs <= 128)
+        return f(Shape<T, 64, 2>(), vecs);
+    if (vecs <= 640)
+        return f(Shape<T, 0, 2>(), vecs);
+    return f(Shape<T, 0, 4>(), vecs);
 }
-static_assert(kNormColsMax == 4096 * 4 && kNormColsMax == 2048 * 8, "the longest row's vectors");
+template <class T, class F>
+hipError_t by_grad_shape(size_t D, F f)
+{
+    return by_wide_shape<T>((D + T::W - 1) / T::W, f);
+}
+static_assert(kNormColsMax == 1024 * 4 * 4 && kNormColsMax == 1024 * 2 * 8 &&
+                  kNormColsMax == 512 * 4 * 8,
+              "the longest row's vectors");
 
 } // namespace
-
-#define RED_NORM_BY_TYPE(t, call)                       \
-    switch (t) {                                        \
-    case LogitType::F32: return by_shape<ElemF32> call; \
-    case LogitType::F16: return by_shape<ElemF16> call; \
-    default: return by_shape<ElemBF16> call;            \
-    }
 
 hipError_t launch_add_rmsnorm(LogitType t, const NormCall& a, const DeviceInfo& dev,
                               hipStream_t stream)
 {
-    const auto f = [&](auto shape) { return shape.norm(a, dev, stream); };
-    RED_NORM_BY_TYPE(t, (a.rows, a.D, dev, f))
+    const bool wide = a.rows <= (size_t)dev.cus;
+    const auto f = [&](auto shape, size_t vecs) { return shape.norm(a, vecs, stream); };
+    switch (t) {
+    case LogitType::F32: return by_shape<ElemF32>(wide, a.D, f);
+    case LogitType::F16: return by_shape<ElemF16>(wide, a.D, f);
+    default: return by_shape<ElemBF16>(wide, a.D, f);
+    }
 }
 
 hipError_t launch_rmsnorm_grad(LogitType t, const NormGradCall& a, const DeviceInfo& dev,
                                const Workspace& ws, hipStream_t stream)
 {
-    const auto f = [&](auto shape) { return shape.grad(a, dev, ws, stream); };
-    RED_NORM_BY_TYPE(t, (a.rows, a.D, dev, f))
+    const auto f = [&](auto shape, size_t vecs) { return shape.grad(a, vecs, dev, ws, stream); };
+    switch (t) {
+    case LogitType::F32: return by_grad_shape<ElemF32>(a.D, f);
+    case LogitType::F16: return by_grad_shape<ElemF16>(a.D, f);
+    default: return by_grad_shape<ElemBF16>(a.D, f);
+    }
 }
 
 } // namespace red

@@ -9,11 +9,16 @@
 // A row is short (its experts), and the rows are many: 4, 16 or 64 lanes share
 // one, and a lane keeps the column sums of its experts in registers over the
 // rows that it takes.  Counts are integer atomics in LDS, whose order changes
-// nothing.  The gradient needs every row's counts, so there are three steps:
-// sums of each workgroup's rows, their sum (in fp64 and in order) with the loss,
-// and the gradient, which reads the logits again, from a cache in most sizes,
-// and takes each row's softmax anew (kept, it would cost as many bytes).  Where
-// one workgroup holds all rows at once the three are one kernel.
+// nothing.  The gradient needs every row's counts, so there are two kernels: the
+// sums of each workgroup's rows, which the last of 16 workgroups to arrive adds
+// up for its team, and the gradient, whose workgroups each add up the teams (a
+// few KB), and which reads the logits again, from a cache in most sizes, and takes
+// each row's softmax anew (kept, it would cost as many bytes).  A kernel of its
+// own between the two, of one workgroup, took 13.6 of 44 us (65536 x 128 f32).
+// Where one workgroup holds all rows at once there is one kernel.
+//
+// The arrivals rest on what gfx950 does with device-scope stores and counts; see
+// rowloss_join.hpp.
 #include <algorithm>
 
 #include "elements.hpp"
@@ -27,12 +32,19 @@ constexpr int kThreads = 1024; // a workgroup of the sums and of the gradient
 constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr float kLn2f = 0.6931471805599453f;
 
+// Workgroups whose sums one of them adds up, and the most teams of them.
+constexpr uint32_t kTeam = 16, kTeams = 32;
+static_assert(kTeams * kCountStride <= kCounterWords, "a count for each team");
+
 struct RouterArgs {
     RouterCall c;
-    float* prob_part;    // groups x E
-    unsigned* count_part; // groups x E
-    double* z_part;      // groups
-    float* q;            // E
+    float* prob_part;               // groups x E
+    unsigned* count_part;           // groups x E
+    double* z_part;                 // groups
+    double* team_prob;              // teams x E
+    unsigned long long* team_count; // teams x E
+    double* team_z;                 // teams
+    unsigned* arrivals;             // of each team's workgroups
     uint32_t groups;
 };
 
@@ -63,24 +75,31 @@ struct RouterRow {
     static constexpr int W = T::W;
     uint32_t t, nvec, rest;
     __device__ __forceinline__ RouterRow(uint32_t E) : t(threadIdx.x % GT), nvec(E / W), rest(E % W) {}
-    // Elements of the row, -inf past its end.
-    __device__ __forceinline__ void load(const typename T::S* p, float (&f)[NV][W]) const
+    // The row's vectors as they are in memory; past its end, anything.
+    __device__ __forceinline__ void load(const typename T::S* p, u32x4_t (&v)[NV]) const
     {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const uint32_t j = k * GT + t;
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                f[k][i] = -INFINITY;
             if (j < nvec) {
                 const u32x4u_t u = reinterpret_cast<const u32x4u_t*>(p)[j];
-                T::unpack(u32x4_t{u.x, u.y, u.z, u.w}, f[k]);
-            } else if (j == nvec) {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (i < (int)rest)
-                        f[k][i] = T::widen(p[(size_t)nvec * W + i]);
+                v[k] = u32x4_t{u.x, u.y, u.z, u.w};
+            } else if (rest && j == nvec) {
+                v[k] = load_rest<T>(p + (size_t)nvec * W, rest, nvec > 0);
             }
+        }
+    }
+    // Its elements, -inf past its end.
+    __device__ __forceinline__ void unpack(const u32x4_t (&v)[NV], float (&f)[NV][W]) const
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const uint32_t j = k * GT + t;
+            const int here = j < nvec ? W : j == nvec ? (int)rest : 0;
+            T::unpack(v[k], f[k]);
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                f[k][i] = i < here ? f[k][i] : -INFINITY;
         }
     }
     __device__ __forceinline__ void store(typename T::S* p, const float (&f)[NV][W]) const
@@ -88,15 +107,11 @@ struct RouterRow {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const uint32_t j = k * GT + t;
-            if (j < nvec) {
-                const u32x4_t v = T::pack(f[k]);
+            const u32x4_t v = T::pack(f[k]);
+            if (j < nvec)
                 reinterpret_cast<u32x4u_t*>(p)[j] = u32x4u_t{v.x, v.y, v.z, v.w};
-            } else if (j == nvec) {
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if (i < (int)rest)
-                        p[(size_t)nvec * W + i] = T::narrow(f[k][i]);
-            }
+            else if (rest && j == nvec)
+                store_rest<T>(p + (size_t)nvec * W, v, rest);
         }
     }
 };
@@ -129,34 +144,101 @@ __device__ __forceinline__ float row_weight(const RouterCall& c, size_t r)
     return c.weight ? c.weight[r] : 1.0f / (float)c.m.rows;
 }
 
-// Step one, by every workgroup: its rows' sums to the workspace.
-template <class T, int GT, int NV>
-__device__ __forceinline__ void sum_rows(const RouterArgs& a, unsigned* lds_count, float* lds_prob)
+// What a workgroup keeps in LDS: its counts, and each wave's column sums.
+template <class T>
+struct RouterLds {
+    unsigned* count; // E
+    float* prob;     // waves x E
+    static size_t bytes(size_t E, int waves) { return E * 4 * (1 + waves); }
+    __device__ __forceinline__ RouterLds(unsigned* lds, uint32_t E)
+        : count(lds), prob(reinterpret_cast<float*>(lds + E))
+    {
+    }
+};
+
+// A row's choices into the counts; `first` is this lane's first, loaded before.
+__device__ __forceinline__ int64_t first_choice(const RouterCall& c, size_t r, uint32_t t)
 {
-    constexpr int W = T::W, RB = kThreads / GT;
+    return t < c.K ? c.experts[r * c.ldk + t] : -1;
+}
+template <int GT>
+__device__ __forceinline__ void count_choices(const RouterCall& c, size_t r, uint32_t t,
+                                              int64_t first, unsigned* count)
+{
+    for (uint32_t k = t; k < c.K; k += GT) {
+        const int64_t e = k == t ? first : c.experts[r * c.ldk + k];
+        if (e >= 0 && e < (int64_t)c.m.V)
+            atomicAdd(&count[e], 1u);
+    }
+}
+
+// The column sums of a wave's lanes that own the same experts, to LDS.
+template <int GT, int NV, int W>
+__device__ __forceinline__ void put_columns(float (&acc)[NV][W], uint32_t t, uint32_t E, float* prob)
+{
+    const uint32_t lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+#pragma unroll
+            for (int d = GT; d < kWave; d *= 2)
+                acc[k][i] += __shfl_xor(acc[k][i], d);
+            const uint32_t e = (k * GT + t) * W + i;
+            if (lane < GT && e < E)
+                prob[threadIdx.x / kWave * E + e] = acc[k][i];
+        }
+}
+
+// Step one, by every workgroup: the sums of its rows, to the workspace, where
+// the last of kTeam workgroups to arrive adds up the team's, in order.
+template <class T, int GT, int NV>
+__global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
+{
+    extern __shared__ unsigned lds[];
+    constexpr int W = T::W, RB = kThreads / GT, WAVES = kThreads / kWave;
     const RouterCall& c = a.c;
     const uint32_t E = (uint32_t)c.m.V;
+    const RouterLds<T> mine(lds, E);
     const RouterRow<T, GT, NV> at(E);
-    __shared__ double lds_z[kThreads / kWave];
-    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
-        lds_count[e] = 0;
-        lds_prob[e] = 0.0f;
-    }
+    __shared__ double lds_z[WAVES];
+    __shared__ unsigned lds_before;
+    for (uint32_t e = threadIdx.x; e < E; e += kThreads)
+        mine.count[e] = 0;
     __syncthreads();
     float acc[NV][W] = {};
     double zsum = 0.0;
-    for (size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT; r < c.m.rows;
-         r += (size_t)a.groups * RB) {
-        const float w = row_weight(c, r);
+    const size_t step = (size_t)a.groups * RB;
+    // The next row is requested before this one is worked on (not where a row takes
+    // a quarter of the registers).
+    constexpr bool kAhead = NV < 8;
+    size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT;
+    u32x4_t next[NV] = {};
+    float wn = 0.0f;
+    int64_t en = -1;
+    const auto request = [&](size_t row) {
+        wn = row_weight(c, row);
+        en = first_choice(c, row, at.t);
+        at.load(static_cast<const typename T::S*>(c.m.z) + row * c.m.ld, next);
+    };
+    if (kAhead && r < c.m.rows)
+        request(r);
+    for (; r < c.m.rows; r += step) {
+        if (!kAhead)
+            request(r);
+        u32x4_t v[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            v[k] = next[k];
+        const float w = wn;
+        const int64_t chosen = en;
+        if (kAhead && r + step < c.m.rows)
+            request(r + step);
         if (w == 0.0f)
             continue;
         float f[NV][W], m, s;
-        at.load(static_cast<const typename T::S*>(c.m.z) + r * c.m.ld, f);
-        for (uint32_t k = at.t; k < c.K; k += GT) {
-            const int64_t e = c.experts[r * c.ldk + k];
-            if (e >= 0 && e < (int64_t)E)
-                atomicAdd(&lds_count[e], 1u);
-        }
+        count_choices<GT>(c, r, at.t, chosen, mine.count);
+        at.unpack(v, f);
         exponentials<GT>(f, m, s);
         const float scale = w / s;
 #pragma unroll
@@ -169,224 +251,349 @@ __device__ __forceinline__ void sum_rows(const RouterArgs& a, unsigned* lds_coun
             zsum += (double)w * lse * lse;
         }
     }
-    // The lanes of a wave that own the same experts, then the waves in order.
+    put_columns<GT>(acc, at.t, E, mine.prob);
+    zsum = wave_sum64(zsum);
+    if (threadIdx.x % kWave == 0)
+        lds_z[threadIdx.x / kWave] = zsum;
+    __syncthreads();
+    const uint32_t g = blockIdx.x;
+    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
+        float p = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k)
+            p += mine.prob[k * E + e];
+        store_shared(a.prob_part + (size_t)g * E + e, p);
+        store_shared(reinterpret_cast<float*>(a.count_part + (size_t)g * E + e),
+                     __uint_as_float(mine.count[e]));
+    }
+    if (threadIdx.x == 0) {
+        double v = 0.0;
+        for (int k = 0; k < WAVES; ++k)
+            v += lds_z[k];
+        store_shared(a.z_part + g, v);
+    }
+    // Every thread's stores have arrived before its workgroup is counted.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    const uint32_t team = g / kTeam, first = team * kTeam;
+    const uint32_t size = a.groups - first < kTeam ? a.groups - first : kTeam;
+    unsigned* count = a.arrivals + team * kCountStride;
+    if (threadIdx.x == 0)
+        lds_before = count_shared(count);
+    __syncthreads();
+    if (lds_before != size - 1)
+        return;
+    if (threadIdx.x == 0)
+        clear_shared(count);
+    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
+        double sum = 0.0;
+        unsigned long long chosen = 0;
+        constexpr uint32_t kAtOnce = 8;
+        for (uint32_t from = 0; from < size; from += kAtOnce) {
+            float p[kAtOnce];
+            unsigned n[kAtOnce];
+#pragma unroll
+            for (uint32_t k = 0; k < kAtOnce; ++k) {
+                const size_t i = (size_t)(first + (from + k < size ? from + k : 0)) * E + e;
+                p[k] = load_shared(a.prob_part + i);
+                n[k] = __float_as_uint(load_shared(reinterpret_cast<const float*>(a.count_part + i)));
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kAtOnce; ++k) {
+                sum += from + k < size ? (double)p[k] : 0.0;
+                chosen += from + k < size ? n[k] : 0;
+            }
+        }
+        a.team_prob[(size_t)team * E + e] = sum;
+        a.team_count[(size_t)team * E + e] = chosen;
+    }
+    if (threadIdx.x == 0) {
+        double v = 0.0;
+        for (uint32_t k = 0; k < size; ++k)
+            v += load_shared(a.z_part + first + k);
+        a.team_z[team] = v;
+    }
+}
+
+__device__ __forceinline__ unsigned long long block_total(unsigned long long v, unsigned long long* lds)
+{
+    for (int d = 1; d < kWave; d *= 2)
+        v += __shfl_xor(v, d);
+    if (threadIdx.x % kWave == 0)
+        lds[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0;
+    for (uint32_t k = 0; k < blockDim.x / kWave; ++k)
+        v += lds[k];
+    return v;
+}
+__device__ __forceinline__ double block_total(double v, double* lds)
+{
+    v = wave_sum64(v);
+    if (threadIdx.x % kWave == 0)
+        lds[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0.0;
+    for (uint32_t k = 0; k < blockDim.x / kWave; ++k)
+        v += lds[k];
+    return v;
+}
+
+// Experts of a thread that joins, kThreads apart.
+constexpr int kJoined = (int)(kRouterExpertsMax / kThreads);
+
+// The factors q from the counts n of thread's experts, to LDS; where `tell`, the
+// outputs too, from the probabilities and the threads' parts z of the sum of
+// w lse^2.
+template <class Prob>
+__device__ __forceinline__ void join(const RouterCall& c, const unsigned long long (&n)[kJoined],
+                                     bool tell, Prob prob, double z, float* q)
+{
+    __shared__ unsigned long long lds_n[kThreads / kWave];
+    __shared__ double lds_p[kThreads / kWave];
+    const uint32_t E = (uint32_t)c.m.V;
+    unsigned long long total = 0;
+#pragma unroll
+    for (int k = 0; k < kJoined; ++k)
+        total += n[k];
+    total = block_total(total, lds_n);
+    const double b = total ? (double)c.balance * (double)E / (double)total : 0.0;
+    double part = 0.0;
+#pragma unroll
+    for (int k = 0; k < kJoined; ++k) {
+        const uint32_t e = threadIdx.x + k * kThreads;
+        if (e >= E)
+            break;
+        const double qe = b * (double)n[k];
+        q[e] = (float)qe;
+        if (tell) {
+            const double p = prob(e);
+            part += total ? qe * p : 0.0; // without a choice p has no part in the loss
+            c.counts[e] = (int64_t)n[k];
+            if (c.prob)
+                c.prob[e] = (float)p;
+        }
+    }
+    if (tell) {
+        part += c.z != 0.0f ? (double)c.z * z : 0.0;
+        part = block_total(part, lds_p);
+        if (threadIdx.x == 0)
+            c.loss[0] = (float)((c.accum ? (double)c.loss[0] : 0.0) + part);
+    }
+    __syncthreads();
+}
+
+// The gradient from a row's exponentials, with the factors q(k, i).
+template <int GT, int NV, int W, class Q>
+__device__ __forceinline__ void gradient(const RouterCall& c, float (&f)[NV][W], float m, float s,
+                                         float w, Q q)
+{
+    float dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int d = GT; d < kWave; d *= 2)
-                acc[k][i] += __shfl_xor(acc[k][i], d);
-    zsum = wave_sum64(zsum);
-    const uint32_t wave = threadIdx.x / kWave;
-    if (threadIdx.x % kWave == 0)
-        lds_z[wave] = zsum;
-    for (uint32_t turn = 0; turn < kThreads / kWave; ++turn) {
-        if (wave == turn && threadIdx.x % kWave < GT) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const uint32_t e = (k * GT + at.t) * W + i;
-                    if (e < E)
-                        lds_prob[e] += acc[k][i];
-                }
-        }
-        __syncthreads();
-    }
-    for (uint32_t e = threadIdx.x; e < E; e += kThreads) {
-        a.prob_part[(size_t)blockIdx.x * E + e] = lds_prob[e];
-        a.count_part[(size_t)blockIdx.x * E + e] = lds_count[e];
-    }
-    if (threadIdx.x == 0) {
-        double v = 0.0;
-        for (int k = 0; k < kThreads / kWave; ++k)
-            v += lds_z[k];
-        a.z_part[blockIdx.x] = v;
-    }
-}
-
-// Step two, by one workgroup: counts, probabilities, the loss and q.  Each
-// expert's groups are added by several threads ("ways"), in order.
-__device__ __forceinline__ void join_rows(const RouterArgs& a)
-{
-    const RouterCall& c = a.c;
-    const uint32_t E = (uint32_t)c.m.V;
-    __shared__ double lds_p[kThreads];
-    __shared__ unsigned long long lds_n[kThreads];
-    __shared__ unsigned long long lds_total[kThreads / kWave];
-    __shared__ double lds_loss[kThreads / kWave];
-    uint32_t cols = 4;
-    while (cols < E && cols < kThreads)
-        cols *= 2;
-    const uint32_t ways = kThreads / cols, col = threadIdx.x % cols, way = threadIdx.x / cols;
-    constexpr int kMost = (int)(kRouterExpertsMax / kThreads);
-    double p[kMost];
-    unsigned long long n[kMost], mine = 0;
-#pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-        p[k] = 0.0;
-        n[k] = 0;
-        const uint32_t e = k * kThreads + col;
-        if (k * kThreads >= E)
-            break;
-        if (e < E) {
-#pragma unroll 8
-            for (uint32_t g = way; g < a.groups; g += ways) {
-                p[k] += (double)a.prob_part[(size_t)g * E + e];
-                n[k] += a.count_part[(size_t)g * E + e];
-            }
-        }
-        __syncthreads();
-        lds_p[threadIdx.x] = p[k];
-        lds_n[threadIdx.x] = n[k];
-        __syncthreads();
-        if (way == 0 && e < E) {
-            for (uint32_t v = 1; v < ways; ++v) {
-                p[k] += lds_p[v * cols + col];
-                n[k] += lds_n[v * cols + col];
-            }
-            c.counts[e] = (int64_t)n[k];
-            if (c.prob)
-                c.prob[e] = (float)p[k];
-            mine += n[k];
-        }
-    }
-    // The number of choices (integers), then the loss.
-    for (int d = 1; d < kWave; d *= 2)
-        mine += __shfl_xor(mine, d);
-    if (threadIdx.x % kWave == 0)
-        lds_total[threadIdx.x / kWave] = mine;
-    __syncthreads();
-    unsigned long long total = 0;
-    for (int k = 0; k < kThreads / kWave; ++k)
-        total += lds_total[k];
-    const double b = (double)c.balance * (double)E;
-    double part = 0.0;
-#pragma unroll
-    for (int k = 0; k < kMost; ++k) {
-        const uint32_t e = k * kThreads + col;
-        if (way == 0 && e < E) {
-            const double q = total ? b * ((double)n[k] / (double)total) : 0.0;
-            // Without a choice the probabilities have no part in the loss.
-            part += total ? q * p[k] : 0.0;
-            a.q[e] = (float)q;
-        }
-    }
-    for (uint32_t g = threadIdx.x; g < a.groups; g += kThreads)
-        if (c.z != 0.0f)
-            part += (double)c.z * a.z_part[g];
-    part = wave_sum64(part);
-    if (threadIdx.x % kWave == 0)
-        lds_loss[threadIdx.x / kWave] = part;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double loss = c.accum ? (double)c.loss[0] : 0.0;
-        for (int k = 0; k < kThreads / kWave; ++k)
-            loss += lds_loss[k];
-        c.loss[0] = (float)loss;
-    }
-}
-
-// Step three, by every workgroup: the gradient of its rows.
-template <class T, int GT, int NV>
-__device__ __forceinline__ void grad_rows(const RouterArgs& a, uint32_t groups)
-{
-    constexpr int W = T::W, RB = kThreads / GT;
-    const RouterCall& c = a.c;
-    const RouterRow<T, GT, NV> at((uint32_t)c.m.V);
-    float q[NV][W];
+            dot += f[k][i] * q(k, i);
+    dot = group_reduce<OpSum, GT>(dot);
+    const float inverse = 1.0f / s;
+    const float lse = m + __builtin_amdgcn_logf(s) * kLn2f;
+    const float offset = 2.0f * c.z * lse - dot * inverse, scale = w * inverse;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const uint32_t e = (k * GT + at.t) * W + i;
-            q[k][i] = e < c.m.V ? a.q[e] : 0.0f;
+        for (int i = 0; i < W; ++i)
+            f[k][i] *= scale * (q(k, i) + offset);
+}
+
+// Step two: every workgroup adds up the teams' counts; the last one tells the
+// outputs, and the others write the gradient of their rows.
+template <class T, int GT, int NV>
+__global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterArgs a)
+{
+    extern __shared__ unsigned lds[];
+    constexpr int W = T::W, RB = kThreads / GT;
+    const RouterCall& c = a.c;
+    const uint32_t E = (uint32_t)c.m.V, teams = (a.groups + kTeam - 1) / kTeam;
+    const RouterRow<T, GT, NV> at(E);
+    float* lds_q = reinterpret_cast<float*>(lds); // GT NV W, zeros past the last expert
+    for (uint32_t e = E + threadIdx.x; e < GT * NV * W; e += kThreads)
+        lds_q[e] = 0.0f;
+    // This workgroup's first rows are on their way meanwhile.
+    const bool tells = blockIdx.x + 1 == gridDim.x;
+    const size_t step = (size_t)(gridDim.x - 1) * RB;
+    size_t r = tells ? c.m.rows : (size_t)blockIdx.x * RB + threadIdx.x / GT;
+    u32x4_t v[NV] = {};
+    float w = 0.0f;
+    const auto request = [&](size_t row) {
+        w = row_weight(c, row);
+        at.load(static_cast<const typename T::S*>(c.m.z) + row * c.m.ld, v);
+    };
+    constexpr bool kAhead = NV < 8;
+    if (kAhead && r < c.m.rows)
+        request(r);
+    unsigned long long n[kJoined];
+#pragma unroll
+    for (int k = 0; k < kJoined; ++k) {
+        const uint32_t e = threadIdx.x + k * kThreads;
+        n[k] = 0;
+        if (e < E)
+#pragma unroll 8
+            for (uint32_t g = 0; g < teams; ++g)
+                n[k] += a.team_count[(size_t)g * E + e];
+    }
+    double p[kJoined], z = 0.0;
+    if (tells) {
+        z = threadIdx.x < teams ? a.team_z[threadIdx.x] : 0.0;
+#pragma unroll
+        for (int k = 0; k < kJoined; ++k) {
+            const uint32_t e = threadIdx.x + k * kThreads;
+            p[k] = 0.0;
+            if (e < E)
+#pragma unroll 8
+                for (uint32_t g = 0; g < teams; ++g)
+                    p[k] += a.team_prob[(size_t)g * E + e];
         }
-    for (size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT; r < c.m.rows;
-         r += (size_t)groups * RB) {
-        const float w = row_weight(c, r);
+    }
+    join(c, n, tells, [&](uint32_t e) { return p[e / kThreads]; }, z, lds_q);
+    if (tells)
+        return;
+    // The lane's factors stay in registers, or in LDS where a row takes a quarter of
+    // those.
+    const auto in_lds = [&](int k, int i) { return lds_q[(k * GT + at.t) * W + i]; };
+    float q[NV][W];
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                q[k][i] = in_lds(k, i);
+    }
+    for (; r < c.m.rows; r += step) {
+        if (!kAhead)
+            request(r);
         float f[NV][W] = {};
         if (w != 0.0f) {
-            float m, s, dot = 0.0f;
-            at.load(static_cast<const typename T::S*>(c.m.z) + r * c.m.ld, f);
+            float m, s;
+            at.unpack(v, f);
             exponentials<GT>(f, m, s);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    dot += f[k][i] * q[k][i];
-            dot = group_reduce<OpSum, GT>(dot);
-            const float inverse = 1.0f / s;
-            const float lse = m + __builtin_amdgcn_logf(s) * kLn2f;
-            const float offset = 2.0f * c.z * lse - dot * inverse, scale = w * inverse;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    f[k][i] *= scale * (q[k][i] + offset);
+            if constexpr (kAhead)
+                gradient<GT>(c, f, m, s, w, [&](int k, int i) { return q[k][i]; });
+            else
+                gradient<GT>(c, f, m, s, w, in_lds);
         }
         at.store(static_cast<typename T::S*>(c.m.dz) + r * c.m.ldd, f);
+        if (kAhead && r + step < c.m.rows)
+            request(r + step);
     }
 }
 
+// All of it by one workgroup that holds every row in its registers.
 template <class T, int GT, int NV>
-__global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
+__global__ __launch_bounds__(kThreads) void router_one_kernel(RouterCall c)
 {
     extern __shared__ unsigned lds[];
-    sum_rows<T, GT, NV>(a, lds, reinterpret_cast<float*>(lds + a.c.m.V));
-}
-
-__global__ __launch_bounds__(kThreads) void router_join_kernel(RouterArgs a) { join_rows(a); }
-
-template <class T, int GT, int NV>
-__global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterArgs a, uint32_t groups)
-{
-    grad_rows<T, GT, NV>(a, groups);
-}
-
-// All three by one workgroup, whose stores are seen by its own threads after a
-// barrier.
-template <class T, int GT, int NV>
-__global__ __launch_bounds__(kThreads) void router_one_kernel(RouterArgs a)
-{
-    extern __shared__ unsigned lds[];
-    sum_rows<T, GT, NV>(a, lds, reinterpret_cast<float*>(lds + a.c.m.V));
+    constexpr int W = T::W;
+    const uint32_t E = (uint32_t)c.m.V, waves = blockDim.x / kWave;
+    const RouterLds<T> mine(lds, E);
+    const RouterRow<T, GT, NV> at(E);
+    const size_t r = threadIdx.x / GT;
+    u32x4_t v[NV] = {};
+    float w = 0.0f;
+    int64_t chosen = -1;
+    if (r < c.m.rows) {
+        w = row_weight(c, r);
+        chosen = first_choice(c, r, at.t);
+        at.load(static_cast<const typename T::S*>(c.m.z) + r * c.m.ld, v);
+    }
+    for (uint32_t e = threadIdx.x; e < E; e += blockDim.x)
+        mine.count[e] = 0;
     __syncthreads();
-    join_rows(a);
+    float f[NV][W] = {}, p[NV][W] = {}, m = 0.0f, s = 0.0f;
+    double z = 0.0;
+    if (w != 0.0f) {
+        count_choices<GT>(c, r, at.t, chosen, mine.count);
+        at.unpack(v, f);
+        exponentials<GT>(f, m, s);
+        const float scale = w / s;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                p[k][i] = f[k][i] * scale;
+        if (c.z != 0.0f && at.t == 0) {
+            const double lse = m + __builtin_amdgcn_logf(s) * kLn2f;
+            z = (double)w * lse * lse;
+        }
+    }
+    put_columns<GT>(p, at.t, E, mine.prob);
     __syncthreads();
-    if (a.c.m.dz)
-        grad_rows<T, GT, NV>(a, 1);
+    unsigned long long n[kJoined];
+    double sum[kJoined];
+#pragma unroll
+    for (int k = 0; k < kJoined; ++k) {
+        const uint32_t e = threadIdx.x + k * kThreads;
+        n[k] = e < E ? mine.count[e] : 0;
+        sum[k] = 0.0;
+        if (e < E)
+            for (uint32_t x = 0; x < waves; ++x)
+                sum[k] += (double)mine.prob[x * E + e];
+    }
+    // q goes where this thread's experts had their counts.
+    join(c, n, true, [&](uint32_t e) { return sum[e / kThreads]; }, z,
+         reinterpret_cast<float*>(mine.count));
+    if (!c.m.dz || r >= c.m.rows)
+        return;
+    if (w != 0.0f) {
+        const float* q = reinterpret_cast<const float*>(mine.count);
+        gradient<GT>(c, f, m, s, w, [&](int k, int i) {
+            const uint32_t e = (k * GT + at.t) * W + i;
+            return e < E ? q[e] : 0.0f;
+        });
+    }
+    at.store(static_cast<typename T::S*>(c.m.dz) + r * c.m.ldd, f);
 }
+
 
 template <class T, int GT, int NV>
 hipError_t launch(const RouterCall& c, const DeviceInfo& dev, const Workspace& ws, hipStream_t s)
 {
     constexpr size_t RB = kThreads / GT;
-    const size_t E = c.m.V, wanted = (c.m.rows + RB - 1) / RB;
-    RouterArgs a = {c, nullptr, nullptr, nullptr, nullptr, 0};
-    a.groups = (uint32_t)std::min(wanted, (size_t)std::min(dev.cus, 1024));
-    char* p = static_cast<char*>(ws.partials);
-    a.z_part = reinterpret_cast<double*>(p);
-    p += sizeof(double) * 1024;
-    a.q = reinterpret_cast<float*>(p);
-    p += sizeof(float) * kRouterExpertsMax;
-    a.groups = (uint32_t)std::min<size_t>(
-        a.groups, (ws.partial_bytes - (p - static_cast<char*>(ws.partials))) / (8 * E));
-    a.prob_part = reinterpret_cast<float*>(p);
-    a.count_part = reinterpret_cast<unsigned*>(a.prob_part + (size_t)a.groups * E);
-    const size_t lds = E * 8;
-    if (a.groups == 1) {
-        hipLaunchKernelGGL((router_one_kernel<T, GT, NV>), dim3(1), dim3(kThreads), lds, s, a);
+    const size_t E = c.m.V;
+    if (c.m.rows <= RB && E <= kThreads) {
+        // As many threads as its rows and its experts need.
+        const size_t threads = std::max((c.m.rows * GT + kWave - 1) / kWave * kWave,
+                                        (E + kWave - 1) / kWave * kWave);
+        hipLaunchKernelGGL((router_one_kernel<T, GT, NV>), dim3(1), dim3((unsigned)threads),
+                           RouterLds<T>::bytes(E, (int)(threads / kWave)), s, c);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((router_sum_kernel<T, GT, NV>), dim3(a.groups), dim3(kThreads), lds, s, a);
-    hipLaunchKernelGGL(router_join_kernel, dim3(1), dim3(kThreads), 0, s, a);
-    if (c.m.dz) {
-        const uint32_t groups = (uint32_t)std::min(wanted, (size_t)dev.cus * 4);
-        hipLaunchKernelGGL((router_grad_kernel<T, GT, NV>), dim3(groups), dim3(kThreads), 0, s, a,
-                           groups);
-    }
+    RouterArgs a = {};
+    a.c = c;
+    const size_t wanted = (c.m.rows + RB - 1) / RB;
+    // The workspace: teams' sums first, then the workgroups'.
+    char* p = static_cast<char*>(ws.partials);
+    const auto take = [&p](size_t bytes) {
+        char* at = p;
+        p += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    a.team_prob = reinterpret_cast<double*>(take(sizeof(double) * kTeams * E));
+    a.team_count = reinterpret_cast<unsigned long long*>(take(8 * kTeams * E));
+    a.team_z = reinterpret_cast<double*>(take(sizeof(double) * kTeams));
+    a.z_part = reinterpret_cast<double*>(take(sizeof(double) * kTeams * kTeam));
+    const size_t left = ws.partial_bytes - (p - static_cast<char*>(ws.partials)) - 512;
+    a.groups = (uint32_t)std::min({wanted, (size_t)dev.cus, (size_t)kTeams * kTeam,
+                                   left / (8 * E)});
+    a.prob_part = reinterpret_cast<float*>(take(sizeof(float) * a.groups * E));
+    a.count_part = reinterpret_cast<unsigned*>(take(sizeof(unsigned) * a.groups * E));
+    a.arrivals = ws.counters;
+    // One workgroup a compute unit in both kernels (65536 x 128 f32: 27.1 us; two in
+    // the sums 32.2, two in the gradient 28.8).
+    hipLaunchKernelGGL((router_sum_kernel<T, GT, NV>), dim3(a.groups), dim3(kThreads),
+                       RouterLds<T>::bytes(E, kThreads / kWave), s, a);
+    const size_t groups = 1 + (c.m.dz ? std::min(wanted, (size_t)dev.cus) : 0);
+    hipLaunchKernelGGL((router_grad_kernel<T, GT, NV>), dim3((unsigned)groups), dim3(kThreads),
+                       sizeof(float) * GT * NV * T::W, s, a);
     return hipGetLastError();
 }
 
