@@ -35,19 +35,30 @@ constexpr float kLog2ef = 1.4426950408889634f;
 constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr int kHalfShift = 8; // exponent of the largest factors of d in half precision
 
-typedef TileShape<256, 256, 2, 4, 2> BigTile;
-typedef TileShape<128, 128, 2, 2, 2> MidTile;
-typedef TileShape<128, 32, 4, 1, 4> FewTile;
+typedef TileShape<256, 256, 2, 4, 64, 2> BigTile;
+#ifndef MIDT
+#define MIDT 128, 128, 2, 2, 64, 2
+#endif
+#ifndef MIDW
+#define MIDW 128, 128, 2, 2, 32, 2
+#endif
+typedef TileShape<MIDT> MidTile;
+typedef TileShape<MIDW> MidWeight;
+typedef TileShape<128, 32, 4, 1, 128, 3> FewTile;
+
+// The hidden rows are padded with zeros to multiples of these.
+constexpr uint32_t kRowPad = 64, kWidthPad = 64;
 
 // What the kernels share.  Pointers into the workspace, except those of the call.
 struct Lce {
     LinearCall c;
-    uint32_t* count;   // [0]: rows that count; [1]: largest exponent (int, half precision)
+    // [0]: rows that count; [1]: largest exponent (int, half precision); [2]: arrivals
+    uint32_t* count;
     int32_t* where;    // of each row of the call: its place among those that count, or -1
     int32_t *row, *target; // of each row that counts: its number, its target
     float *w, *zt, *lse2, *fa, *fb, *fs; // weight, target's product, lse log2 e, factors, 2^(e - 8)
     int32_t* e;
-    double* row_loss;
+    double* loss_part; // of each workgroup that joins rows
     char *h, *hs;      // hidden rows, and in half precision a scaled copy
     size_t ldh;        // bytes
     float2* stat;      // maximum and sum of each row and vocabulary tile
@@ -58,7 +69,19 @@ struct Lce {
     uint32_t splits;
 };
 
+__device__ __forceinline__ uint32_t round_up32(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
+
 // ---- rows that count --------------------------------------------------------
+
+__device__ __forceinline__ float weight_of(const LinearCall& c, size_t r)
+{
+    return c.row_weight ? c.row_weight[r] : 1.0f / (float)c.rows;
+}
+__device__ __forceinline__ bool counted(const LinearCall& c, size_t r)
+{
+    const int64_t t = c.targets[r];
+    return weight_of(c, r) != 0.0f && t >= 0 && t < (int64_t)c.V;
+}
 
 __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
 {
@@ -67,13 +90,7 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
     uint32_t before = 0;
     for (size_t first = 0; first < a.c.rows; first += 1024) {
         const size_t r = first + threadIdx.x;
-        int64_t t = -1;
-        float w = 0.0f;
-        if (r < a.c.rows) {
-            t = a.c.targets[r];
-            w = a.c.row_weight ? a.c.row_weight[r] : 1.0f / (float)a.c.rows;
-        }
-        const bool counts = w != 0.0f && t >= 0 && t < (int64_t)a.c.V;
+        const bool counts = r < a.c.rows && counted(a.c, r);
         const uint64_t all = __ballot(counts);
         if (lane == 0)
             lds[wave] = __popcll(all);
@@ -88,8 +105,8 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
             a.where[r] = counts ? (int32_t)at : -1;
         if (counts) {
             a.row[at] = (int32_t)r;
-            a.target[at] = (int32_t)t;
-            a.w[at] = w;
+            a.target[at] = (int32_t)a.c.targets[r];
+            a.w[at] = weight_of(a.c, r);
         }
         before += total;
         __syncthreads();
@@ -97,19 +114,51 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
     if (threadIdx.x == 0) {
         a.count[0] = before;
         a.count[1] = (uint32_t)INT32_MIN;
+        a.count[2] = 0;
     }
 }
 
-// One workgroup a row of the call, and kStepK more for the zeros after the last
-// row that counts.
+// One workgroup a row of the call, and kRowPad more for the zeros after the last
+// row that counts.  ALONE: there has been no lce_rows_kernel; with few rows each
+// workgroup counts those before its own itself, which takes less than a launch.
+template <bool ALONE>
 __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
 {
     const size_t r = blockIdx.x;
     const uint32_t D = (uint32_t)a.c.D, chunks = (uint32_t)(a.ldh / 16);
     const uint16_t* from = nullptr;
     uint32_t to;
+    int32_t at;
+    if constexpr (ALONE) {
+        __shared__ uint32_t lds[kWaves];
+        const uint32_t before = (uint32_t)(r < a.c.rows ? r : a.c.rows);
+        uint32_t n = 0;
+        for (uint32_t i = threadIdx.x; i < before; i += 256)
+            n += counted(a.c, i);
+        n = (uint32_t)wave_sum64((double)n);
+        if (threadIdx.x % kWave == 0)
+            lds[threadIdx.x / kWave] = n;
+        __syncthreads();
+        at = (int32_t)(lds[0] + lds[1] + lds[2] + lds[3]);
+        const bool counts = r < a.c.rows && counted(a.c, r);
+        if (threadIdx.x == 0) {
+            if (counts) {
+                a.row[at] = (int32_t)r;
+                a.target[at] = (int32_t)a.c.targets[r];
+                a.w[at] = weight_of(a.c, r);
+            }
+            if (r == a.c.rows) {
+                a.count[0] = (uint32_t)at;
+                a.count[1] = (uint32_t)INT32_MIN;
+                a.count[2] = 0;
+            }
+        }
+        if (r < a.c.rows && !counts)
+            at = -1;
+    } else {
+        at = r < a.c.rows ? a.where[r] : (int32_t)a.count[0];
+    }
     if (r < a.c.rows) {
-        const int32_t at = a.where[r];
         if (at < 0) {
             if (threadIdx.x == 0) {
                 if (a.c.logp)
@@ -127,9 +176,8 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
         to = (uint32_t)at;
         from = static_cast<const uint16_t*>(a.c.hidden) + r * a.c.ldh;
     } else {
-        const uint32_t n = a.count[0];
-        to = n + (uint32_t)(r - a.c.rows);
-        if (to >= (n + kStepK - 1) / kStepK * kStepK)
+        to = (uint32_t)at + (uint32_t)(r - a.c.rows);
+        if (to >= round_up32((uint32_t)at, kRowPad))
             return;
     }
     u32x4_t* out = reinterpret_cast<u32x4_t*>(a.h + to * a.ldh);
@@ -244,18 +292,12 @@ __global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t f
     }
 }
 
-// One wave a row: its tiles' sums, its loss and the factors of its gradient.
+// One wave a row: its tiles' sums, its loss and the factors of its gradient.  The
+// workgroup that arrives last adds up the losses, in order.
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
 template <class T>
-__global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
+__device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t lane)
 {
-    const uint32_t n = blockIdx.x * kWaves + threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    if (n >= a.c.rows)
-        return;
-    if (n >= a.count[0]) {
-        if (lane == 0)
-            a.row_loss[n] = 0.0;
-        return;
-    }
     const float2* stat = a.stat + (size_t)n * a.tiles_v;
     const float c = a.c.scale * kLog2ef;
     float m = -INFINITY;
@@ -270,7 +312,7 @@ __global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
     }
     s = wave_sum64(s);
     if (lane)
-        return;
+        return 0.0;
     const double scale = a.c.scale, w = a.w[n];
     const double ln = log(s), lse = scale * (double)ref + ln;
     const double logp = scale * ((double)a.zt[n] - (double)ref) - ln;
@@ -279,7 +321,6 @@ __global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
         a.c.logp[r] = (float)logp;
     if (a.c.lse)
         a.c.lse[r] = (float)lse;
-    a.row_loss[n] = w * ((double)a.c.z * lse * lse - logp);
     a.lse2[n] = (float)(lse * kLog2e64);
     double fa = w * scale * (1.0 + 2.0 * (double)a.c.z * lse), fb = w * scale;
     if constexpr (__is_same(T, ElemF16)) {
@@ -290,10 +331,194 @@ __global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
         fb = ldexp(fb, kHalfShift - e);
         a.e[n] = e;
         a.fs[n] = ldexpf(1.0f, e - kHalfShift);
-        atomicMax(reinterpret_cast<int*>(a.count + 1), e); // of integers: in any order
+        // Of integers, in any order; where it would change nothing, not at all (1331
+        // rows at one address took 16 us).
+        int* largest = reinterpret_cast<int*>(a.count + 1);
+        if (e > __hip_atomic_load(largest, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            atomicMax(largest, e);
     }
     a.fa[n] = (float)fa;
     a.fb[n] = (float)fb;
+    return w * ((double)a.c.z * lse * lse - logp);
+}
+
+template <class T>
+__global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
+{
+    __shared__ double lds[kJoinWaves];
+    __shared__ uint32_t lds_before;
+    const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const uint32_t n = blockIdx.x * kJoinWaves + wave;
+    const double mine = n < a.count[0] ? join_row<T>(a, n, lane) : 0.0;
+    if (lane == 0)
+        lds[wave] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double v = 0.0;
+        for (int k = 0; k < kJoinWaves; ++k)
+            v += lds[k];
+        store_shared(a.loss_part + blockIdx.x, v);
+        lds_before = count_shared(a.count + 2);
+    }
+    __syncthreads();
+    if (lds_before != gridDim.x - 1)
+        return;
+    double v = 0.0;
+    for (uint32_t k = threadIdx.x; k < gridDim.x; k += kJoinThreads)
+        v += load_shared(a.loss_part + k);
+    v = wave_sum64(v);
+    if (lane == 0)
+        lds[wave] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = a.c.accum ? (double)a.c.loss[0] : 0.0;
+        for (int k = 0; k < kJoinWaves; ++k)
+            v += lds[k];
+        a.c.loss[0] = (float)v;
+    }
+}
+
+// ---- up to 16 rows ------------------------------------------------------------
+//
+// The layer is only read, so what counts is the rate of its reading: each wave
+// takes 16 of its rows from end to end, straight into the operand registers of
+// v_mfma_f32_16x16x32 (lane l: row l % 16, 16 bytes at 64 s + 16 (l / 16) in step s),
+// with kAhead steps, 512 bytes of each row, in flight twice over; the hidden rows
+// stay in LDS (16 bytes of padding a row spread 16 rows over the banks).
+constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 8;
+constexpr size_t kStreamLds = 144 * 1024;
+
+template <class T>
+__device__ __forceinline__ f32x4_t mfma16(const s16x8_t& a, const s16x8_t& b, const f32x4_t& c)
+{
+    if constexpr (__is_same(T, ElemBF16))
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                      __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+__device__ const u32x4_t kNothing = {0, 0, 0, 0};
+
+// The products of columns v0 .. v0 + 15 (from `end` on, of end - 1 again): lane l has
+// those of hidden row l % ROWS with columns v0 + 4 (l / 16) + e.
+template <class T>
+__device__ __forceinline__ f32x4_t stream_columns(const Lce& a, const char* lds_row, uint32_t v0,
+                                                  uint32_t end)
+{
+    const uint32_t lane = threadIdx.x % kWave, part = lane / 16;
+    const uint32_t v = v0 + lane % 16 < end ? v0 + lane % 16 : end - 1;
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
+                                                        (size_t)v * a.c.ldw * 2) + part;
+    const uint32_t D = (uint32_t)a.c.D, steps = (D + 31) / 32;
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4_t w[2][kAhead];
+    const auto request = [&](uint32_t s, u32x4_t (&to)[kAhead]) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            to[i] = *((s + i) * 32 + part * 8 < D ? p + (s + i) * 4 : &kNothing);
+    };
+    const auto multiply = [&](uint32_t s, const u32x4_t (&from)[kAhead]) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s + i < steps) {
+                const s16x8_t h = *reinterpret_cast<const s16x8_t*>(lds_row + (s + i) * 64 + part * 16);
+                acc = mfma16<T>(__builtin_bit_cast(s16x8_t, from[i]), h, acc);
+            }
+        }
+    };
+    request(0, w[0]);
+    for (uint32_t s = 0; s < steps; s += 2 * kAhead) {
+        request(s + kAhead, w[1]);
+        multiply(s, w[0]);
+        request(s + 2 * kAhead, w[0]);
+        multiply(s + kAhead, w[1]);
+    }
+    return acc;
+}
+
+// Columns [begin, end) of the layer for all rows, a run of them to each workgroup.
+// F::column takes each lane's four products.
+template <class T, int ROWS, class F>
+__device__ __forceinline__ void stream_layer(const Lce& a, char* lds, uint32_t begin, uint32_t end, F f)
+{
+    const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16);
+    for (uint32_t i = threadIdx.x; i < ROWS * chunks; i += kStreamThreads)
+        *reinterpret_cast<u32x4_t*>(lds + i / chunks * stride + i % chunks * 16) =
+            *reinterpret_cast<const u32x4_t*>(a.h + i / chunks * a.ldh + i % chunks * 16);
+    __syncthreads();
+    const uint32_t blocks = (end - begin + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
+    const uint32_t first = blockIdx.x * per, last = first + per < blocks ? first + per : blocks;
+    for (uint32_t b = first + threadIdx.x / kWave; b < last; b += kStreamWaves) {
+        const uint32_t v0 = begin + b * 16;
+        f(stream_columns<T>(a, lds + threadIdx.x % ROWS * stride, v0, end),
+          v0 + threadIdx.x % kWave / 16 * 4);
+    }
+}
+
+template <class T, int ROWS>
+__global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
+{
+    extern __shared__ __align__(16) char buffer[];
+    const uint32_t n = threadIdx.x % 16, rows = a.count[0], V = (uint32_t)a.c.V;
+    const bool in = n < rows && n < ROWS;
+    const uint32_t target = in ? (uint32_t)a.target[n] : ~0u;
+    const float c = a.c.scale * kLog2ef;
+    float m = -INFINITY, s = 0.0f;
+    stream_layer<T, ROWS>(a, buffer, 0, V, [&](const f32x4_t& z, uint32_t v) {
+        float most = m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            most = fmaxf(most, v + e < V ? z[e] : -INFINITY);
+            if (v + e == target)
+                a.zt[n] = z[e];
+        }
+        const float ref = most == -INFINITY ? 0.0f : most;
+        s *= __builtin_amdgcn_exp2f((m - ref) * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s += v + e < V ? __builtin_amdgcn_exp2f((z[e] - ref) * c) : 0.0f;
+        m = most;
+    });
+    __shared__ float2 part[kStreamWaves * 4][16];
+    part[threadIdx.x / 16][n] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x >= 16 || !in)
+        return;
+    m = -INFINITY;
+    for (int k = 0; k < kStreamWaves * 4; ++k)
+        m = fmaxf(m, part[k][n].x);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    s = 0.0f;
+    for (int k = 0; k < kStreamWaves * 4; ++k)
+        s += part[k][n].y * __builtin_amdgcn_exp2f((part[k][n].x - ref) * c);
+    a.stat[(size_t)n * a.tiles_v + blockIdx.x] = make_float2(m, s);
+}
+
+template <class T, int ROWS>
+__global__ __launch_bounds__(kStreamThreads) void lce_stream_d_kernel(Lce a, uint32_t first)
+{
+    extern __shared__ __align__(16) char buffer[];
+    const uint32_t n = threadIdx.x % 16, rows = a.count[0];
+    const uint32_t left = (uint32_t)a.c.V - first, cols = left < a.piece ? left : a.piece;
+    const bool in = n < rows && n < ROWS;
+    const uint32_t target = in ? (uint32_t)a.target[n] : ~0u;
+    const float c = a.c.scale * kLog2ef, lse2 = in ? a.lse2[n] : 0.0f;
+    const float fa = in ? a.fa[n] : 0.0f, fb = in ? a.fb[n] : 0.0f;
+    stream_layer<T, ROWS>(a, buffer, first, first + cols, [&](const f32x4_t& z, uint32_t v) {
+        uint64_t packed = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float d = fa * __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], c, -lse2));
+            d = v + e == target ? d - fb : d;
+            d = v + e < first + cols ? d : 0.0f;
+            packed |= (uint64_t)(uint16_t)T::narrow(d) << (16 * e);
+        }
+        if (in)
+            *reinterpret_cast<uint64_t*>(reinterpret_cast<uint16_t*>(a.d) + (size_t)n * a.piece + v - first) =
+                packed;
+    });
 }
 
 // ---- gradients --------------------------------------------------------------
@@ -302,7 +527,7 @@ __global__ __launch_bounds__(kBlock) void lce_join_kernel(Lce a)
 __global__ __launch_bounds__(256) void lce_scale_kernel(Lce a)
 {
     const uint32_t n = blockIdx.x, rows = a.count[0];
-    if (n >= (rows + kStepK - 1) / kStepK * kStepK)
+    if (n >= round_up32(rows, kRowPad))
         return;
     const float f = n < rows ? ldexpf(1.0f, a.e[n] - (int)a.count[1]) : 0.0f;
     const u32x4_t* from = reinterpret_cast<const u32x4_t*>(a.h + n * a.ldh);
@@ -369,8 +594,8 @@ __global__ __launch_bounds__(S::kThreads) void lce_dh_kernel(Lce a, uint32_t fir
     if (n0 >= rows)
         return;
     const uint32_t left = (uint32_t)a.c.V - first, k = left < a.piece ? left : a.piece;
-    const uint32_t stages = (k + kStepK - 1) / kStepK;
-    const uint32_t per = (stages + a.splits - 1) / a.splits * kStepK;
+    const uint32_t stages = (k + S::K - 1) / S::K;
+    const uint32_t per = (stages + a.splits - 1) / a.splits * S::K;
     const uint32_t begin = blockIdx.y * per < k ? blockIdx.y * per : k;
     const uint32_t end = begin + per < k ? begin + per : k;
     const Operand W = {static_cast<const char*>(a.c.weight) + (size_t)first * a.c.ldw * 2,
@@ -397,33 +622,44 @@ __global__ __launch_bounds__(S::kThreads) void lce_dh_kernel(Lce a, uint32_t fir
             }
 }
 
-// The rows of dh, one a workgroup: their splits' sums, in order, rounded once.
+// dh's 32 x 32 blocks, one a workgroup: their splits' sums, in order, rounded once,
+// through LDS to the rows of the call.
 template <class T, class S>
-__global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t tiles_m, uint32_t tiles_n)
+__global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t tiles_m, uint32_t tiles_n,
+                                                               uint32_t blocks_m)
 {
-    const uint32_t n = blockIdx.x;
-    if (n >= a.count[0])
+    constexpr uint32_t kRow = 32 + 8; // elements of a row in LDS
+    __shared__ __align__(16) uint16_t lds[32 * kRow];
+    const uint32_t rows = a.count[0], n0 = blockIdx.x / blocks_m * 32, m0 = blockIdx.x % blocks_m * 32;
+    if (n0 >= rows)
         return;
-    for (uint32_t m = threadIdx.x * 4; m < a.c.D; m += kBlock * 4) {
-        const uint32_t in_m = m % S::M, in_n = n % S::N;
-        const uint32_t wave = in_m / (S::MS * 32) * S::WN + in_n / (S::NS * 32);
-        const uint32_t i = in_m / 32 % S::MS, j = in_n / 32 % S::NS;
-        const uint32_t lane = in_m / 4 % 2 * 32 + in_n % 32, q = in_m / 8 % 4;
-        const size_t tile = (size_t)(m / S::M) * tiles_n + n / S::N;
-        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.dh) + tile * (S::M * S::N / 4) +
-                           ((wave * S::MS * S::NS + i * S::NS + j) * 4 + q) * kWave + lane;
-        const size_t split = (size_t)tiles_m * tiles_n * (S::M * S::N / 4);
-        f32x4_t v = *p;
-#pragma unroll 4
-        for (uint32_t k = 1; k < a.splits; ++k)
-            v += p[k * split];
-        if constexpr (__is_same(T, ElemF16))
-            v *= a.fs[n];
-        uint16_t* out = static_cast<uint16_t*>(a.c.dhidden) + (size_t)a.row[n] * a.c.lddh + m;
+    const uint32_t in_m = m0 % S::M, in_n = n0 % S::N;
+    const uint32_t wave = in_m / (S::MS * 32) * S::WN + in_n / (S::NS * 32);
+    const uint32_t i = in_m / 32 % S::MS, j = in_n / 32 % S::NS;
+    const uint32_t q = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const size_t tile = (size_t)(m0 / S::M) * tiles_n + n0 / S::N;
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.dh) + tile * (S::M * S::N / 4) +
+                       ((wave * S::MS * S::NS + i * S::NS + j) * 4 + q) * kWave + lane;
+    const size_t split = (size_t)tiles_m * tiles_n * (S::M * S::N / 4);
+    f32x4_t v = *p;
+#pragma unroll 8
+    for (uint32_t k = 1; k < a.splits; ++k)
+        v += p[k * split];
+    const uint32_t n = lane % 32;
+    if constexpr (__is_same(T, ElemF16))
+        v *= n0 + n < rows ? a.fs[n0 + n] : 0.0f;
+    uint64_t packed = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            out[x] = T::narrow(v[x]);
-    }
+    for (int x = 0; x < 4; ++x)
+        packed |= (uint64_t)(uint16_t)T::narrow(v[x]) << (16 * x);
+    *reinterpret_cast<uint64_t*>(lds + n * kRow + q * 8 + lane / 32 * 4) = packed;
+    __syncthreads();
+    const uint32_t r = threadIdx.x / 4, c = threadIdx.x % 4 * 8; // D is a multiple of 8
+    if (threadIdx.x >= 128 || n0 + r >= rows || m0 + c >= a.c.D)
+        return;
+    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(lds + r * kRow + c);
+    uint16_t* out = static_cast<uint16_t*>(a.c.dhidden) + (size_t)a.row[n0 + r] * a.c.lddh + m0 + c;
+    *reinterpret_cast<u32x4u_t*>(out) = u32x4u_t{u.x, u.y, u.z, u.w};
 }
 
 // The piece's rows of dW.
@@ -453,28 +689,32 @@ __global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t fir
 // ---- plan -------------------------------------------------------------------
 
 constexpr size_t kPieceBytes = size_t(256) << 20; // of d, where that is 2048 columns or more
-constexpr size_t kRowPad = 256, kColPad = 256;
+constexpr size_t kRowsPad = 256, kColPad = 256; // of rows in the workspace, of a piece
 // A launch holds at most 2^32 - 1 work-items, of which a tile takes up to 512.
 constexpr uint32_t kTilesPerLaunch = 1u << 22;
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-enum class Kind { Few, Mid, Big };
+// Rows up to which lce_gather_kernel goes alone.
+constexpr size_t kRowsAlone = 1024;
+
+enum class Kind { Stream, Few, Mid, Big };
 
 // Tiles by the work: 32 rows by 128 columns where there are few rows, whose
 // product only reads the layer; 256 x 256, the fastest, where there are enough of
 // them to give every compute unit one; 128 x 128 in between.
 struct LcePlan {
     Kind kind, kind_w; // of the products over rows; of the layer's gradient
-    uint32_t tile_m, tile_n, tile_w;
     uint32_t tiles_v, tiles_n, tiles_d;
     size_t rows, piece, splits, bytes;
+    size_t stream_rows, stream_lds;
 };
 
 template <class F>
 auto with_shape(Kind k, F f)
 {
     switch (k) {
+    case Kind::Stream:
     case Kind::Few: return f(FewTile());
     case Kind::Mid: return f(MidTile());
     default: return f(BigTile());
@@ -498,38 +738,44 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
 {
     LcePlan p;
     const bool grad = c.dhidden || c.dweight;
-    p.rows = round_up(c.rows, kRowPad);
+    Lce dummy;
+    Lce& o = a ? *a : dummy;
+    p.rows = round_up(c.rows, kRowsPad);
     const size_t big = round_up(c.V, 256) / 256 * (p.rows / 256);
-    p.kind = c.rows <= 32 ? Kind::Few : c.rows > 128 && big >= (size_t)dev.cus ? Kind::Big : Kind::Mid;
+    o.ldh = round_up(c.D, kWidthPad) * 2;
+    p.stream_rows = c.rows <= 8 ? 8 : 16;
+    p.stream_lds = p.stream_rows * (o.ldh + 16);
+    p.kind = c.rows <= 16 && p.stream_lds <= kStreamLds ? Kind::Stream
+             : c.rows <= 32                             ? Kind::Few
+             : c.rows > 128 && big >= (size_t)dev.cus   ? Kind::Big
+                                                        : Kind::Mid;
+    size_t tile = 0; // elements
     with_shape(p.kind, [&](auto s) {
-        p.tile_m = s.M;
-        p.tile_n = s.N;
+        p.tiles_v = (uint32_t)((c.V + s.M - 1) / s.M);
+        p.tiles_n = (uint32_t)((c.rows + s.N - 1) / s.N);
+        p.tiles_d = (uint32_t)((c.D + s.M - 1) / s.M);
+        tile = (size_t)s.M * s.N;
         return 0;
     });
-    p.tiles_v = (uint32_t)((c.V + p.tile_m - 1) / p.tile_m);
-    p.tiles_n = (uint32_t)((c.rows + p.tile_n - 1) / p.tile_n);
-    p.tiles_d = (uint32_t)((c.D + p.tile_m - 1) / p.tile_m);
+    if (p.kind == Kind::Stream)
+        p.tiles_v = (uint32_t)std::min<size_t>((size_t)dev.cus, (c.V + 15) / 16);
     p.kind_w = c.rows <= 128 || p.kind != Kind::Big ? Kind::Mid : Kind::Big;
-    p.tile_w = p.kind_w == Kind::Mid ? 128 : 256;
     p.piece = std::min(round_up(c.V, kColPad),
                        std::max<size_t>(2048, kPieceBytes / 2 / p.rows / kColPad * kColPad));
-    const size_t tiles = (size_t)p.tiles_d * p.tiles_n, stages = p.piece / kStepK;
+    const size_t tiles = (size_t)p.tiles_d * p.tiles_n, stages = p.piece / 64;
     p.splits = std::max<size_t>(1, std::min((size_t)dev.cus / std::max<size_t>(1, tiles), stages / 8));
 
     Places w = {static_cast<char*>(c.workspace)};
-    Lce dummy;
-    Lce& o = a ? *a : dummy;
     o.c = c;
     const size_t n = p.rows;
-    o.ldh = round_up(c.D, kStepK) * 2;
-    w.take(o.count, 8);
+    w.take(o.count, 12);
     w.take(o.where, 4 * n);
     w.take(o.row, 4 * n);
     w.take(o.target, 4 * n);
     for (float** f : {&o.w, &o.zt, &o.lse2, &o.fa, &o.fb, &o.fs})
         w.take(*f, 4 * n);
     w.take(o.e, 4 * n);
-    w.take(o.row_loss, 8 * n);
+    w.take(o.loss_part, 8 * n / kJoinWaves + 8);
     w.take(o.h, o.ldh * n);
     o.hs = nullptr;
     if (t == LogitType::F16 && c.dweight)
@@ -541,7 +787,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     if (grad)
         w.take(o.d, 2 * p.piece * n);
     if (c.dhidden)
-        w.take(o.dh, 4 * p.splits * p.tiles_d * p.tile_m * p.tiles_n * p.tile_n);
+        w.take(o.dh, 4 * p.splits * tiles * tile);
     p.bytes = w.used;
     return p;
 }
@@ -551,32 +797,54 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
 {
     Lce a;
     const LcePlan p = plan_of(t, c, dev, &a);
-    hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
-    hipLaunchKernelGGL(lce_gather_kernel, dim3((unsigned)c.rows + kStepK), dim3(256), 0, s, a);
-    with_shape(p.kind, [&](auto shape) {
-        typedef decltype(shape) S;
-        const uint32_t most = std::max(8u, kTilesPerLaunch / p.tiles_n);
-        for (uint32_t first = 0; first < p.tiles_v; first += most) {
-            const uint32_t tiles_m = std::min(most, p.tiles_v - first);
-            hipLaunchKernelGGL((lce_stat_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads),
-                               0, s, a, first, tiles_m, p.tiles_n);
-        }
-        return 0;
-    });
-    hipLaunchKernelGGL(lce_join_kernel<T>, dim3((unsigned)((c.rows + kWaves - 1) / kWaves)),
-                       dim3(kBlock), 0, s, a);
-    hipError_t e = launch_loss_sum(a.row_loss, c.rows, c.loss, c.accum, nullptr, nullptr, s);
-    if (e != hipSuccess || (!c.dhidden && !c.dweight))
-        return e;
+    const dim3 gather((unsigned)c.rows + kRowPad);
+    if (c.rows <= kRowsAlone) {
+        hipLaunchKernelGGL(lce_gather_kernel<true>, gather, dim3(256), 0, s, a);
+    } else {
+        hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+        hipLaunchKernelGGL(lce_gather_kernel<false>, gather, dim3(256), 0, s, a);
+    }
+    if (p.kind == Kind::Stream) {
+        if (p.stream_rows == 8)
+            hipLaunchKernelGGL((lce_stream_stat_kernel<T, 8>), dim3(p.tiles_v), dim3(kStreamThreads),
+                               p.stream_lds, s, a);
+        else
+            hipLaunchKernelGGL((lce_stream_stat_kernel<T, 16>), dim3(p.tiles_v), dim3(kStreamThreads),
+                               p.stream_lds, s, a);
+    } else {
+        with_shape(p.kind, [&](auto shape) {
+            typedef decltype(shape) S;
+            const uint32_t most = std::max(8u, kTilesPerLaunch / p.tiles_n);
+            for (uint32_t first = 0; first < p.tiles_v; first += most) {
+                const uint32_t tiles_m = std::min(most, p.tiles_v - first);
+                hipLaunchKernelGGL((lce_stat_kernel<T, S>), dim3(tiles_m * p.tiles_n),
+                                   dim3(S::kThreads), 0, s, a, first, tiles_m, p.tiles_n);
+            }
+            return 0;
+        });
+    }
+    hipLaunchKernelGGL(lce_join_kernel<T>, dim3((unsigned)((c.rows + kJoinWaves - 1) / kJoinWaves)),
+                       dim3(kJoinThreads), 0, s, a);
+    if (!c.dhidden && !c.dweight)
+        return hipGetLastError();
     if (a.hs)
         hipLaunchKernelGGL(lce_scale_kernel, dim3((unsigned)p.rows), dim3(256), 0, s, a);
     for (size_t first = 0; first < c.V; first += p.piece) {
         const uint32_t f = (uint32_t)first;
+        if (p.kind == Kind::Stream) {
+            if (p.stream_rows == 8)
+                hipLaunchKernelGGL((lce_stream_d_kernel<T, 8>), dim3(p.tiles_v), dim3(kStreamThreads),
+                                   p.stream_lds, s, a, f);
+            else
+                hipLaunchKernelGGL((lce_stream_d_kernel<T, 16>), dim3(p.tiles_v), dim3(kStreamThreads),
+                                   p.stream_lds, s, a, f);
+        }
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
             const uint32_t tiles_m = (uint32_t)p.piece / S::M;
-            hipLaunchKernelGGL((lce_d_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads), 0,
-                               s, a, f, p.tiles_n);
+            if (p.kind != Kind::Stream)
+                hipLaunchKernelGGL((lce_d_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads),
+                                   0, s, a, f, p.tiles_n);
             if (c.dhidden)
                 hipLaunchKernelGGL((lce_dh_kernel<T, S>),
                                    dim3(p.tiles_d * p.tiles_n, (unsigned)p.splits),
@@ -593,7 +861,7 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
                                    dim3(S::kThreads), 0, s, a, f, tiles_m, tiles_n);
             };
             if (p.kind_w == Kind::Mid)
-                dw(MidTile());
+                dw(MidWeight());
             else
                 dw(BigTile());
         }
@@ -601,8 +869,10 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
     if (c.dhidden)
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
-            hipLaunchKernelGGL((lce_dh_finish_kernel<T, S>),
-                               dim3((unsigned)c.rows), dim3(kBlock), 0, s, a, p.tiles_d, p.tiles_n);
+            const uint32_t blocks_m = (uint32_t)((c.D + 31) / 32);
+            const uint32_t blocks_n = (uint32_t)((c.rows + 31) / 32);
+            hipLaunchKernelGGL((lce_dh_finish_kernel<T, S>), dim3(blocks_m * blocks_n), dim3(kBlock),
+                               0, s, a, p.tiles_d, p.tiles_n, blocks_m);
             return 0;
         });
     return hipGetLastError();

@@ -3,7 +3,7 @@
 //
 // Each operand lies in memory either with its contraction index contiguous
 // ("row" form, A[m][k]) or with the other one ("column" form, A[k][m]).  Tiles
-// of 64 steps of k go from memory to LDS without passing registers
+// of K steps of k go from memory to LDS without passing registers
 // (buffer_load ... lds, 16 bytes a lane, 1 KiB a wave), into a ring of STAGES
 // buffers, and from there to the operand registers of v_mfma_f32_32x32x16:
 // by ds_read_b128 from row form, by ds_read_b64_tr_b16, which transposes 4 x 16
@@ -11,7 +11,7 @@
 //
 // The loads write LDS in lane order, so 16-byte chunks are permuted on the
 // memory side instead, to where 16 lanes that read at once find 64 banks:
-//   row form    (128 bytes a row)        chunk c of row r at c ^ ((r >> 1) & 7)
+//   row form    (2 K bytes a row)        chunk c of row r at c ^ row_swizzle(r)
 //   column form (2 M bytes a step of k)  chunk c of step k at c ^ 4 (k & 3)
 //
 // Elements outside an operand are zeros: their lanes load from past the end of
@@ -31,7 +31,13 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kStepK = 64; // steps of k a stage
+// Row form: the rows of 256 bytes share the permutation, the next rows have others.
+template <int K>
+__device__ __forceinline__ constexpr uint32_t row_swizzle(uint32_t r)
+{
+    constexpr uint32_t kRows = K < 128 ? 128 / K : 1, kMask = K / 8 < 16 ? K / 8 - 1 : 15;
+    return r / kRows & kMask;
+}
 
 template <class T>
 __device__ __forceinline__ f32x16_t mfma(const s16x8_t& a, const s16x8_t& b, const f32x16_t& c)
@@ -72,20 +78,22 @@ __device__ __forceinline__ void wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
+constexpr int kLdsDone = 0xc07f; // lgkmcnt(0) alone
 __device__ __forceinline__ void barrier()
 {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(kLdsDone);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
-// One operand's tile of R rows by kStepK.
-template <int R, bool ROW, int WAVES>
+// One operand's tile of R rows by K.
+template <int R, int K, bool ROW, int WAVES>
 struct TileOperand {
-    static constexpr int kBytes = R * kStepK * 2;
+    static constexpr int kBytes = R * K * 2;
     static constexpr int kLoads = kBytes / 1024 / WAVES;
     static_assert(kLoads >= 1 && kLoads * WAVES * 1024 == kBytes, "whole loads for every wave");
-    static constexpr int kChunks = R / 8; // of a step of k, column form
+    static constexpr int kChunks = ROW ? K / 8 : R / 8; // of a row, or of a step of k
 
     uint32_t offset[kLoads], k_of[kLoads]; // of this lane's chunk: bytes from `at`, step of k
     uint64_t at;
@@ -93,7 +101,7 @@ struct TileOperand {
     uint32_t k;
 
     // first: the tile's first row; begin, end: its steps of k (begin a multiple
-    // of kStepK).
+    // of 8).
     __device__ __forceinline__ TileOperand(const Operand& o, uint32_t first, uint32_t begin,
                                            uint32_t end)
     {
@@ -101,20 +109,20 @@ struct TileOperand {
         k = end - begin;
         if constexpr (ROW) {
             at = (uint64_t)o.p + (uint64_t)first * o.ld + (uint64_t)begin * 2;
-            advance = kStepK * 2;
+            advance = K * 2;
         } else {
             at = (uint64_t)o.p + (uint64_t)begin * o.ld + (uint64_t)first * 2;
-            advance = (uint64_t)kStepK * o.ld;
+            advance = (uint64_t)K * o.ld;
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t load = i * WAVES + wave;
+            const uint32_t s = (i * WAVES + wave) * kWave + lane;
             if constexpr (ROW) {
-                const uint32_t r = load * 8 + lane / 8, c = (lane % 8) ^ ((r >> 1) & 7);
+                const uint32_t r = s / kChunks, c = (s % kChunks) ^ row_swizzle<K>(r);
                 k_of[i] = c * 8;
                 offset[i] = first + r < o.count ? r * (uint32_t)o.ld + c * 16 : kOutside;
             } else {
-                const uint32_t s = load * 64 + lane, kk = s / kChunks;
+                const uint32_t kk = s / kChunks;
                 const uint32_t c = (s % kChunks) ^ ((kk & 3) << 2);
                 k_of[i] = kk;
                 offset[i] = first + c * 8 < o.count ? kk * (uint32_t)o.ld + c * 16 : kOutside;
@@ -122,9 +130,8 @@ struct TileOperand {
         }
     }
 
-    // Requests stage number `stage` into LDS at `lds`; a stage past the last
-    // one brings zeros.
-    __device__ __forceinline__ void request(uint32_t stage, uint32_t lds) const
+    // The descriptor of stage number `stage`.
+    __device__ __forceinline__ u32x4_t stage(uint32_t stage) const
     {
         const uint64_t p = at + advance * stage;
         u32x4_t rsrc;
@@ -132,18 +139,16 @@ struct TileOperand {
         rsrc.y = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32) & 0xffffu);
         rsrc.z = 0x7fffffffu;
         rsrc.w = 0x00020000u;
+        return rsrc;
+    }
+    // Requests load i of stage number `stage` (rsrc) into LDS at `lds`; a stage past
+    // the last one brings zeros.
+    __device__ __forceinline__ void request(const u32x4_t& rsrc, int i, uint32_t stage,
+                                            uint32_t lds) const
+    {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        const uint32_t before = stage * kStepK;
-        if (before + kStepK <= k) {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_to_lds(rsrc, offset[i], lds + (i * WAVES + wave) * 1024);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_to_lds(rsrc, before + k_of[i] < k ? offset[i] : kOutside,
-                            lds + (i * WAVES + wave) * 1024);
-        }
+        load_to_lds(rsrc, stage * K + k_of[i] < k ? offset[i] : kOutside,
+                    lds + (i * WAVES + wave) * 1024);
     }
 
     // The operand registers of 32 rows from `row` (a multiple of 32) on, steps
@@ -153,7 +158,8 @@ struct TileOperand {
         const uint32_t lane = threadIdx.x % kWave, half = lane / 32;
         if constexpr (ROW) {
             const uint32_t r = lane % 32;
-            const uint32_t a = lds + row * 128 + r * 128 + ((kk * 2 + half) ^ ((r >> 1) & 7)) * 16;
+            const uint32_t a =
+                lds + (row + r) * (K * 2) + ((kk * 2 + half) ^ row_swizzle<K>(r)) * 16;
             return *(__attribute__((address_space(3))) const s16x8_t*)a;
         } else {
             typedef __attribute__((address_space(3))) s16x4_t* ptr;
@@ -167,14 +173,14 @@ struct TileOperand {
     }
 };
 
-// The shape of a workgroup's tile: M x N elements by WM x WN waves, STAGES
-// buffers in LDS.
-template <int M_, int N_, int WM_, int WN_, int STAGES_>
+// The shape of a workgroup's tile: M x N elements by WM x WN waves, STAGES buffers
+// of K steps in LDS.
+template <int M_, int N_, int WM_, int WN_, int K_, int STAGES_>
 struct TileShape {
-    static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, STAGES = STAGES_;
+    static constexpr int M = M_, N = N_, WM = WM_, WN = WN_, K = K_, STAGES = STAGES_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int MS = M / WM / 32, NS = N / WN / 32; // 32 x 32 blocks of a wave
-    static constexpr int kStage = (M + N) * kStepK * 2;
+    static constexpr int kStage = (M + N) * K * 2;
     // The finished tile passes through LDS too: rows of M 16-bit elements.
     static constexpr int kOutRow = M * 2 + 16;
     static constexpr int kLds = kStage * STAGES > kOutRow * N ? kStage * STAGES : kOutRow * N;
@@ -200,11 +206,11 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
                                          uint32_t m0, uint32_t n0, uint32_t begin, uint32_t end,
                                          uint32_t lds)
 {
-    typedef TileOperand<S::M, AROW, S::kWaves> A;
-    typedef TileOperand<S::N, BROW, S::kWaves> B;
+    typedef TileOperand<S::M, S::K, AROW, S::kWaves> A;
+    typedef TileOperand<S::N, S::K, BROW, S::kWaves> B;
     const A ta(a, m0, begin, end);
     const B tb(b, n0, begin, end);
-    const uint32_t stages = (end - begin + kStepK - 1) / kStepK;
+    const uint32_t stages = (end - begin + S::K - 1) / S::K;
 #pragma unroll
     for (int i = 0; i < S::MS; ++i)
 #pragma unroll
@@ -212,39 +218,79 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc.c[i][j][e] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < S::STAGES - 1; ++s) {
-        ta.request(s, lds + s * S::kStage);
-        tb.request(s, lds + s * S::kStage + A::kBytes);
-    }
     const uint32_t wm = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_m());
     const uint32_t wn = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_n());
-    uint32_t cur = 0, next = S::STAGES - 1; // buffers of this stage and of the one requested
+    constexpr int kSteps = S::K / 16, kLoads = A::kLoads + B::kLoads;
+    // Load i of a stage, A's first.
+    const auto request = [&](const u32x4_t& ra, const u32x4_t& rb, int i, uint32_t stage,
+                             uint32_t buffer) {
+        const uint32_t at = lds + buffer * S::kStage;
+        if (i < A::kLoads)
+            ta.request(ra, i, stage, at);
+        else
+            tb.request(rb, i - A::kLoads, stage, at + A::kBytes);
+    };
+    // Two sets of operand registers: while one is multiplied the other is read.
+    s16x8_t fa[2][S::MS], fb[2][S::NS];
+    const auto read = [&](uint32_t buffer, int kk) {
+        const uint32_t at = lds + buffer * S::kStage;
+#pragma unroll
+        for (int j = 0; j < S::NS; ++j)
+            fb[kk & 1][j] = B::read(at + A::kBytes, wn + j * 32, kk);
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+            fa[kk & 1][i] = A::read(at, wm + i * 32, kk);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int s = 0; s < S::STAGES; ++s) {
+        const u32x4_t ra = ta.stage(s), rb = tb.stage(s);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            request(ra, rb, i, s, s);
+    }
+    wait_loads<(S::STAGES - 1) * kLoads>();
+    barrier();
+    read(0, 0);
+    __builtin_amdgcn_s_waitcnt(kLdsDone); // or the loop's first wait is for all its reads
+    uint32_t cur = 0; // this stage's buffer
     for (uint32_t s = 0; s < stages; ++s) {
-        // This wave's loads of the stage have landed; behind the barrier all have,
-        // and nobody reads the buffer of the stage before any more.
-        wait_loads<(S::STAGES - 2) * (A::kLoads + B::kLoads)>();
-        barrier();
-        ta.request(s + S::STAGES - 1, lds + next * S::kStage);
-        tb.request(s + S::STAGES - 1, lds + next * S::kStage + A::kBytes);
-        const uint32_t at = lds + cur * S::kStage;
+        const uint32_t next = cur + 1 == S::STAGES ? 0 : cur + 1;
 #pragma unroll
-        for (int kk = 0; kk < kStepK / 16; ++kk) {
-            s16x8_t fa[S::MS], fb[S::NS];
-#pragma unroll
-            for (int j = 0; j < S::NS; ++j)
-                fb[j] = B::read(at + A::kBytes, wn + j * 32, kk);
-#pragma unroll
-            for (int i = 0; i < S::MS; ++i)
-                fa[i] = A::read(at, wm + i * 32, kk);
+        for (int kk = 0; kk < kSteps - 1; ++kk) {
+            read(cur, kk + 1);
 #pragma unroll
             for (int i = 0; i < S::MS; ++i)
 #pragma unroll
                 for (int j = 0; j < S::NS; ++j)
-                    acc.c[i][j] = mfma<T>(fa[i], fb[j], acc.c[i][j]);
+                    acc.c[i][j] = mfma<T>(fa[kk & 1][i], fb[kk & 1][j], acc.c[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        cur = cur + 1 == S::STAGES ? 0 : cur + 1;
-        next = next + 1 == S::STAGES ? 0 : next + 1;
+        // This wave has read all of the stage, and its loads of the next have landed;
+        // behind the barrier that goes for every wave, so the buffer can take another
+        // stage while this one's last step is multiplied, a load behind each product.
+        wait_loads<(S::STAGES - 2) * kLoads>();
+        barrier();
+        read(next, 0);
+        const u32x4_t ra = ta.stage(s + S::STAGES), rb = tb.stage(s + S::STAGES);
+        constexpr int last = (kSteps - 1) & 1;
+        int load = 0;
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j) {
+                acc.c[i][j] = mfma<T>(fa[last][i], fb[last][j], acc.c[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (load < kLoads)
+                    request(ra, rb, load++, s + S::STAGES, cur);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (i >= S::MS * S::NS)
+                request(ra, rb, i, s + S::STAGES, cur);
+        __builtin_amdgcn_sched_barrier(0);
+        cur = next;
     }
     // The last requests brought zeros to buffers that are not read; they have
     // landed, and every wave is done reading, before LDS is used otherwise.
