@@ -23,6 +23,7 @@
 // products (for dW, whose sum runs over rows, on a copy of the hidden rows).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "linear_ce.hpp"
 #include "mfma_tile.hpp"
@@ -36,14 +37,8 @@ constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr int kHalfShift = 8; // exponent of the largest factors of d in half precision
 
 typedef TileShape<256, 256, 2, 4, 64, 2> BigTile;
-#ifndef MIDT
-#define MIDT 128, 128, 2, 2, 64, 2
-#endif
-#ifndef MIDW
-#define MIDW 128, 128, 2, 2, 32, 2
-#endif
-typedef TileShape<MIDT> MidTile;
-typedef TileShape<MIDW> MidWeight;
+typedef TileShape<128, 128, 2, 2, 32, 4> MidTile;
+typedef TileShape<128, 128, 2, 2, 32, 2> MidWeight;
 typedef TileShape<128, 32, 4, 1, 128, 3> FewTile;
 
 // The hidden rows are padded with zeros to multiples of these.
@@ -63,6 +58,7 @@ struct Lce {
     size_t ldh;        // bytes
     float2* stat;      // maximum and sum of each row and vocabulary tile
     uint32_t tiles_v;
+    float* z;          // kept products, rows x piece
     char* d;           // rows x piece
     uint32_t piece;
     float* dh;         // splits x padded rows x padded width, in tile order
@@ -215,9 +211,17 @@ __device__ __forceinline__ uint32_t lds_of(char (&lds)[S::kLds])
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 }
 
+// Where a tile of few rows starts along k; the others keep in step, since what they
+// read is shared.
+template <class S>
+__device__ __forceinline__ uint32_t turn_of(uint32_t tile)
+{
+    return S::N < 256 ? tile * 3 : 0;
+}
+
 // ---- forward ------------------------------------------------------------------
 
-template <class T, class S>
+template <class T, class S, bool KEEP>
 __global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t first,
                                                                uint32_t tiles_m, uint32_t tiles_n)
 {
@@ -231,10 +235,25 @@ __global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t f
     const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
     const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
     TileAcc<S> acc;
-    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds);
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(t.m));
 
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0; // columns of this tile
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < S::NS; ++j) {
+            const uint32_t n = n0 + acc.n(j);
+            if (n < rows)
+#pragma unroll
+                for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        if (acc.m(i, e) < left) // a.piece is a multiple of 4
+                            *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v0 + acc.m(i, e)) =
+                                f32x4_t{acc.c[i][j][e], acc.c[i][j][e + 1], acc.c[i][j][e + 2],
+                                        acc.c[i][j][e + 3]};
+        }
+    }
     float2* part = reinterpret_cast<float2*>(buffer); // [WM][N]
 #pragma unroll
     for (int j = 0; j < S::NS; ++j) {
@@ -300,13 +319,25 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
 {
     const float2* stat = a.stat + (size_t)n * a.tiles_v;
     const float c = a.c.scale * kLog2ef;
+    // The first 512 tiles stay in registers between the maximum and the sum.
+    constexpr uint32_t kHeld = 8;
+    float2 held[kHeld];
     float m = -INFINITY;
-    for (uint32_t k = lane; k < a.tiles_v; k += kWave)
+#pragma unroll
+    for (uint32_t k = 0; k < kHeld; ++k)
+        held[k] = lane + k * kWave < a.tiles_v ? stat[lane + k * kWave] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (uint32_t k = 0; k < kHeld; ++k)
+        m = fmaxf(m, held[k].x);
+    for (uint32_t k = lane + kHeld * kWave; k < a.tiles_v; k += kWave)
         m = fmaxf(m, stat[k].x);
     m = wave_reduce<OpMax>(m);
     const float ref = m == -INFINITY ? 0.0f : m;
     double s = 0.0;
-    for (uint32_t k = lane; k < a.tiles_v; k += kWave) {
+#pragma unroll
+    for (uint32_t k = 0; k < kHeld; ++k)
+        s += (double)(held[k].y * __builtin_amdgcn_exp2f((held[k].x - ref) * c));
+    for (uint32_t k = lane + kHeld * kWave; k < a.tiles_v; k += kWave) {
         const float2 p = stat[k];
         s += (double)(p.y * __builtin_amdgcn_exp2f((p.x - ref) * c));
     }
@@ -358,10 +389,13 @@ __global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
         for (int k = 0; k < kJoinWaves; ++k)
             v += lds[k];
         store_shared(a.loss_part + blockIdx.x, v);
-        lds_before = count_shared(a.count + 2);
+        if (gridDim.x == 1)
+            a.c.loss[0] = (float)((a.c.accum ? (double)a.c.loss[0] : 0.0) + v);
+        else
+            lds_before = count_shared(a.count + 2);
     }
     __syncthreads();
-    if (lds_before != gridDim.x - 1)
+    if (gridDim.x == 1 || lds_before != gridDim.x - 1)
         return;
     double v = 0.0;
     for (uint32_t k = threadIdx.x; k < gridDim.x; k += kJoinThreads)
@@ -386,6 +420,7 @@ __global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
 // with kAhead steps, 512 bytes of each row, in flight twice over; the hidden rows
 // stay in LDS (16 bytes of padding a row spread 16 rows over the banks).
 constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 8;
+constexpr uint32_t kTurn = 2 * kAhead * 32; // steps of k
 constexpr size_t kStreamLds = 144 * 1024;
 
 template <class T>
@@ -401,63 +436,69 @@ __device__ __forceinline__ f32x4_t mfma16(const s16x8_t& a, const s16x8_t& b, co
 
 __device__ const u32x4_t kNothing = {0, 0, 0, 0};
 
-// The products of columns v0 .. v0 + 15 (from `end` on, of end - 1 again): lane l has
-// those of hidden row l % ROWS with columns v0 + 4 (l / 16) + e.
-template <class T>
-__device__ __forceinline__ f32x4_t stream_columns(const Lce& a, const char* lds_row, uint32_t v0,
-                                                  uint32_t end)
+// Columns [begin, end) of the layer for all rows, a run of blocks of 16 to each
+// workgroup.  f takes the products of a block: lane l has those of hidden row l % ROWS
+// with columns v .. v + 3, v = the block's first + 4 (l / 16).
+template <class T, int ROWS, class F>
+__device__ __forceinline__ void stream_layer(const Lce& a, char* lds, uint32_t begin, uint32_t end, F f)
 {
     const uint32_t lane = threadIdx.x % kWave, part = lane / 16;
-    const uint32_t v = v0 + lane % 16 < end ? v0 + lane % 16 : end - 1;
-    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
-                                                        (size_t)v * a.c.ldw * 2) + part;
-    const uint32_t D = (uint32_t)a.c.D, steps = (D + 31) / 32;
-    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t blocks = (end - begin + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
+    const uint32_t first = blockIdx.x * per, last = first + per < blocks ? first + per : blocks;
+    const uint32_t D = (uint32_t)a.c.D, turns = (D + kTurn - 1) / kTurn;
+    const uint32_t from = (blockIdx.x * kStreamWaves + threadIdx.x / kWave) * 5 % turns;
+    // The lane's row of block b, its last one again past the end.
+    const auto row_of = [&](uint32_t b) {
+        const uint32_t v = begin + b * 16 + lane % 16;
+        return reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
+                                                (size_t)(v < end ? v : end - 1) * a.c.ldw * 2) +
+               part;
+    };
     u32x4_t w[2][kAhead];
-    const auto request = [&](uint32_t s, u32x4_t (&to)[kAhead]) {
+    const auto request = [&](const u32x4_t* p, uint32_t s, u32x4_t (&to)[kAhead]) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             to[i] = *((s + i) * 32 + part * 8 < D ? p + (s + i) * 4 : &kNothing);
     };
-    const auto multiply = [&](uint32_t s, const u32x4_t (&from)[kAhead]) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (s + i < steps) {
-                const s16x8_t h = *reinterpret_cast<const s16x8_t*>(lds_row + (s + i) * 64 + part * 16);
-                acc = mfma16<T>(__builtin_bit_cast(s16x8_t, from[i]), h, acc);
-            }
-        }
-    };
-    request(0, w[0]);
-    for (uint32_t s = 0; s < steps; s += 2 * kAhead) {
-        request(s + kAhead, w[1]);
-        multiply(s, w[0]);
-        request(s + 2 * kAhead, w[0]);
-        multiply(s + kAhead, w[1]);
-    }
-    return acc;
-}
-
-// Columns [begin, end) of the layer for all rows, a run of them to each workgroup.
-// F::column takes each lane's four products.
-template <class T, int ROWS, class F>
-__device__ __forceinline__ void stream_layer(const Lce& a, char* lds, uint32_t begin, uint32_t end, F f)
-{
-    const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16);
+    uint32_t b = first + threadIdx.x / kWave;
+    const u32x4_t* p = row_of(b < last ? b : first);
+    if (b < last)
+        request(p, from * (2 * kAhead), w[0]);
+    // The hidden rows, zeros behind those that count.
+    const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16), rows = a.count[0];
+#pragma unroll 8
     for (uint32_t i = threadIdx.x; i < ROWS * chunks; i += kStreamThreads)
         *reinterpret_cast<u32x4_t*>(lds + i / chunks * stride + i % chunks * 16) =
-            *reinterpret_cast<const u32x4_t*>(a.h + i / chunks * a.ldh + i % chunks * 16);
+            *(i / chunks < rows ? reinterpret_cast<const u32x4_t*>(a.h + i / chunks * a.ldh) + i % chunks
+                                : &kNothing);
     __syncthreads();
-    const uint32_t blocks = (end - begin + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
-    const uint32_t first = blockIdx.x * per, last = first + per < blocks ? first + per : blocks;
-    for (uint32_t b = first + threadIdx.x / kWave; b < last; b += kStreamWaves) {
-        const uint32_t v0 = begin + b * 16;
-        f(stream_columns<T>(a, lds + threadIdx.x % ROWS * stride, v0, end),
-          v0 + threadIdx.x % kWave / 16 * 4);
+    const char* mine = lds + threadIdx.x % ROWS * stride + part * 16;
+    f32x4_t acc;
+    const auto multiply = [&](uint32_t s, const u32x4_t (&from)[kAhead]) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if ((s + i) * 32 < D)
+                acc = mfma16<T>(__builtin_bit_cast(s16x8_t, from[i]),
+                                *reinterpret_cast<const s16x8_t*>(mine + (s + i) * 64), acc);
+    };
+    for (; b < last; b += kStreamWaves) {
+        const u32x4_t* next = row_of(b + kStreamWaves < last ? b + kStreamWaves : b);
+        acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t turn = from;
+        for (uint32_t k = 0; k < turns; ++k) {
+            const uint32_t s = turn * (2 * kAhead);
+            turn = turn + 1 == turns ? 0 : turn + 1;
+            request(p, s + kAhead, w[1]);
+            multiply(s, w[0]);
+            request(k + 1 < turns ? p : next, turn * (2 * kAhead), w[0]);
+            multiply(s + kAhead, w[1]);
+        }
+        f(acc, begin + b * 16 + part * 4);
+        p = next;
     }
 }
 
-template <class T, int ROWS>
+template <class T, int ROWS, bool KEEP>
 __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
 {
     extern __shared__ __align__(16) char buffer[];
@@ -467,6 +508,8 @@ __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
     const float c = a.c.scale * kLog2ef;
     float m = -INFINITY, s = 0.0f;
     stream_layer<T, ROWS>(a, buffer, 0, V, [&](const f32x4_t& z, uint32_t v) {
+        if (KEEP && in && v < V)
+            *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v) = z;
         float most = m;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -496,31 +539,6 @@ __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
     a.stat[(size_t)n * a.tiles_v + blockIdx.x] = make_float2(m, s);
 }
 
-template <class T, int ROWS>
-__global__ __launch_bounds__(kStreamThreads) void lce_stream_d_kernel(Lce a, uint32_t first)
-{
-    extern __shared__ __align__(16) char buffer[];
-    const uint32_t n = threadIdx.x % 16, rows = a.count[0];
-    const uint32_t left = (uint32_t)a.c.V - first, cols = left < a.piece ? left : a.piece;
-    const bool in = n < rows && n < ROWS;
-    const uint32_t target = in ? (uint32_t)a.target[n] : ~0u;
-    const float c = a.c.scale * kLog2ef, lse2 = in ? a.lse2[n] : 0.0f;
-    const float fa = in ? a.fa[n] : 0.0f, fb = in ? a.fb[n] : 0.0f;
-    stream_layer<T, ROWS>(a, buffer, first, first + cols, [&](const f32x4_t& z, uint32_t v) {
-        uint64_t packed = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float d = fa * __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], c, -lse2));
-            d = v + e == target ? d - fb : d;
-            d = v + e < first + cols ? d : 0.0f;
-            packed |= (uint64_t)(uint16_t)T::narrow(d) << (16 * e);
-        }
-        if (in)
-            *reinterpret_cast<uint64_t*>(reinterpret_cast<uint16_t*>(a.d) + (size_t)n * a.piece + v - first) =
-                packed;
-    });
-}
-
 // ---- gradients --------------------------------------------------------------
 
 // Half precision: the hidden rows times 2^(e - the largest e).
@@ -542,6 +560,28 @@ __global__ __launch_bounds__(256) void lce_scale_kernel(Lce a)
     }
 }
 
+// d from the kept products: eight columns a thread.
+template <class T>
+__global__ __launch_bounds__(kBlock) void lce_kept_kernel(Lce a, uint32_t blocks)
+{
+    const uint32_t n = blockIdx.x / blocks, v = (blockIdx.x % blocks * kBlock + threadIdx.x) * 8;
+    const uint32_t V = (uint32_t)a.c.V;
+    if (n >= a.count[0] || v >= V)
+        return;
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.z + (size_t)n * a.piece + v);
+    const f32x4_t z[2] = {p[0], p[1]}; // past V anything
+    const float c = a.c.scale * kLog2ef, lse2 = a.lse2[n], fa = a.fa[n], fb = a.fb[n];
+    const uint32_t target = (uint32_t)a.target[n];
+    float d[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        d[e] = fa * __builtin_amdgcn_exp2f(__builtin_fmaf(z[e / 4][e % 4], c, -lse2));
+        d[e] = v + e == target ? d[e] - fb : d[e];
+        d[e] = v + e < V ? d[e] : 0.0f;
+    }
+    *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.d) + (size_t)n * a.piece + v) = T::pack(d);
+}
+
 // d of the piece that starts at column `first`, rows of a.piece elements.
 template <class T, class S>
 __global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t first, uint32_t tiles_n)
@@ -556,7 +596,7 @@ __global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t firs
     const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
     const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
     TileAcc<S> acc;
-    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds);
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(t.m));
 
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0;
@@ -571,7 +611,7 @@ __global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t firs
         fb[j] = in ? a.fb[n] : 0.0f;
         at[j] = in ? (uint32_t)a.target[n] - v0 : ~0u;
     }
-    store_tile<T>(acc, lds, S::M, [&](float z, int i, int j, int e) {
+    store_tile<T, false>(acc, lds, S::M, [&](float z, int i, int j, int e) {
         const uint32_t m = acc.m(i, e);
         float d = fa[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -lse2[j]));
         d = m == at[j] ? d - fb[j] : d;
@@ -678,7 +718,7 @@ __global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t fir
     TileAcc<S> acc;
     multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
     const float f = __is_same(T, ElemF16) && rows ? ldexpf(1.0f, (int)a.count[1] - kHalfShift) : 1.0f;
-    store_tile<T>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
+    store_tile<T, true>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
                   [&](uint32_t n) -> uint16_t* {
                       return n0 + n < left ? static_cast<uint16_t*>(a.c.dweight) +
                                                  (size_t)(first + n0 + n) * a.c.lddw + m0
@@ -695,6 +735,11 @@ constexpr uint32_t kTilesPerLaunch = 1u << 22;
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
+// Where the vocabulary is one piece and its products (fp32) take no more than this,
+// they are kept from the first pass for the gradients: writing and reading them costs
+// less than the layer's rows again, unless those are short.
+constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640;
+
 // Rows up to which lce_gather_kernel goes alone.
 constexpr size_t kRowsAlone = 1024;
 
@@ -708,6 +753,7 @@ struct LcePlan {
     uint32_t tiles_v, tiles_n, tiles_d;
     size_t rows, piece, splits, bytes;
     size_t stream_rows, stream_lds;
+    bool keep;
 };
 
 template <class F>
@@ -784,6 +830,10 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     w.take(o.stat, sizeof(float2) * p.tiles_v * c.rows);
     o.piece = (uint32_t)p.piece;
     o.splits = (uint32_t)p.splits;
+    p.keep = grad && p.piece >= c.V && 4 * p.piece * c.rows <= kKeptBytes &&
+             (p.kind == Kind::Stream || c.D >= kKeptWidth);
+    if (p.keep)
+        w.take(o.z, 4 * p.piece * c.rows);
     if (grad)
         w.take(o.d, 2 * p.piece * n);
     if (c.dhidden)
@@ -804,25 +854,33 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
         hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
         hipLaunchKernelGGL(lce_gather_kernel<false>, gather, dim3(256), 0, s, a);
     }
-    if (p.kind == Kind::Stream) {
-        if (p.stream_rows == 8)
-            hipLaunchKernelGGL((lce_stream_stat_kernel<T, 8>), dim3(p.tiles_v), dim3(kStreamThreads),
-                               p.stream_lds, s, a);
-        else
-            hipLaunchKernelGGL((lce_stream_stat_kernel<T, 16>), dim3(p.tiles_v), dim3(kStreamThreads),
-                               p.stream_lds, s, a);
-    } else {
+    const auto stat = [&](auto keep) {
+        constexpr bool KEEP = decltype(keep)::value;
+        if (p.kind == Kind::Stream) {
+            const dim3 grid(p.tiles_v), threads(kStreamThreads);
+            if (p.stream_rows == 8)
+                hipLaunchKernelGGL((lce_stream_stat_kernel<T, 8, KEEP>), grid, threads, p.stream_lds,
+                                   s, a);
+            else
+                hipLaunchKernelGGL((lce_stream_stat_kernel<T, 16, KEEP>), grid, threads, p.stream_lds,
+                                   s, a);
+            return;
+        }
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
             const uint32_t most = std::max(8u, kTilesPerLaunch / p.tiles_n);
             for (uint32_t first = 0; first < p.tiles_v; first += most) {
                 const uint32_t tiles_m = std::min(most, p.tiles_v - first);
-                hipLaunchKernelGGL((lce_stat_kernel<T, S>), dim3(tiles_m * p.tiles_n),
+                hipLaunchKernelGGL((lce_stat_kernel<T, S, KEEP>), dim3(tiles_m * p.tiles_n),
                                    dim3(S::kThreads), 0, s, a, first, tiles_m, p.tiles_n);
             }
             return 0;
         });
-    }
+    };
+    if (p.keep)
+        stat(std::true_type());
+    else
+        stat(std::false_type());
     hipLaunchKernelGGL(lce_join_kernel<T>, dim3((unsigned)((c.rows + kJoinWaves - 1) / kJoinWaves)),
                        dim3(kJoinThreads), 0, s, a);
     if (!c.dhidden && !c.dweight)
@@ -831,18 +889,15 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
         hipLaunchKernelGGL(lce_scale_kernel, dim3((unsigned)p.rows), dim3(256), 0, s, a);
     for (size_t first = 0; first < c.V; first += p.piece) {
         const uint32_t f = (uint32_t)first;
-        if (p.kind == Kind::Stream) {
-            if (p.stream_rows == 8)
-                hipLaunchKernelGGL((lce_stream_d_kernel<T, 8>), dim3(p.tiles_v), dim3(kStreamThreads),
-                                   p.stream_lds, s, a, f);
-            else
-                hipLaunchKernelGGL((lce_stream_d_kernel<T, 16>), dim3(p.tiles_v), dim3(kStreamThreads),
-                                   p.stream_lds, s, a, f);
+        if (p.keep) {
+            const uint32_t blocks = (uint32_t)((c.V + 8 * kBlock - 1) / (8 * kBlock));
+            hipLaunchKernelGGL(lce_kept_kernel<T>, dim3((unsigned)c.rows * blocks), dim3(kBlock), 0, s,
+                               a, blocks);
         }
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
             const uint32_t tiles_m = (uint32_t)p.piece / S::M;
-            if (p.kind != Kind::Stream)
+            if (!p.keep)
                 hipLaunchKernelGGL((lce_d_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads),
                                    0, s, a, f, p.tiles_n);
             if (c.dhidden)

@@ -141,13 +141,13 @@ struct TileOperand {
         rsrc.w = 0x00020000u;
         return rsrc;
     }
-    // Requests load i of stage number `stage` (rsrc) into LDS at `lds`; a stage past
-    // the last one brings zeros.
-    __device__ __forceinline__ void request(const u32x4_t& rsrc, int i, uint32_t stage,
+    // Requests load i of stage number `stage` (rsrc) into LDS at `lds`; zeros where
+    // not `wanted`.
+    __device__ __forceinline__ void request(const u32x4_t& rsrc, int i, uint32_t stage, bool wanted,
                                             uint32_t lds) const
     {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        load_to_lds(rsrc, stage * K + k_of[i] < k ? offset[i] : kOutside,
+        load_to_lds(rsrc, stage * K + k_of[i] < (wanted ? k : 0) ? offset[i] : kOutside,
                     lds + (i * WAVES + wave) * 1024);
     }
 
@@ -201,10 +201,13 @@ struct TileAcc {
     static __device__ __forceinline__ uint32_t n(int j) { return wave_n() + j * 32 + threadIdx.x % 32; }
 };
 
+// The tile at (m0, n0) over steps [begin, end) of k, in the order of the stages from
+// number `turn` on and round.  (Workgroups that read rows of the same length from
+// memory in step ask the same few channels at a time; different turns spread them.)
 template <class T, class S, bool AROW, bool BROW>
 __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, const Operand& b,
                                          uint32_t m0, uint32_t n0, uint32_t begin, uint32_t end,
-                                         uint32_t lds)
+                                         uint32_t lds, uint32_t turn = 0)
 {
     typedef TileOperand<S::M, S::K, AROW, S::kWaves> A;
     typedef TileOperand<S::N, S::K, BROW, S::kWaves> B;
@@ -221,14 +224,16 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
     const uint32_t wm = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_m());
     const uint32_t wn = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_n());
     constexpr int kSteps = S::K / 16, kLoads = A::kLoads + B::kLoads;
-    // Load i of a stage, A's first.
-    const auto request = [&](const u32x4_t& ra, const u32x4_t& rb, int i, uint32_t stage,
-                             uint32_t buffer) {
-        const uint32_t at = lds + buffer * S::kStage;
+    // Turn number s works on stage (s + turn) mod stages.
+    const uint32_t from = turn % (stages ? stages : 1);
+    const auto stage_of = [&](uint32_t s) { return s + from < stages ? s + from : s + from - stages; };
+    // Load i of turn s, A's first; past the last turn it brings zeros.
+    const auto request = [&](const u32x4_t& ra, const u32x4_t& rb, int i, uint32_t s, uint32_t buffer) {
+        const uint32_t at = lds + buffer * S::kStage, stage = stage_of(s);
         if (i < A::kLoads)
-            ta.request(ra, i, stage, at);
+            ta.request(ra, i, stage, s < stages, at);
         else
-            tb.request(rb, i - A::kLoads, stage, at + A::kBytes);
+            tb.request(rb, i - A::kLoads, stage, s < stages, at + A::kBytes);
     };
     // Two sets of operand registers: while one is multiplied the other is read.
     s16x8_t fa[2][S::MS], fb[2][S::NS];
@@ -244,7 +249,7 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
     };
 #pragma unroll
     for (int s = 0; s < S::STAGES; ++s) {
-        const u32x4_t ra = ta.stage(s), rb = tb.stage(s);
+        const u32x4_t ra = ta.stage(stage_of(s)), rb = tb.stage(stage_of(s));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             request(ra, rb, i, s, s);
@@ -272,7 +277,8 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
         wait_loads<(S::STAGES - 2) * kLoads>();
         barrier();
         read(next, 0);
-        const u32x4_t ra = ta.stage(s + S::STAGES), rb = tb.stage(s + S::STAGES);
+        const u32x4_t ra = ta.stage(stage_of(s + S::STAGES));
+        const u32x4_t rb = tb.stage(stage_of(s + S::STAGES));
         constexpr int last = (kSteps - 1) & 1;
         int load = 0;
 #pragma unroll
@@ -300,7 +306,8 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
 
 // The tile as 16-bit elements f(value, i, j, e), to rows n of memory:
 // row(n) gives a row's first element for column m0, or null.  cols: valid columns.
-template <class T, class S, class F, class Rows>
+// PASS: nobody reads them soon, they pass the caches by.
+template <class T, bool PASS, class S, class F, class Rows>
 __device__ __forceinline__ void store_tile(const TileAcc<S>& acc, uint32_t lds, uint32_t cols, F f,
                                            Rows row)
 {
@@ -328,7 +335,11 @@ __device__ __forceinline__ void store_tile(const TileAcc<S>& acc, uint32_t lds, 
             continue;
         const u32x4_t v = *(ptr16)(lds + n * S::kOutRow + c * 16);
         if (c * 8 + 8 <= cols) {
-            *reinterpret_cast<u32x4u_t*>(out + c * 8) = u32x4u_t{v.x, v.y, v.z, v.w};
+            if constexpr (PASS)
+                __builtin_nontemporal_store(u32x4u_t{v.x, v.y, v.z, v.w},
+                                            reinterpret_cast<u32x4u_t*>(out + c * 8));
+            else
+                *reinterpret_cast<u32x4u_t*>(out + c * 8) = u32x4u_t{v.x, v.y, v.z, v.w};
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
