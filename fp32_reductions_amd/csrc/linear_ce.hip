@@ -122,21 +122,34 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
 {
     const size_t r = blockIdx.x;
     const uint32_t D = (uint32_t)a.c.D, chunks = (uint32_t)(a.ldh / 16);
-    const uint16_t* from = nullptr;
+    const bool real = r < a.c.rows;
+    const uint16_t* from = static_cast<const uint16_t*>(a.c.hidden) + (real ? r * a.c.ldh : 0);
+    // This thread's first chunk of the row is on its way while its place is found.
+    // (Past D there are zeros; D is a multiple of 8.)
+    const auto chunk = [&](uint32_t i) {
+        u32x4_t v = {0, 0, 0, 0};
+        if (real && i * 8 < D) {
+            const u32x4u_t u = reinterpret_cast<const u32x4u_t*>(from)[i];
+            v = u32x4_t{u.x, u.y, u.z, u.w};
+        }
+        return v;
+    };
+    const u32x4_t first = chunk(threadIdx.x);
     uint32_t to;
     int32_t at;
     if constexpr (ALONE) {
         __shared__ uint32_t lds[kWaves];
-        const uint32_t before = (uint32_t)(r < a.c.rows ? r : a.c.rows);
+        const uint32_t before = (uint32_t)(real ? r : a.c.rows);
         uint32_t n = 0;
+#pragma unroll 4
         for (uint32_t i = threadIdx.x; i < before; i += 256)
             n += counted(a.c, i);
+        const bool counts = real && counted(a.c, r);
         n = (uint32_t)wave_sum64((double)n);
         if (threadIdx.x % kWave == 0)
             lds[threadIdx.x / kWave] = n;
         __syncthreads();
         at = (int32_t)(lds[0] + lds[1] + lds[2] + lds[3]);
-        const bool counts = r < a.c.rows && counted(a.c, r);
         if (threadIdx.x == 0) {
             if (counts) {
                 a.row[at] = (int32_t)r;
@@ -149,12 +162,12 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
                 a.count[2] = 0;
             }
         }
-        if (r < a.c.rows && !counts)
+        if (real && !counts)
             at = -1;
     } else {
-        at = r < a.c.rows ? a.where[r] : (int32_t)a.count[0];
+        at = real ? a.where[r] : (int32_t)a.count[0];
     }
-    if (r < a.c.rows) {
+    if (real) {
         if (at < 0) {
             if (threadIdx.x == 0) {
                 if (a.c.logp)
@@ -170,21 +183,16 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
             return;
         }
         to = (uint32_t)at;
-        from = static_cast<const uint16_t*>(a.c.hidden) + r * a.c.ldh;
     } else {
         to = (uint32_t)at + (uint32_t)(r - a.c.rows);
         if (to >= round_up32((uint32_t)at, kRowPad))
             return;
     }
     u32x4_t* out = reinterpret_cast<u32x4_t*>(a.h + to * a.ldh);
-    for (uint32_t i = threadIdx.x; i < chunks; i += 256) {
-        u32x4_t v = {0, 0, 0, 0};
-        if (from && i * 8 < D) { // D is a multiple of 8
-            const u32x4u_t u = reinterpret_cast<const u32x4u_t*>(from)[i];
-            v = u32x4_t{u.x, u.y, u.z, u.w};
-        }
-        out[i] = v;
-    }
+    if (threadIdx.x < chunks)
+        out[threadIdx.x] = first;
+    for (uint32_t i = threadIdx.x + 256; i < chunks; i += 256)
+        out[i] = chunk(i);
 }
 
 // ---- tiles ------------------------------------------------------------------
@@ -321,6 +329,8 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
     const float c = a.c.scale * kLog2ef;
     // The first 512 tiles stay in registers between the maximum and the sum.
     constexpr uint32_t kHeld = 8;
+    const float zt = a.zt[n], weight = a.w[n];
+    const uint32_t r = (uint32_t)a.row[n];
     float2 held[kHeld];
     float m = -INFINITY;
 #pragma unroll
@@ -344,10 +354,9 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
     s = wave_sum64(s);
     if (lane)
         return 0.0;
-    const double scale = a.c.scale, w = a.w[n];
+    const double scale = a.c.scale, w = weight;
     const double ln = log(s), lse = scale * (double)ref + ln;
-    const double logp = scale * ((double)a.zt[n] - (double)ref) - ln;
-    const uint32_t r = (uint32_t)a.row[n];
+    const double logp = scale * ((double)zt - (double)ref) - ln;
     if (a.c.logp)
         a.c.logp[r] = (float)logp;
     if (a.c.lse)
@@ -741,7 +750,7 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640;
 
 // Rows up to which lce_gather_kernel goes alone.
-constexpr size_t kRowsAlone = 1024;
+constexpr size_t kRowsAlone = 2048;
 
 enum class Kind { Stream, Few, Mid, Big };
 
