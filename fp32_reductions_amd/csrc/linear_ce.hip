@@ -421,16 +421,27 @@ __global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
     }
 }
 
-// ---- up to 16 rows ------------------------------------------------------------
+// ---- a few rows ---------------------------------------------------------------
 //
 // The layer is only read, so what counts is the rate of its reading: each wave
 // takes 16 of its rows from end to end, straight into the operand registers of
 // v_mfma_f32_16x16x32 (lane l: row l % 16, 16 bytes at 64 s + 16 (l / 16) in step s),
 // with kAhead steps, 512 bytes of each row, in flight twice over; the hidden rows
-// stay in LDS (16 bytes of padding a row spread 16 rows over the banks).
+// stay in LDS (16 bytes of padding a row spread 16 rows over the banks).  Waves start
+// at different places of their rows: in step they ask the same few memory channels
+// at a time (1 row against 32768 x 4096: 55 us in step, 49 so; tiles through LDS
+// took 59).  Where there are fewer blocks of 16 rows than waves, the waves of a
+// workgroup share a block's steps and their sums meet in LDS, in order.
 constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 8;
 constexpr uint32_t kTurn = 2 * kAhead * 32; // steps of k
-constexpr size_t kStreamLds = 144 * 1024;
+constexpr size_t kStreamLds = 156 * 1024;
+constexpr size_t kStreamRowsMax = 64;
+
+// LDS for `rows` hidden rows of ldh bytes, and for the waves' sums.
+constexpr size_t stream_lds(size_t rows, size_t ldh)
+{
+    return rows * (ldh + 16) + (rows + 15) / 16 * kStreamWaves * kWave * sizeof(f32x4_t);
+}
 
 template <class T>
 __device__ __forceinline__ f32x4_t mfma16(const s16x8_t& a, const s16x8_t& b, const f32x4_t& c)
@@ -445,22 +456,27 @@ __device__ __forceinline__ f32x4_t mfma16(const s16x8_t& a, const s16x8_t& b, co
 
 __device__ const u32x4_t kNothing = {0, 0, 0, 0};
 
-// Columns [begin, end) of the layer for all rows, a run of blocks of 16 to each
-// workgroup.  f takes the products of a block: lane l has those of hidden row l % ROWS
-// with columns v .. v + 3, v = the block's first + 4 (l / 16).
-template <class T, int ROWS, class F>
-__device__ __forceinline__ void stream_layer(const Lce& a, char* lds, uint32_t begin, uint32_t end, F f)
+// Columns [0, V) of the layer for G groups of 16 hidden rows, a run of blocks of 16
+// columns to each workgroup.  f takes the products of a block: lane l has, in acc[g],
+// those of hidden row 16 g + l % 16 (past the call's last row, of that one) with columns
+// v .. v + 3, v = the block's first + 4 (l / 16).
+template <class T, int G, class F>
+__device__ __forceinline__ void stream_layer(const Lce& a, char* lds, F f)
 {
-    const uint32_t lane = threadIdx.x % kWave, part = lane / 16;
-    const uint32_t blocks = (end - begin + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
+    const uint32_t lane = threadIdx.x % kWave, part = lane / 16, wave = threadIdx.x / kWave;
+    const uint32_t V = (uint32_t)a.c.V, D = (uint32_t)a.c.D, turns = (D + kTurn - 1) / kTurn;
+    const uint32_t blocks = (V + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
     const uint32_t first = blockIdx.x * per, last = first + per < blocks ? first + per : blocks;
-    const uint32_t D = (uint32_t)a.c.D, turns = (D + kTurn - 1) / kTurn;
-    const uint32_t from = (blockIdx.x * kStreamWaves + threadIdx.x / kWave) * 5 % turns;
-    // The lane's row of block b, its last one again past the end.
+    const bool share = per < (uint32_t)kStreamWaves; // the waves share each block
+    // This wave's blocks, and its turns along k: the first one, how many, how far apart.
+    const uint32_t step = share ? 1 : kStreamWaves, apart = share ? kStreamWaves : 1;
+    const uint32_t from = share ? wave : (blockIdx.x * kStreamWaves + wave) * 5 % turns;
+    const uint32_t count = share ? (turns + kStreamWaves - 1 - wave) / kStreamWaves : turns;
+    // The lane's row of block b; past the last column that one again.
     const auto row_of = [&](uint32_t b) {
-        const uint32_t v = begin + b * 16 + lane % 16;
+        const uint32_t v = b * 16 + lane % 16;
         return reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
-                                                (size_t)(v < end ? v : end - 1) * a.c.ldw * 2) +
+                                                (size_t)(v < V ? v : V - 1) * a.c.ldw * 2) +
                part;
     };
     u32x4_t w[2][kAhead];
@@ -469,83 +485,129 @@ __device__ __forceinline__ void stream_layer(const Lce& a, char* lds, uint32_t b
         for (int i = 0; i < kAhead; ++i)
             to[i] = *((s + i) * 32 + part * 8 < D ? p + (s + i) * 4 : &kNothing);
     };
-    uint32_t b = first + threadIdx.x / kWave;
-    const u32x4_t* p = row_of(b < last ? b : first);
-    if (b < last)
+    uint32_t b = first + (share ? 0 : wave);
+    const u32x4_t* p = row_of(b < last ? b : 0);
+    if (b < last && count)
         request(p, from * (2 * kAhead), w[0]);
     // The hidden rows, zeros behind those that count.
-    const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16), rows = a.count[0];
+    const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16);
+    const uint32_t held = (uint32_t)a.c.rows, rows = a.count[0];
 #pragma unroll 8
-    for (uint32_t i = threadIdx.x; i < ROWS * chunks; i += kStreamThreads)
+    for (uint32_t i = threadIdx.x; i < held * chunks; i += kStreamThreads)
         *reinterpret_cast<u32x4_t*>(lds + i / chunks * stride + i % chunks * 16) =
             *(i / chunks < rows ? reinterpret_cast<const u32x4_t*>(a.h + i / chunks * a.ldh) + i % chunks
                                 : &kNothing);
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds + held * stride); // waves x G x lanes
     __syncthreads();
-    const char* mine = lds + threadIdx.x % ROWS * stride + part * 16;
-    f32x4_t acc;
+    const char* mine[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint32_t n = lane % 16 + g * 16;
+        mine[g] = lds + (n < held ? n : held - 1) * stride + part * 16;
+    }
+    f32x4_t acc[G];
     const auto multiply = [&](uint32_t s, const u32x4_t (&from)[kAhead]) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if ((s + i) * 32 < D)
-                acc = mfma16<T>(__builtin_bit_cast(s16x8_t, from[i]),
-                                *reinterpret_cast<const s16x8_t*>(mine + (s + i) * 64), acc);
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    acc[g] = mfma16<T>(
+                        __builtin_bit_cast(s16x8_t, from[i]),
+                        *reinterpret_cast<const s16x8_t*>(mine[g] + (s + i) * 64), acc[g]);
     };
-    for (; b < last; b += kStreamWaves) {
-        const u32x4_t* next = row_of(b + kStreamWaves < last ? b + kStreamWaves : b);
-        acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (; b < last; b += step) {
+        const u32x4_t* next = row_of(b + step < last ? b + step : b);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            acc[g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t turn = from;
-        for (uint32_t k = 0; k < turns; ++k) {
+        for (uint32_t k = 0; k < count; ++k) {
             const uint32_t s = turn * (2 * kAhead);
-            turn = turn + 1 == turns ? 0 : turn + 1;
+            turn += apart;
+            if (!share && turn == turns)
+                turn = 0;
+            const bool more = k + 1 < count;
             request(p, s + kAhead, w[1]);
             multiply(s, w[0]);
-            request(k + 1 < turns ? p : next, turn * (2 * kAhead), w[0]);
+            request(more ? p : next, (more ? turn : from) * (2 * kAhead), w[0]);
             multiply(s + kAhead, w[1]);
         }
-        f(acc, begin + b * 16 + part * 4);
         p = next;
+        if (share) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                sums[(wave * G + g) * kWave + lane] = acc[g];
+            __syncthreads();
+            if (wave == 0) {
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int x = 1; x < kStreamWaves; ++x)
+                        acc[g] += sums[(x * G + g) * kWave + lane];
+                f(acc, b * 16 + part * 4);
+            }
+            __syncthreads();
+        } else {
+            f(acc, b * 16 + part * 4);
+        }
     }
 }
 
-template <class T, int ROWS, bool KEEP>
+template <class T, int G, bool KEEP>
 __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
 {
     extern __shared__ __align__(16) char buffer[];
-    const uint32_t n = threadIdx.x % 16, rows = a.count[0], V = (uint32_t)a.c.V;
-    const bool in = n < rows && n < ROWS;
-    const uint32_t target = in ? (uint32_t)a.target[n] : ~0u;
+    const uint32_t n0 = threadIdx.x % 16, rows = a.count[0], V = (uint32_t)a.c.V;
     const float c = a.c.scale * kLog2ef;
-    float m = -INFINITY, s = 0.0f;
-    stream_layer<T, ROWS>(a, buffer, 0, V, [&](const f32x4_t& z, uint32_t v) {
-        if (KEEP && in && v < V)
-            *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v) = z;
-        float most = m;
+    uint32_t target[G];
+    float m[G], s[G];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            most = fmaxf(most, v + e < V ? z[e] : -INFINITY);
-            if (v + e == target)
-                a.zt[n] = z[e];
+    for (int g = 0; g < G; ++g) {
+        target[g] = n0 + g * 16 < rows ? (uint32_t)a.target[n0 + g * 16] : ~0u;
+        m[g] = -INFINITY;
+        s[g] = 0.0f;
+    }
+    stream_layer<T, G>(a, buffer, [&](const f32x4_t (&z)[G], uint32_t v) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint32_t n = n0 + g * 16;
+            if (KEEP && n < rows && v < V)
+                *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v) = z[g];
+            float most = m[g];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                most = fmaxf(most, v + e < V ? z[g][e] : -INFINITY);
+                if (v + e == target[g])
+                    a.zt[n] = z[g][e];
+            }
+            const float ref = most == -INFINITY ? 0.0f : most;
+            s[g] *= __builtin_amdgcn_exp2f((m[g] - ref) * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[g] += v + e < V ? __builtin_amdgcn_exp2f((z[g][e] - ref) * c) : 0.0f;
+            m[g] = most;
         }
-        const float ref = most == -INFINITY ? 0.0f : most;
-        s *= __builtin_amdgcn_exp2f((m - ref) * c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            s += v + e < V ? __builtin_amdgcn_exp2f((z[e] - ref) * c) : 0.0f;
-        m = most;
     });
-    __shared__ float2 part[kStreamWaves * 4][16];
-    part[threadIdx.x / 16][n] = make_float2(m, s);
+    // The workgroup's lanes that have the same row, in order (the sums' LDS).
+    constexpr int kParts = kStreamThreads / 16;
+    float2* part = reinterpret_cast<float2*>(buffer + a.c.rows * (a.ldh + 16));
+    static_assert(kParts * 16 * sizeof(float2) <= kStreamWaves * kWave * sizeof(f32x4_t), "a group's");
     __syncthreads();
-    if (threadIdx.x >= 16 || !in)
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        part[threadIdx.x / 16 * (G * 16) + g * 16 + n0] = make_float2(m[g], s[g]);
+    __syncthreads();
+    const uint32_t n = threadIdx.x;
+    if (n >= G * 16 || n >= rows)
         return;
-    m = -INFINITY;
-    for (int k = 0; k < kStreamWaves * 4; ++k)
-        m = fmaxf(m, part[k][n].x);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    s = 0.0f;
-    for (int k = 0; k < kStreamWaves * 4; ++k)
-        s += part[k][n].y * __builtin_amdgcn_exp2f((part[k][n].x - ref) * c);
-    a.stat[(size_t)n * a.tiles_v + blockIdx.x] = make_float2(m, s);
+    float most = -INFINITY, sum = 0.0f;
+    for (int k = 0; k < kParts; ++k)
+        most = fmaxf(most, part[k * (G * 16) + n].x);
+    const float ref = most == -INFINITY ? 0.0f : most;
+    for (int k = 0; k < kParts; ++k)
+        sum += part[k * (G * 16) + n].y * __builtin_amdgcn_exp2f((part[k * (G * 16) + n].x - ref) * c);
+    a.stat[(size_t)n * a.tiles_v + blockIdx.x] = make_float2(most, sum);
 }
 
 // ---- gradients --------------------------------------------------------------
@@ -752,7 +814,7 @@ constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640;
 // Rows up to which lce_gather_kernel goes alone.
 constexpr size_t kRowsAlone = 2048;
 
-enum class Kind { Stream, Few, Mid, Big };
+enum class Kind { Few, Mid, Big };
 
 // Tiles by the work: 32 rows by 128 columns where there are few rows, whose
 // product only reads the layer; 256 x 256, the fastest, where there are enough of
@@ -761,15 +823,14 @@ struct LcePlan {
     Kind kind, kind_w; // of the products over rows; of the layer's gradient
     uint32_t tiles_v, tiles_n, tiles_d;
     size_t rows, piece, splits, bytes;
-    size_t stream_rows, stream_lds;
-    bool keep;
+    size_t stream_lds;
+    bool stream, keep; // the logits by stream_layer; kept
 };
 
 template <class F>
 auto with_shape(Kind k, F f)
 {
     switch (k) {
-    case Kind::Stream:
     case Kind::Few: return f(FewTile());
     case Kind::Mid: return f(MidTile());
     default: return f(BigTile());
@@ -798,12 +859,11 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     p.rows = round_up(c.rows, kRowsPad);
     const size_t big = round_up(c.V, 256) / 256 * (p.rows / 256);
     o.ldh = round_up(c.D, kWidthPad) * 2;
-    p.stream_rows = c.rows <= 8 ? 8 : 16;
-    p.stream_lds = p.stream_rows * (o.ldh + 16);
-    p.kind = c.rows <= 16 && p.stream_lds <= kStreamLds ? Kind::Stream
-             : c.rows <= 32                             ? Kind::Few
-             : c.rows > 128 && big >= (size_t)dev.cus   ? Kind::Big
-                                                        : Kind::Mid;
+    p.stream_lds = stream_lds(c.rows, o.ldh);
+    p.stream = c.rows <= kStreamRowsMax && p.stream_lds <= kStreamLds;
+    p.kind = c.rows <= 32                             ? Kind::Few
+             : c.rows > 128 && big >= (size_t)dev.cus ? Kind::Big
+                                                      : Kind::Mid;
     size_t tile = 0; // elements
     with_shape(p.kind, [&](auto s) {
         p.tiles_v = (uint32_t)((c.V + s.M - 1) / s.M);
@@ -812,7 +872,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
         tile = (size_t)s.M * s.N;
         return 0;
     });
-    if (p.kind == Kind::Stream)
+    if (p.stream)
         p.tiles_v = (uint32_t)std::min<size_t>((size_t)dev.cus, (c.V + 15) / 16);
     p.kind_w = c.rows <= 128 || p.kind != Kind::Big ? Kind::Mid : Kind::Big;
     p.piece = std::min(round_up(c.V, kColPad),
@@ -840,7 +900,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     o.piece = (uint32_t)p.piece;
     o.splits = (uint32_t)p.splits;
     p.keep = grad && p.piece >= c.V && 4 * p.piece * c.rows <= kKeptBytes &&
-             (p.kind == Kind::Stream || c.D >= kKeptWidth);
+             (p.stream || c.D >= kKeptWidth);
     if (p.keep)
         w.take(o.z, 4 * p.piece * c.rows);
     if (grad)
@@ -865,15 +925,17 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
     }
     const auto stat = [&](auto keep) {
         constexpr bool KEEP = decltype(keep)::value;
-        if (p.kind == Kind::Stream) {
-            const dim3 grid(p.tiles_v), threads(kStreamThreads);
-            if (p.stream_rows == 8)
-                hipLaunchKernelGGL((lce_stream_stat_kernel<T, 8, KEEP>), grid, threads, p.stream_lds,
-                                   s, a);
-            else
-                hipLaunchKernelGGL((lce_stream_stat_kernel<T, 16, KEEP>), grid, threads, p.stream_lds,
-                                   s, a);
-            return;
+        if (p.stream) {
+            const auto go = [&](auto groups) {
+                hipLaunchKernelGGL((lce_stream_stat_kernel<T, decltype(groups)::value, KEEP>),
+                                   dim3(p.tiles_v), dim3(kStreamThreads), p.stream_lds, s, a);
+            };
+            switch ((c.rows + 15) / 16) {
+            case 1: return go(std::integral_constant<int, 1>());
+            case 2: return go(std::integral_constant<int, 2>());
+            case 3: return go(std::integral_constant<int, 3>());
+            default: return go(std::integral_constant<int, 4>());
+            }
         }
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
