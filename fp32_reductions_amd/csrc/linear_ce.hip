@@ -737,11 +737,11 @@ __global__ __launch_bounds__(S::kThreads) void lce_dh_kernel(Lce a, uint32_t fir
 // through LDS to the rows of the call.
 template <class T, class S>
 __global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t tiles_m, uint32_t tiles_n,
-                                                               uint32_t blocks_m)
+                                                               uint32_t blocks_m, uint32_t first)
 {
     constexpr uint32_t kRow = 32 + 8; // elements of a row in LDS
     __shared__ __align__(16) uint16_t lds[32 * kRow];
-    const uint32_t rows = a.count[0], n0 = blockIdx.x / blocks_m * 32, m0 = blockIdx.x % blocks_m * 32;
+    const uint32_t rows = a.count[0], n0 = (first + blockIdx.x / blocks_m) * 32, m0 = blockIdx.x % blocks_m * 32;
     if (n0 >= rows)
         return;
     const uint32_t in_m = m0 % S::M, in_n = n0 % S::N;
@@ -997,8 +997,11 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
             typedef decltype(shape) S;
             const uint32_t blocks_m = (uint32_t)((c.D + 31) / 32);
             const uint32_t blocks_n = (uint32_t)((c.rows + 31) / 32);
-            hipLaunchKernelGGL((lce_dh_finish_kernel<T, S>), dim3(blocks_m * blocks_n), dim3(kBlock),
-                               0, s, a, p.tiles_d, p.tiles_n, blocks_m);
+            const uint32_t most = std::max(1u, kTilesPerLaunch / blocks_m);
+            for (uint32_t first = 0; first < blocks_n; first += most)
+                hipLaunchKernelGGL((lce_dh_finish_kernel<T, S>),
+                                   dim3(blocks_m * std::min(most, blocks_n - first)), dim3(kBlock), 0,
+                                   s, a, p.tiles_d, p.tiles_n, blocks_m, first);
             return 0;
         });
     return hipGetLastError();

@@ -21,7 +21,11 @@ HALF = ["f16", "bf16"]
 SHAPES = [(1, 1, 8), (1, 5, 8), (1, 4097, 1024), (2, 127, 16), (3, 128, 56), (7, 129, 64),
           (31, 1000, 72), (32, 300, 120), (33, 131, 128), (40, 2000, 136), (64, 1023, 192),
           (65, 4096, 200), (100, 255, 8), (127, 257, 320), (128, 999, 512), (129, 640, 72),
-          (130, 5001, 1000), (255, 384, 64), (256, 1280, 264), (257, 2049, 328), (500, 3333, 88)]
+          (130, 5001, 1000), (255, 384, 64), (256, 1280, 264), (257, 2049, 328), (500, 3333, 88),
+          # rows whose layer is streamed: each group of 16, blocks shared by the waves or
+          # not, and widths past the LDS that this takes
+          (8, 70, 520), (9, 40000, 24), (16, 3001, 1032), (17, 515, 2056), (48, 1000, 704),
+          (49, 33, 1400), (64, 5000, 776), (12, 400, 6152), (60, 300, 2504)]
 CASES = [(s, t, cus) for s in SHAPES for t in HALF for cus in (None, 1, 4096)]
 BIG = [((1100, 17001, 136), t, None) for t in HALF] + [((2000, 50001, 264), "bf16", None)]
 
@@ -124,6 +128,23 @@ def test_several_pieces(red, rows, V, D, t):
 
 
 @pytest.mark.parametrize("t", HALF)
+def test_few_rows_and_several_pieces(red, t):
+    """A vocabulary past one piece, whose products are not kept."""
+    say("few rows, pieces %s" % t)
+    h, W, y, w = draw(3, 600001, 16, t, 4)
+    check(run(red, h, W, y, w, t, 1.0, 0.001), ref.linear_ce(h, W, y, w, 1.0, 0.001))
+
+
+@pytest.mark.parametrize("t", HALF)
+@pytest.mark.parametrize("V,D", [(70000, 640), (70000, 632), (140000, 648)])
+def test_products_kept_or_computed_again(red, t, V, D):
+    """On both sides of the width and of the size up to which they are kept."""
+    say("kept or not %d x %d %s" % (V, D, t))
+    h, W, y, w = draw(1040, V, D, t, 5)
+    check(run(red, h, W, y, w, t, 1.0, 0.001), ref.linear_ce(h, W, y, w, 1.0, 0.001))
+
+
+@pytest.mark.parametrize("t", HALF)
 @pytest.mark.parametrize("rows", [9, 90, 700])
 def test_masked_rows_hold_anything(red, monkeypatch, rows, t):
     if rows == 700:
@@ -174,6 +195,16 @@ def test_weights_of_all_sizes(red, t):
         torch.arange(140, device="cuda") % 3 == 0, -1.0, 1.0)
     say("weights %s" % t)
     check(run(red, h, W, y, w, t, zc=0.05), ref.linear_ce(h, W, y, w, 1.0, 0.05))
+
+
+@pytest.mark.parametrize("t", HALF)
+def test_more_rows_than_one_workgroup_counts(red, t):
+    """Rows on both sides of the number up to which each workgroup finds its own
+    row's place."""
+    for rows in (2047, 2048, 2049, 5000):
+        say("places of %d rows %s" % (rows, t))
+        h, W, y, w = draw(rows, 130, 32, t, rows)
+        check(run(red, h, W, y, w, t), ref.linear_ce(h, W, y, w, 1.0, 0.0))
 
 
 @pytest.mark.parametrize("t", HALF)
