@@ -51,7 +51,9 @@ struct Lce {
     uint32_t* count;
     int32_t* where;    // of each row of the call: its place among those that count, or -1
     int32_t *row, *target; // of each row that counts: its number, its target
-    float *w, *zt, *lse2, *fa, *fb, *fs; // weight, target's product, lse log2 e, factors, 2^(e - 8)
+    // Weight, target's product, largest product, log2 of the sum of 2^((z - m) scale log2 e),
+    // factors of d, 2^(e - 8).
+    float *w, *zt, *m, *ls, *fa, *fb, *fs;
     int32_t* e;
     double* loss_part; // of each workgroup that joins rows
     char *h, *hs;      // hidden rows, and in half precision a scaled copy
@@ -361,7 +363,8 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
         a.c.logp[r] = (float)logp;
     if (a.c.lse)
         a.c.lse[r] = (float)lse;
-    a.lse2[n] = (float)(lse * kLog2e64);
+    a.m[n] = ref;
+    a.ls[n] = (float)(ln * kLog2e64);
     double fa = w * scale * (1.0 + 2.0 * (double)a.c.z * lse), fb = w * scale;
     if constexpr (__is_same(T, ElemF16)) {
         const double most = fmax(fabs(fa), fabs(fb));
@@ -641,12 +644,12 @@ __global__ __launch_bounds__(kBlock) void lce_kept_kernel(Lce a, uint32_t blocks
         return;
     const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.z + (size_t)n * a.piece + v);
     const f32x4_t z[2] = {p[0], p[1]}; // past V anything
-    const float c = a.c.scale * kLog2ef, lse2 = a.lse2[n], fa = a.fa[n], fb = a.fb[n];
+    const float c = a.c.scale * kLog2ef, m = a.m[n], ls = a.ls[n], fa = a.fa[n], fb = a.fb[n];
     const uint32_t target = (uint32_t)a.target[n];
     float d[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        d[e] = fa * __builtin_amdgcn_exp2f(__builtin_fmaf(z[e / 4][e % 4], c, -lse2));
+        d[e] = fa * __builtin_amdgcn_exp2f(__builtin_fmaf(z[e / 4][e % 4] - m, c, -ls));
         d[e] = v + e == target ? d[e] - fb : d[e];
         d[e] = v + e < V ? d[e] : 0.0f;
     }
@@ -671,20 +674,21 @@ __global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t firs
 
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0;
-    float lse2[S::NS], fa[S::NS], fb[S::NS];
+    float most[S::NS], ls[S::NS], fa[S::NS], fb[S::NS];
     uint32_t at[S::NS];
 #pragma unroll
     for (int j = 0; j < S::NS; ++j) {
         const uint32_t n = n0 + acc.n(j);
         const bool in = n < rows;
-        lse2[j] = in ? a.lse2[n] : 0.0f;
+        most[j] = in ? a.m[n] : 0.0f;
+        ls[j] = in ? a.ls[n] : 0.0f;
         fa[j] = in ? a.fa[n] : 0.0f;
         fb[j] = in ? a.fb[n] : 0.0f;
         at[j] = in ? (uint32_t)a.target[n] - v0 : ~0u;
     }
     store_tile<T, false>(acc, lds, S::M, [&](float z, int i, int j, int e) {
         const uint32_t m = acc.m(i, e);
-        float d = fa[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(z, c, -lse2[j]));
+        float d = fa[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(z - most[j], c, -ls[j]));
         d = m == at[j] ? d - fb[j] : d;
         return m < left ? d : 0.0f;
     }, [&](uint32_t n) {
@@ -887,7 +891,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     w.take(o.where, 4 * n);
     w.take(o.row, 4 * n);
     w.take(o.target, 4 * n);
-    for (float** f : {&o.w, &o.zt, &o.lse2, &o.fa, &o.fb, &o.fs})
+    for (float** f : {&o.w, &o.zt, &o.m, &o.ls, &o.fa, &o.fb, &o.fs})
         w.take(*f, 4 * n);
     w.take(o.e, 4 * n);
     w.take(o.loss_part, 8 * n / kJoinWaves + 8);

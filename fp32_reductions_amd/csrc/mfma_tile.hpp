@@ -160,14 +160,14 @@ struct TileOperand {
             const uint32_t r = lane % 32;
             const uint32_t a =
                 lds + (row + r) * (K * 2) + ((kk * 2 + half) ^ row_swizzle<K>(r)) * 16;
-            return *(__attribute__((address_space(3))) const s16x8_t*)a;
+            return *(__attribute__((address_space(3))) const s16x8_t*)(uintptr_t)a;
         } else {
             typedef __attribute__((address_space(3))) s16x4_t* ptr;
             const uint32_t i = lane % 16, c = row / 8 + (lane / 16 % 2) * 2 + (i & 3) / 2;
             const uint32_t a = lds + (kk * 16 + half * 8 + i / 4) * (R * 2) +
                                (c ^ (i / 4 << 2)) * 16 + (i & 1) * 8;
-            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)a);
-            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(a + 4 * (R * 2)));
+            const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)a);
+            const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(a + 4 * (R * 2)));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
@@ -323,7 +323,7 @@ __device__ __forceinline__ void store_tile(const TileAcc<S>& acc, uint32_t lds, 
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     q |= (uint64_t)(uint16_t)T::narrow(f(acc.c[i][j][e + x], i, j, e + x)) << (16 * x);
-                *(ptr8)(lds + acc.n(j) * S::kOutRow + acc.m(i, e) * 2) = q;
+                *(ptr8)(uintptr_t)(lds + acc.n(j) * S::kOutRow + acc.m(i, e) * 2) = q;
             }
     barrier();
     constexpr int kPerRow = S::M / 8; // threads of a row
@@ -333,7 +333,7 @@ __device__ __forceinline__ void store_tile(const TileAcc<S>& acc, uint32_t lds, 
         uint16_t* out = row(n);
         if (!out || c * 8 >= cols)
             continue;
-        const u32x4_t v = *(ptr16)(lds + n * S::kOutRow + c * 16);
+        const u32x4_t v = *(ptr16)(uintptr_t)(lds + n * S::kOutRow + c * 16);
         if (c * 8 + 8 <= cols) {
             if constexpr (PASS)
                 __builtin_nontemporal_store(u32x4u_t{v.x, v.y, v.z, v.w},

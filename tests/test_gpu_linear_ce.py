@@ -219,6 +219,36 @@ def test_confident_and_far_logits(red, t):
     check(run(red, h, W, y, None, t), ref.linear_ce(h, W, y, None, 1.0, 0.0))
 
 
+@pytest.mark.parametrize("t", HALF)
+def test_large_logits(red, t):
+    """Logits in the thousands: a row's probabilities rest on differences from its
+    largest, not on its log-sum-exp, whose fp32 step is 1e-4 and more there."""
+    h, W, y, w = draw(200, 800, 64, t, 21)
+    h, W = h * 16, W * 128
+    y.clamp_(0, 799)
+    w[:] = 1.0 / 200
+    say("large logits %s" % t)
+    check(run(red, h, W, y, w, t, scale=0.5), ref.linear_ce(h, W, y, w, 0.5, 0.0))
+    check(run(red, h[:5], W, y[:5], w[:5], t, scale=0.5),
+          ref.linear_ce(h[:5], W, y[:5], w[:5], 0.5, 0.0))
+
+
+@pytest.mark.parametrize("rows", [3, 40, 300])
+def test_subnormal_values_are_kept(red, rows):
+    """Hidden values below f16's normal range against large weights."""
+    h, W, y, _ = draw(rows, 500, 64, "f16", 22, weighted=False)
+    h = (h * 2.0 ** -20).to(h.dtype)
+    W = (W.float() * 2.0 ** 12).to(W.dtype)
+    assert (h.abs().max() < torch.finfo(torch.float16).tiny) and (h != 0).any()
+    say("subnormal %d" % rows)
+    want = ref.linear_ce(h, W, y, None, 1.0, 0.0)
+    assert want["logp"][0].std() > 1e-3  # the values matter
+    check(run(red, h, W, y, None, "f16", scale=1.0), want)
+    # as weights: what the gradient of the rows is made of
+    check(run(red, W[:rows], h[:rows] if rows < 500 else h, y % rows, None, "f16"),
+          ref.linear_ce(W[:rows], h, y % rows, None, 1.0, 0.0))
+
+
 def test_accumulated_loss_and_same_bits(red):
     h, W, y, w = draw(600, 3000, 128, "bf16", 12)
     first = run(red, h, W, y, w, "bf16")
