@@ -18,9 +18,13 @@
 // together (rows D elements, nothing beside rows V D), which also keeps a NaN in
 // a masked row out of dW, and makes the products' operand aligned and padded.
 //
-// In half precision d would lose its small values: it is kept as d 2^(8 - e), e
-// the exponent of its row's factors, put back exactly in fp32 behind the
-// products (for dW, whose sum runs over rows, on a copy of the hidden rows).
+// What is rounded is d without its row's weight: d / (w s) times the mantissa of w over
+// the largest weight, so that where all weights are equal the target's element, the
+// largest, of a row that is unsure of it is -1, exactly.  The weights' exponents and the
+// largest go where they are exact: dh takes them behind its product, in fp32; for dW,
+// whose sum runs over rows, a copy of the hidden rows has the exponents.  In half
+// precision d is 2^4 times larger, which keeps probabilities down to 4e-6 normal
+// numbers and overflows where 1 + 2 c lse passes 2000.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -34,7 +38,7 @@ namespace {
 
 constexpr float kLog2ef = 1.4426950408889634f;
 constexpr double kLog2e64 = 1.4426950408889634074;
-constexpr int kHalfShift = 8; // exponent of the largest factors of d in half precision
+constexpr float kHalfScale = 16.0f; // of d in half precision
 
 typedef TileShape<256, 256, 2, 4, 64, 2> BigTile;
 typedef TileShape<128, 128, 2, 2, 32, 4> MidTile;
@@ -47,16 +51,16 @@ constexpr uint32_t kRowPad = 64, kWidthPad = 64;
 // What the kernels share.  Pointers into the workspace, except those of the call.
 struct Lce {
     LinearCall c;
-    // [0]: rows that count; [1]: largest exponent (int, half precision); [2]: arrivals
+    // [0]: rows that count; [1]: the largest of their weights' magnitudes (float);
+    // [2]: arrivals
     uint32_t* count;
     int32_t* where;    // of each row of the call: its place among those that count, or -1
     int32_t *row, *target; // of each row that counts: its number, its target
     // Weight, target's product, largest product, log2 of the sum of 2^((z - m) scale log2 e),
-    // factors of d, 2^(e - 8).
+    // factors of d, factor of dh.
     float *w, *zt, *m, *ls, *fa, *fb, *fs;
-    int32_t* e;
     double* loss_part; // of each workgroup that joins rows
-    char *h, *hs;      // hidden rows, and in half precision a scaled copy
+    char *h, *hs;      // hidden rows, and a copy times 2^(exponent of their weight)
     size_t ldh;        // bytes
     float2* stat;      // maximum and sum of each row and vocabulary tile
     uint32_t tiles_v;
@@ -81,9 +85,24 @@ __device__ __forceinline__ bool counted(const LinearCall& c, size_t r)
     return weight_of(c, r) != 0.0f && t >= 0 && t < (int64_t)c.V;
 }
 
+// A weight over the largest: mantissa, 1 to 2 in magnitude, and exponent, 0 or less.
+struct Share {
+    float mantissa;
+    int exponent;
+};
+__device__ __forceinline__ Share share_of(float w, float largest)
+{
+    const float r = w / largest;
+    int e = fabsf(r) > 0.0f && fabsf(r) <= 1.0f ? ilogbf(r) : 0; // 0 where one is no number
+    e = e < -100 ? -100 : e;
+    return {ldexpf(r, -e), e};
+}
+
 __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
 {
     __shared__ uint32_t lds[1024 / kWave];
+    __shared__ float lds_w[1024 / kWave];
+    float largest = 0.0f;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     uint32_t before = 0;
     for (size_t first = 0; first < a.c.rows; first += 1024) {
@@ -105,13 +124,20 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
             a.row[at] = (int32_t)r;
             a.target[at] = (int32_t)a.c.targets[r];
             a.w[at] = weight_of(a.c, r);
+            largest = fmaxf(largest, fabsf(weight_of(a.c, r)));
         }
         before += total;
         __syncthreads();
     }
+    largest = wave_reduce<OpMax>(largest);
+    if (lane == 0)
+        lds_w[wave] = largest;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        for (int k = 0; k < 1024 / kWave; ++k)
+            largest = fmaxf(largest, lds_w[k]);
         a.count[0] = before;
-        a.count[1] = (uint32_t)INT32_MIN;
+        a.count[1] = __float_as_uint(largest);
         a.count[2] = 0;
     }
 }
@@ -119,7 +145,7 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
 // One workgroup a row of the call, and kRowPad more for the zeros after the last
 // row that counts.  ALONE: there has been no lce_rows_kernel; with few rows each
 // workgroup counts those before its own itself, which takes less than a launch.
-template <bool ALONE>
+template <class T, bool ALONE>
 __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
 {
     const size_t r = blockIdx.x;
@@ -139,19 +165,27 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
     const u32x4_t first = chunk(threadIdx.x);
     uint32_t to;
     int32_t at;
+    float largest = 0.0f;
     if constexpr (ALONE) {
         __shared__ uint32_t lds[kWaves];
-        const uint32_t before = (uint32_t)(real ? r : a.c.rows);
+        __shared__ float lds_w[kWaves];
         uint32_t n = 0;
 #pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < before; i += 256)
-            n += counted(a.c, i);
+        for (uint32_t i = threadIdx.x; i < a.c.rows; i += 256)
+            if (counted(a.c, i)) {
+                n += i < r;
+                largest = fmaxf(largest, fabsf(weight_of(a.c, i)));
+            }
         const bool counts = real && counted(a.c, r);
         n = (uint32_t)wave_sum64((double)n);
-        if (threadIdx.x % kWave == 0)
+        largest = wave_reduce<OpMax>(largest);
+        if (threadIdx.x % kWave == 0) {
             lds[threadIdx.x / kWave] = n;
+            lds_w[threadIdx.x / kWave] = largest;
+        }
         __syncthreads();
         at = (int32_t)(lds[0] + lds[1] + lds[2] + lds[3]);
+        largest = fmaxf(fmaxf(lds_w[0], lds_w[1]), fmaxf(lds_w[2], lds_w[3]));
         if (threadIdx.x == 0) {
             if (counts) {
                 a.row[at] = (int32_t)r;
@@ -160,7 +194,7 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
             }
             if (r == a.c.rows) {
                 a.count[0] = (uint32_t)at;
-                a.count[1] = (uint32_t)INT32_MIN;
+                a.count[1] = __float_as_uint(largest);
                 a.count[2] = 0;
             }
         }
@@ -168,6 +202,7 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
             at = -1;
     } else {
         at = real ? a.where[r] : (int32_t)a.count[0];
+        largest = __uint_as_float(a.count[1]);
     }
     if (real) {
         if (at < 0) {
@@ -191,10 +226,23 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
             return;
     }
     u32x4_t* out = reinterpret_cast<u32x4_t*>(a.h + to * a.ldh);
+    u32x4_t* scaled = a.hs ? reinterpret_cast<u32x4_t*>(a.hs + to * a.ldh) : nullptr;
+    const int e = scaled && real ? share_of(weight_of(a.c, r), largest).exponent : 0;
+    const auto put = [&](uint32_t i, const u32x4_t& v) {
+        out[i] = v;
+        if (!scaled)
+            return;
+        float f[8];
+        T::unpack(v, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f[k] = ldexpf(f[k], e);
+        scaled[i] = e ? T::pack(f) : v;
+    };
     if (threadIdx.x < chunks)
-        out[threadIdx.x] = first;
+        put(threadIdx.x, first);
     for (uint32_t i = threadIdx.x + 256; i < chunks; i += 256)
-        out[i] = chunk(i);
+        put(i, chunk(i));
 }
 
 // ---- tiles ------------------------------------------------------------------
@@ -365,23 +413,12 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
         a.c.lse[r] = (float)lse;
     a.m[n] = ref;
     a.ls[n] = (float)(ln * kLog2e64);
-    double fa = w * scale * (1.0 + 2.0 * (double)a.c.z * lse), fb = w * scale;
-    if constexpr (__is_same(T, ElemF16)) {
-        const double most = fmax(fabs(fa), fabs(fb));
-        int e = most > 0.0 && most < 1e38 ? ilogb(most) : 0;
-        e = e < -100 ? -100 : e > 100 ? 100 : e;
-        fa = ldexp(fa, kHalfShift - e);
-        fb = ldexp(fb, kHalfShift - e);
-        a.e[n] = e;
-        a.fs[n] = ldexpf(1.0f, e - kHalfShift);
-        // Of integers, in any order; where it would change nothing, not at all (1331
-        // rows at one address took 16 us).
-        int* largest = reinterpret_cast<int*>(a.count + 1);
-        if (e > __hip_atomic_load(largest, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-            atomicMax(largest, e);
-    }
-    a.fa[n] = (float)fa;
-    a.fb[n] = (float)fb;
+    const float largest = __uint_as_float(a.count[1]);
+    const Share share = share_of(weight, largest);
+    const float up = __is_same(T, ElemF16) ? kHalfScale : 1.0f;
+    a.fb[n] = share.mantissa * up;
+    a.fa[n] = (float)((double)(share.mantissa * up) * (1.0 + 2.0 * (double)a.c.z * lse));
+    a.fs[n] = ldexpf((float)((double)largest * scale / up), share.exponent);
     return w * ((double)a.c.z * lse * lse - logp);
 }
 
@@ -615,25 +652,6 @@ __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
 
 // ---- gradients --------------------------------------------------------------
 
-// Half precision: the hidden rows times 2^(e - the largest e).
-__global__ __launch_bounds__(256) void lce_scale_kernel(Lce a)
-{
-    const uint32_t n = blockIdx.x, rows = a.count[0];
-    if (n >= round_up32(rows, kRowPad))
-        return;
-    const float f = n < rows ? ldexpf(1.0f, a.e[n] - (int)a.count[1]) : 0.0f;
-    const u32x4_t* from = reinterpret_cast<const u32x4_t*>(a.h + n * a.ldh);
-    u32x4_t* to = reinterpret_cast<u32x4_t*>(a.hs + n * a.ldh);
-    for (uint32_t i = threadIdx.x; i < a.ldh / 16; i += 256) {
-        float v[8];
-        ElemF16::unpack(from[i], v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] *= f;
-        to[i] = ElemF16::pack(v);
-    }
-}
-
 // d from the kept products: eight columns a thread.
 template <class T>
 __global__ __launch_bounds__(kBlock) void lce_kept_kernel(Lce a, uint32_t blocks)
@@ -761,8 +779,7 @@ __global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t t
     for (uint32_t k = 1; k < a.splits; ++k)
         v += p[k * split];
     const uint32_t n = lane % 32;
-    if constexpr (__is_same(T, ElemF16))
-        v *= n0 + n < rows ? a.fs[n0 + n] : 0.0f;
+    v *= n0 + n < rows ? a.fs[n0 + n] : 0.0f;
     uint64_t packed = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
@@ -788,11 +805,12 @@ __global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t fir
     const TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
     const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
     const uint32_t left = (uint32_t)a.c.V - first;
-    const Operand H = {__is_same(T, ElemF16) ? a.hs : a.h, a.ldh, (uint32_t)(a.ldh / 2), rows};
+    const Operand H = {a.hs, a.ldh, (uint32_t)(a.ldh / 2), rows};
     const Operand d = {a.d, (size_t)a.piece * 2, a.piece, rows};
     TileAcc<S> acc;
     multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
-    const float f = __is_same(T, ElemF16) && rows ? ldexpf(1.0f, (int)a.count[1] - kHalfShift) : 1.0f;
+    const float f = (float)((double)__uint_as_float(a.count[1]) * (double)a.c.scale /
+                            (__is_same(T, ElemF16) ? (double)kHalfScale : 1.0));
     store_tile<T, true>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
                   [&](uint32_t n) -> uint16_t* {
                       return n0 + n < left ? static_cast<uint16_t*>(a.c.dweight) +
@@ -893,11 +911,10 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     w.take(o.target, 4 * n);
     for (float** f : {&o.w, &o.zt, &o.m, &o.ls, &o.fa, &o.fb, &o.fs})
         w.take(*f, 4 * n);
-    w.take(o.e, 4 * n);
     w.take(o.loss_part, 8 * n / kJoinWaves + 8);
     w.take(o.h, o.ldh * n);
     o.hs = nullptr;
-    if (t == LogitType::F16 && c.dweight)
+    if (c.dweight)
         w.take(o.hs, o.ldh * n);
     o.tiles_v = p.tiles_v;
     w.take(o.stat, sizeof(float2) * p.tiles_v * c.rows);
@@ -922,10 +939,10 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
     const LcePlan p = plan_of(t, c, dev, &a);
     const dim3 gather((unsigned)c.rows + kRowPad);
     if (c.rows <= kRowsAlone) {
-        hipLaunchKernelGGL(lce_gather_kernel<true>, gather, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((lce_gather_kernel<T, true>), gather, dim3(256), 0, s, a);
     } else {
         hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
-        hipLaunchKernelGGL(lce_gather_kernel<false>, gather, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((lce_gather_kernel<T, false>), gather, dim3(256), 0, s, a);
     }
     const auto stat = [&](auto keep) {
         constexpr bool KEEP = decltype(keep)::value;
@@ -960,8 +977,6 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
                        dim3(kJoinThreads), 0, s, a);
     if (!c.dhidden && !c.dweight)
         return hipGetLastError();
-    if (a.hs)
-        hipLaunchKernelGGL(lce_scale_kernel, dim3((unsigned)p.rows), dim3(256), 0, s, a);
     for (size_t first = 0; first < c.V; first += p.piece) {
         const uint32_t f = (uint32_t)first;
         if (p.keep) {

@@ -555,7 +555,7 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
                            red_stream_t stream);
 
 /* Cross entropy of hidden rows (rows x D) against an output layer weight
- * (V x D) and targets, without logits in memory:
+ * (V x D) and targets, in pieces of the vocabulary:
  *   z_v = scale hidden[r] . weight[v],  lse = ln sum_v exp z_v,
  *   loss = sum_r row_weight[r] (lse - z_target + z_coef lse^2).
  * row_weight: one factor per row (NULL: 1 / rows each).  A row of weight 0, or
@@ -563,13 +563,15 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
  * and its hidden values are not looked at.  logp takes z_target - lse, lse the
  * log-sum-exp (NULL: not wanted).  dhidden and dweight (NULL: not wanted) take
  * the gradients, of the inputs' type; every element of their rows is written.
- * accum != 0 adds to the old loss.
+ * accum != 0 adds to the old loss.  No output may lie over an input.
  *
- * Products are of the 16-bit values, summed in fp32.  The gradient of each
- * logit is rounded to the inputs' type before it is multiplied by weight or
- * hidden rows: an error of half a step, 2^-9 (bf16) or 2^-12 (f16) of each term
- * in relative terms.  The logits are computed once for the loss and again, a
- * piece of the vocabulary at a time, for the gradients.
+ * Products are of the 16-bit values, summed in fp32; subnormal values count.
+ * A logit's gradient over its row's weight (up to a power of two) is rounded
+ * to the inputs' type before it is multiplied by weight or hidden rows: half a
+ * step of each term, 2^-8 (bf16) or 2^-11 (f16) of it at most, and in f16 at
+ * least 2^-29 of the row's weight.  In f16 1 + 2 z_coef lse must stay below
+ * 2000 in magnitude (gradients overflow otherwise).  A row with a NaN or an
+ * infinity has a NaN loss, and NaN in dhidden's row; dweight sums over rows.
  *
  * D a multiple of 8 and at most 65536; the rows of weight aligned to 16 bytes
  * (RED_ERR_ALIGN, or RED_ERR_INVALID where ldw is no multiple of 8);
@@ -578,9 +580,12 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
  * workspace: device memory of the caller's, aligned to 256 bytes, whose needed
  * size red_linear_ce_workspace_* gives (on the device of the call; dhidden,
  * dweight: whether they are wanted).  It holds nothing between calls; calls
- * that share one must be ordered.  RED_ERR_SCRATCH where it is too small.  Its
- * size is about rows D 2 bytes, 8 rows V / 128 or less, and for gradients up to
- * 256 MiB (more past 65536 rows) and rows D 4. */
+ * that share one must be ordered.  RED_ERR_SCRATCH where it is too small.  It
+ * takes the hidden rows once or, for dweight, twice, 8 bytes a row for each 128
+ * or 256 columns, for gradients a piece of their logits' gradients (256 MiB or
+ * 2048 columns), the logits themselves in fp32 where they are one piece and at
+ * most 512 MiB (larger ones are computed a second time), and for dhidden its
+ * fp32 sums. */
 int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
                       const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
                       const float* row_weight, float scale, float z_coef, float* loss, int accum,

@@ -142,10 +142,13 @@ def linear_ce(hidden, weight, targets, row_weight, scale, zc):
     16 at a time, so (D / 16 + 16) u bounds what they do (one rounding a block,
     and 16 within).  ez is that of a row's worst logit.  A term's exponent adds
     (|x| + 2) u, the row's sum V / tiles terms in fp32: 128 / 2 of a lane and 8
-    joins, then fp64; so ln S is off by scale ez + stat.  d is rounded to the
-    inputs' type before it is multiplied (half a step of each term, and of the
-    smallest number of f16, 2^-25 of 2^8 of the row's factors), and the sums over V and
-    over rows are fp32: (V / 16 + 16) u, and as much for rows."""
+    joins, then fp64; so ln S is off by scale ez + stat.  d over its weight is rounded
+    to the inputs' type before it is multiplied (half a step of each term; in f16,
+    where it is 16 times larger, at least half of the smallest step, 2^-25 / 16 of the
+    weight), and the sums over V and over rows are fp32: (V / 16 + 16) u, and as much
+    for rows.  For dW the hidden rows carry their weights' exponents: exact, but for
+    f16's smallest step, half of which is 2^-25 of up to twice the largest weight over
+    the row's."""
     dtype = hidden.dtype
     rows, D = hidden.shape
     V = weight.shape[0]
@@ -183,15 +186,13 @@ def linear_ce(hidden, weight, targets, row_weight, scale, zc):
     d = torch.where(live.unsqueeze(1), d, 0.0)
     d = d.scatter_add(1, y.unsqueeze(1), -b.unsqueeze(1))
     ed = ed + U * (a.abs() * p + d.abs()) * 4
-    most = torch.maximum(a.abs().squeeze(1), b.abs())
-    small = 2.0 ** -25 * 2.0 ** -8 * 2 * most.unsqueeze(1) if dtype == torch.float16 else 0.0
+    most = b.abs()
+    small = 2.0 ** -25 / 16 * most.unsqueeze(1) if dtype == torch.float16 else 0.0
     ed = torch.where(live.unsqueeze(1), ed + half_step(dtype) * (d.abs() + ed) + small, 0.0)
     dh = d @ W
     edh = ed @ W.abs() + (V / 16 + 24) * U * (d.abs() @ W.abs())
     dw = d.t() @ h
-    hs = h.abs()
     if dtype == torch.float16:  # the scaled copy of the hidden rows: its smallest steps
-        hs = hs + 2.0 ** -25 * 2 * (most.max() / most.clamp_min(1e-300)).unsqueeze(1).clamp_max(2.0 ** 60)
         lost = 2.0 ** -25 * 2 * most.max() * (d.abs() / most.clamp_min(1e-300).unsqueeze(1)).sum(0)
     edw = ed.t() @ h.abs() + (rows / 16 + 24) * U * (d.abs().t() @ h.abs())
     if dtype == torch.float16:
