@@ -94,6 +94,7 @@ struct TileOperand {
     static constexpr int kLoads = kBytes / 1024 / WAVES;
     static_assert(kLoads >= 1 && kLoads * WAVES * 1024 == kBytes, "whole loads for every wave");
     static constexpr int kChunks = ROW ? K / 8 : R / 8; // of a row, or of a step of k
+    static_assert(ROW || kChunks % 16 == 0, "the permutation stays in the step of k");
 
     uint32_t offset[kLoads], k_of[kLoads]; // of this lane's chunk: bytes from `at`, step of k
     uint64_t at;
