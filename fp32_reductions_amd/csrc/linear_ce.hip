@@ -41,6 +41,8 @@ constexpr double kLog2e64 = 1.4426950408889634074;
 constexpr float kHalfScale = 16.0f; // of d in half precision
 
 typedef TileShape<256, 256, 2, 4, 64, 2> BigTile;
+typedef TileShape<256, 128, 2, 4, 64, 2> HalfTile;   // the last big tiles, cut along n
+typedef TileShape<256, 64, 4, 2, 64, 2> QuarterTile;
 typedef TileShape<128, 128, 2, 2, 32, 4> MidTile;
 typedef TileShape<128, 128, 2, 2, 32, 2> MidWeight;
 typedef TileShape<128, 32, 4, 1, 128, 3> FewTile;
@@ -68,7 +70,7 @@ struct Lce {
     char* d;           // rows x piece
     uint32_t piece;
     float* dh;         // splits x padded rows x padded width, in tile order
-    uint32_t splits;
+    uint32_t splits, cus;
 };
 
 __device__ __forceinline__ uint32_t round_up32(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
@@ -247,24 +249,69 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
 
 // ---- tiles ------------------------------------------------------------------
 
-// The tile of workgroup `id`: each XCD takes a run of the order, in which 8
-// tiles along m go with every tile along n, so that what one XCD's compute units
-// read at a time is few operand rows, from its own L2.
+// Workgroup `id` of `total`: each XCD takes a run of the order of tiles ...
+__device__ __forceinline__ uint32_t in_order(uint32_t id, uint32_t total)
+{
+    const uint32_t x = id % kXcds, i = id / kXcds, per = total / kXcds, rest = total % kXcds;
+    return x * per + (x < rest ? x : rest) + i;
+}
+// ... in which 8 tiles along m go with every tile along n, so that what one XCD's
+// compute units read at a time is few operand rows, from its own L2.
 struct TileAt {
     uint32_t m, n;
 };
-__device__ __forceinline__ TileAt tile_at(uint32_t id, uint32_t tiles_m, uint32_t tiles_n)
+__device__ __forceinline__ TileAt tile_at(uint32_t o, uint32_t tiles_m, uint32_t tiles_n)
 {
-    const uint32_t total = tiles_m * tiles_n, x = id % kXcds, i = id / kXcds;
-    const uint32_t per = total / kXcds, rest = total % kXcds;
-    const uint32_t o = x * per + (x < rest ? x : rest) + i;
     const uint32_t group = o / (8 * tiles_n), in = o % (8 * tiles_n);
     const uint32_t left = tiles_m - group * 8, height = left < 8 ? left : 8;
     return {group * 8 + in % height, in / height};
 }
 
+// The work of workgroup `id`: f(shape, tile along m, first row n).  Big tiles come a
+// compute unit each, so those of the last round, if they are at most half as many as
+// the units, are cut in two or four (PARTS) along n and given to as many.  (921 rows
+// against 50001 x 2048, 784 tiles on 256 units: 232 us whole, 216 cut; 600 rows with
+// their gradient, 1265 and 1242.)
+template <class S, uint32_t PARTS = 4, class F>
+__device__ __forceinline__ void with_tile(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t cus,
+                                          F f)
+{
+    const uint32_t total = tiles_m * tiles_n;
+    if constexpr (__is_same(S, BigTile)) {
+        const uint32_t rest = total % cus, whole = total - rest;
+        const uint32_t parts = PARTS == 4 && rest * 4 <= cus ? 4 : rest * 2 <= cus ? 2 : 1;
+        if (id >= whole) {
+            const uint32_t k = id - whole;
+            if (k >= rest * parts)
+                return;
+            const TileAt t = tile_at(whole + k / parts, tiles_m, tiles_n);
+            const uint32_t n0 = t.n * S::N + k % parts * (S::N / parts);
+            if (parts == 1)
+                f(S(), t.m, n0);
+            else if (parts == 2)
+                f(HalfTile(), t.m, n0);
+            else if constexpr (PARTS == 4)
+                f(QuarterTile(), t.m, n0);
+            return;
+        }
+        const TileAt t = tile_at(in_order(id, whole), tiles_m, tiles_n);
+        f(S(), t.m, t.n * S::N);
+    } else {
+        if (id >= total)
+            return;
+        const TileAt t = tile_at(in_order(id, total), tiles_m, tiles_n);
+        f(S(), t.m, t.n * S::N);
+    }
+}
+// Workgroups enough for that, whatever the rows that count leave of tiles_n.
 template <class S>
-__device__ __forceinline__ uint32_t lds_of(char (&lds)[S::kLds])
+uint32_t workgroups(uint32_t tiles_m, uint32_t tiles_n, uint32_t cus)
+{
+    const uint32_t total = tiles_m * tiles_n;
+    return total + (__is_same(S, BigTile) ? std::min(cus, total * 3) : 0);
+}
+
+__device__ __forceinline__ uint32_t lds_of(char* lds)
 {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 }
@@ -279,21 +326,17 @@ __device__ __forceinline__ uint32_t turn_of(uint32_t tile)
 
 // ---- forward ------------------------------------------------------------------
 
+// Tile number t along the vocabulary, rows n0 on.
 template <class T, class S, bool KEEP>
-__global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t first,
-                                                               uint32_t tiles_m, uint32_t tiles_n)
+__device__ __forceinline__ void stat_tile(const Lce& a, char* buffer, uint32_t t, uint32_t n0)
 {
-    __shared__ __align__(1024) char buffer[S::kLds];
-    const uint32_t lds = lds_of<S>(buffer);
-    TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
-    t.m += first;
-    const uint32_t v0 = t.m * S::M, n0 = t.n * S::N, rows = a.count[0];
+    const uint32_t lds = lds_of(buffer), v0 = t * S::M, rows = a.count[0];
     if (n0 >= rows)
         return;
     const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
     const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
     TileAcc<S> acc;
-    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(t.m));
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(t));
 
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0; // columns of this tile
@@ -365,8 +408,20 @@ __global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t f
             const float2 p = part[k * S::N + n];
             s += p.y * __builtin_amdgcn_exp2f((p.x - ref) * c);
         }
-        a.stat[(size_t)(n0 + n) * a.tiles_v + t.m] = make_float2(m, s);
+        a.stat[(size_t)(n0 + n) * a.tiles_v + t] = make_float2(m, s);
     }
+}
+
+__device__ __forceinline__ uint32_t live_tiles(const Lce& a, uint32_t n) { return (a.count[0] + n - 1) / n; }
+
+// `tiles` tiles along the vocabulary, from number `first` on.
+template <class T, class S, bool KEEP>
+__global__ __launch_bounds__(S::kThreads) void lce_stat_kernel(Lce a, uint32_t first, uint32_t tiles)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    with_tile<S>(blockIdx.x, tiles, live_tiles(a, S::N), a.cus, [&](auto shape, uint32_t m, uint32_t n0) {
+        stat_tile<T, decltype(shape), KEEP>(a, buffer, first + m, n0);
+    });
 }
 
 // One wave a row: its tiles' sums, its loss and the factors of its gradient.  The
@@ -676,19 +731,16 @@ __global__ __launch_bounds__(kBlock) void lce_kept_kernel(Lce a, uint32_t blocks
 
 // d of the piece that starts at column `first`, rows of a.piece elements.
 template <class T, class S>
-__global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t first, uint32_t tiles_n)
+__device__ __forceinline__ void d_tile(const Lce& a, char* buffer, uint32_t first, uint32_t m0,
+                                       uint32_t n0)
 {
-    __shared__ __align__(1024) char buffer[S::kLds];
-    const uint32_t lds = lds_of<S>(buffer);
-    const uint32_t rows = a.count[0];
-    const TileAt t = tile_at(blockIdx.x, a.piece / S::M, tiles_n);
-    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N, v0 = first + m0;
+    const uint32_t lds = lds_of(buffer), rows = a.count[0], v0 = first + m0;
     if (n0 >= rows || v0 >= (uint32_t)a.c.V)
         return;
     const Operand W = {static_cast<const char*>(a.c.weight), a.c.ldw * 2, (uint32_t)a.c.V, (uint32_t)a.c.D};
     const Operand H = {a.h, a.ldh, rows, (uint32_t)a.c.D};
     TileAcc<S> acc;
-    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(t.m));
+    multiply<T, S, true, true>(acc, W, H, v0, n0, 0, (uint32_t)a.c.D, lds, turn_of<S>(m0 / S::M));
 
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0;
@@ -714,18 +766,27 @@ __global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t firs
     });
 }
 
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_d_kernel(Lce a, uint32_t first, uint32_t tiles)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    with_tile<S>(blockIdx.x, tiles, live_tiles(a, S::N), a.cus, [&](auto shape, uint32_t m, uint32_t n0) {
+        d_tile<T, decltype(shape)>(a, buffer, first, m * S::M, n0);
+    });
+}
+
 // dh [+]= d W over the steps of k of split blockIdx.y.
 template <class T, class S>
 __global__ __launch_bounds__(S::kThreads) void lce_dh_kernel(Lce a, uint32_t first, uint32_t tiles_m,
                                                              uint32_t tiles_n)
 {
     __shared__ __align__(1024) char buffer[S::kLds];
-    const uint32_t lds = lds_of<S>(buffer);
-    const uint32_t rows = a.count[0];
-    const TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
-    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
-    if (n0 >= rows)
+    const uint32_t lds = lds_of(buffer);
+    const uint32_t rows = a.count[0], live = live_tiles(a, S::N);
+    if (blockIdx.x >= tiles_m * live)
         return;
+    const TileAt t = tile_at(in_order(blockIdx.x, tiles_m * live), tiles_m, live);
+    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
     const uint32_t left = (uint32_t)a.c.V - first, k = left < a.piece ? left : a.piece;
     const uint32_t stages = (k + S::K - 1) / S::K;
     const uint32_t per = (stages + a.splits - 1) / a.splits * S::K;
@@ -796,15 +857,13 @@ __global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t t
 
 // The piece's rows of dW.
 template <class T, class S>
-__global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t first, uint32_t tiles_m,
-                                                             uint32_t tiles_n)
+__device__ __forceinline__ void dw_tile(const Lce& a, char* buffer, uint32_t first, uint32_t m0,
+                                        uint32_t n0)
 {
-    __shared__ __align__(1024) char buffer[S::kLds];
-    const uint32_t lds = lds_of<S>(buffer);
-    const uint32_t rows = a.count[0];
-    const TileAt t = tile_at(blockIdx.x, tiles_m, tiles_n);
-    const uint32_t m0 = t.m * S::M, n0 = t.n * S::N;
+    const uint32_t lds = lds_of(buffer), rows = a.count[0];
     const uint32_t left = (uint32_t)a.c.V - first;
+    if (n0 >= left)
+        return;
     const Operand H = {a.hs, a.ldh, (uint32_t)(a.ldh / 2), rows};
     const Operand d = {a.d, (size_t)a.piece * 2, a.piece, rows};
     TileAcc<S> acc;
@@ -817,6 +876,17 @@ __global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t fir
                                                  (size_t)(first + n0 + n) * a.c.lddw + m0
                                            : nullptr;
                   });
+}
+
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t first, uint32_t tiles_m,
+                                                             uint32_t tiles_n)
+{
+    __shared__ __align__(1024) char buffer[S::kLds];
+    // In halves at most: the tile's rows of d need 128 columns.
+    with_tile<S, 2>(blockIdx.x, tiles_m, tiles_n, a.cus, [&](auto shape, uint32_t m, uint32_t n0) {
+        dw_tile<T, decltype(shape)>(a, buffer, first, m * S::M, n0);
+    });
 }
 
 // ---- plan -------------------------------------------------------------------
@@ -920,6 +990,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     w.take(o.stat, sizeof(float2) * p.tiles_v * c.rows);
     o.piece = (uint32_t)p.piece;
     o.splits = (uint32_t)p.splits;
+    o.cus = (uint32_t)dev.cus;
     p.keep = grad && p.piece >= c.V && 4 * p.piece * c.rows <= kKeptBytes &&
              (p.stream || c.D >= kKeptWidth);
     if (p.keep)
@@ -963,8 +1034,9 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
             const uint32_t most = std::max(8u, kTilesPerLaunch / p.tiles_n);
             for (uint32_t first = 0; first < p.tiles_v; first += most) {
                 const uint32_t tiles_m = std::min(most, p.tiles_v - first);
-                hipLaunchKernelGGL((lce_stat_kernel<T, S, KEEP>), dim3(tiles_m * p.tiles_n),
-                                   dim3(S::kThreads), 0, s, a, first, tiles_m, p.tiles_n);
+                hipLaunchKernelGGL((lce_stat_kernel<T, S, KEEP>),
+                                   dim3(workgroups<S>(tiles_m, p.tiles_n, a.cus)), dim3(S::kThreads),
+                                   0, s, a, first, tiles_m);
             }
             return 0;
         });
@@ -988,8 +1060,9 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
             typedef decltype(shape) S;
             const uint32_t tiles_m = (uint32_t)p.piece / S::M;
             if (!p.keep)
-                hipLaunchKernelGGL((lce_d_kernel<T, S>), dim3(tiles_m * p.tiles_n), dim3(S::kThreads),
-                                   0, s, a, f, p.tiles_n);
+                hipLaunchKernelGGL((lce_d_kernel<T, S>),
+                                   dim3(workgroups<S>(tiles_m, p.tiles_n, a.cus)), dim3(S::kThreads),
+                                   0, s, a, f, tiles_m);
             if (c.dhidden)
                 hipLaunchKernelGGL((lce_dh_kernel<T, S>),
                                    dim3(p.tiles_d * p.tiles_n, (unsigned)p.splits),
@@ -1002,8 +1075,9 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
                 typedef decltype(shape) S;
                 const uint32_t tiles_m = (uint32_t)((c.D + S::M - 1) / S::M);
                 const uint32_t tiles_n = (cols + S::N - 1) / S::N;
-                hipLaunchKernelGGL((lce_dw_kernel<T, S>), dim3(tiles_m * tiles_n),
-                                   dim3(S::kThreads), 0, s, a, f, tiles_m, tiles_n);
+                hipLaunchKernelGGL((lce_dw_kernel<T, S>),
+                                   dim3(workgroups<S>(tiles_m, tiles_n, a.cus)), dim3(S::kThreads), 0,
+                                   s, a, f, tiles_m, tiles_n);
             };
             if (p.kind_w == Kind::Mid)
                 dw(MidWeight());
