@@ -521,13 +521,14 @@ __global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
 // The layer is only read, so what counts is the rate of its reading: each wave
 // takes 16 of its rows from end to end, straight into the operand registers of
 // v_mfma_f32_16x16x32 (lane l: row l % 16, 16 bytes at 64 s + 16 (l / 16) in step s),
-// with kAhead steps, 512 bytes of each row, in flight twice over; the hidden rows
+// with kAhead steps, 128 bytes of each row, in flight twice over (8 steps instead of
+// 2: 190.8 us instead of 185.7 for 8 rows against 131072 x 4096); the hidden rows
 // stay in LDS (16 bytes of padding a row spread 16 rows over the banks).  Waves start
 // at different places of their rows: in step they ask the same few memory channels
-// at a time (1 row against 32768 x 4096: 55 us in step, 49 so; tiles through LDS
+// at a time (1 row against 32768 x 4096: 55 us in step, 48 so; tiles through LDS
 // took 59).  Where there are fewer blocks of 16 rows than waves, the waves of a
 // workgroup share a block's steps and their sums meet in LDS, in order.
-constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 8;
+constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 2;
 constexpr uint32_t kTurn = 2 * kAhead * 32; // steps of k
 constexpr size_t kStreamLds = 156 * 1024;
 constexpr size_t kStreamRowsMax = 64;

@@ -112,6 +112,19 @@ def test_loss_and_gradients(red, monkeypatch, shape, t, cus):
 
 
 @pytest.mark.parametrize("t", HALF)
+@pytest.mark.parametrize("cus", [8, 9, 10, 12, 13, 16, 17, 18, 21])
+@pytest.mark.parametrize("masked", [0, 200])
+def test_last_round_of_tiles(red, monkeypatch, cus, t, masked):
+    """3 x 6 tiles (2 x 6 of rows that count) on so many units that a last round is
+    whole, half or a quarter full, or empty, or the only one."""
+    say("last round on %d, %d masked %s" % (cus, masked, t))
+    monkeypatch.setenv("RED_TEST_CUS", str(cus))
+    h, W, y, w = draw(601, 1400, 136, t, cus)
+    y[:masked] = -1
+    check(run(red, h, W, y, w, t, 0.5, 0.01, odd=True), ref.linear_ce(h, W, y, w, 0.5, 0.01))
+
+
+@pytest.mark.parametrize("t", HALF)
 def test_without_weights(red, t):
     h, W, y, _ = draw(77, 500, 96, t, 3, weighted=False)
     check(run(red, h, W, y, None, t), ref.linear_ce(h, W, y, None, 1.0, 0.0))
