@@ -526,17 +526,19 @@ __global__ __launch_bounds__(kJoinThreads) void lce_join_kernel(Lce a)
 // stay in LDS (16 bytes of padding a row spread 16 rows over the banks).  Waves start
 // at different places of their rows: in step they ask the same few memory channels
 // at a time (1 row against 32768 x 4096: 55 us in step, 48 so; tiles through LDS
-// took 59).  Where there are fewer blocks of 16 rows than waves, the waves of a
-// workgroup share a block's steps and their sums meet in LDS, in order.
+// took 59).  The blocks that a workgroup's waves would not all have one of are shared,
+// a part of k to each wave, whose sums meet in LDS, in order, where that is shorter.
 constexpr int kStreamWaves = 8, kStreamThreads = kStreamWaves * kWave, kAhead = 2;
 constexpr uint32_t kTurn = 2 * kAhead * 32; // steps of k
 constexpr size_t kStreamLds = 156 * 1024;
-constexpr size_t kStreamRowsMax = 64;
+// More rows take tiles, whose hidden rows need not be in LDS first (32 rows against 32768 x
+// 2048: 40.5 us streamed, 35.8 in tiles; 16 rows against 131072 x 2048: 103 and 106).
+constexpr size_t kStreamRowsMax = 16;
 
 // LDS for `rows` hidden rows of ldh bytes, and for the waves' sums.
 constexpr size_t stream_lds(size_t rows, size_t ldh)
 {
-    return rows * (ldh + 16) + (rows + 15) / 16 * kStreamWaves * kWave * sizeof(f32x4_t);
+    return rows * (ldh + 16) + kStreamWaves * kWave * sizeof(f32x4_t);
 }
 
 template <class T>
@@ -552,39 +554,52 @@ __device__ __forceinline__ f32x4_t mfma16(const s16x8_t& a, const s16x8_t& b, co
 
 __device__ const u32x4_t kNothing = {0, 0, 0, 0};
 
-// Columns [0, V) of the layer for G groups of 16 hidden rows, a run of blocks of 16
-// columns to each workgroup.  f takes the products of a block: lane l has, in acc[g],
-// those of hidden row 16 g + l % 16 (past the call's last row, of that one) with columns
-// v .. v + 3, v = the block's first + 4 (l / 16).
-template <class T, int G, class F>
+// Columns [0, V) of the layer, a run of blocks of 16 columns to each workgroup.  f
+// takes the products of a block: lane l has those of hidden row l % 16 (past the call's
+// last row, of that one) with columns v .. v + 3, v = the block's first + 4 (l / 16).
+template <class T, class F>
 __device__ __forceinline__ void stream_layer(const Lce& a, char* lds, F f)
 {
     const uint32_t lane = threadIdx.x % kWave, part = lane / 16, wave = threadIdx.x / kWave;
     const uint32_t V = (uint32_t)a.c.V, D = (uint32_t)a.c.D, turns = (D + kTurn - 1) / kTurn;
     const uint32_t blocks = (V + 15) / 16, per = (blocks + gridDim.x - 1) / gridDim.x;
-    const uint32_t first = blockIdx.x * per, last = first + per < blocks ? first + per : blocks;
-    const bool share = per < (uint32_t)kStreamWaves; // the waves share each block
-    // This wave's blocks, and its turns along k: the first one, how many, how far apart.
-    const uint32_t step = share ? 1 : kStreamWaves, apart = share ? kStreamWaves : 1;
-    const uint32_t from = share ? wave : (blockIdx.x * kStreamWaves + wave) * 5 % turns;
-    const uint32_t count = share ? (turns + kStreamWaves - 1 - wave) / kStreamWaves : turns;
-    // The lane's row of block b; past the last column that one again.
-    const auto row_of = [&](uint32_t b) {
-        const uint32_t v = b * 16 + lane % 16;
-        return reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
-                                                (size_t)(v < V ? v : V - 1) * a.c.ldw * 2) +
-               part;
+    const uint32_t first = blockIdx.x * per < blocks ? blockIdx.x * per : blocks;
+    const uint32_t own = first + per < blocks ? per : blocks - first;
+    // Rounds in which every wave has a block, and then the rest: a block after the other
+    // by all waves, or one more round.
+    const uint32_t whole = own / kStreamWaves, rest = own % kStreamWaves;
+    const bool share = rest * ((turns + kStreamWaves - 1) / kStreamWaves) < turns;
+    const uint32_t rounds = whole + (share ? rest : wave < rest);
+    const uint32_t turned = (blockIdx.x * kStreamWaves + wave) * 5 % turns;
+    // A round: its block, the lane's row of that (past the last column that one again),
+    // and this wave's turns along k: the first one, how many, how far apart.
+    struct Round {
+        uint32_t block, from, count, apart;
+        const u32x4_t* row;
+    };
+    const auto round = [&](uint32_t i) {
+        const bool shared = share && i >= whole;
+        Round r;
+        r.block = first + (shared ? whole * kStreamWaves + i - whole : i * kStreamWaves + wave);
+        r.from = shared ? wave : turned;
+        r.count = shared ? (turns + kStreamWaves - 1 - wave) / kStreamWaves : turns;
+        r.apart = shared ? kStreamWaves : 1;
+        const uint32_t v = r.block * 16 + lane % 16;
+        r.row = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.c.weight) +
+                                                 (size_t)(v < V ? v : V - 1) * a.c.ldw * 2) +
+                part;
+        return r;
     };
     u32x4_t w[2][kAhead];
-    const auto request = [&](const u32x4_t* p, uint32_t s, u32x4_t (&to)[kAhead]) {
+    const auto request = [&](const u32x4_t* p, uint32_t turn, uint32_t half, u32x4_t (&to)[kAhead]) {
+        const uint32_t s = (turn * 2 + half) * kAhead;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             to[i] = *((s + i) * 32 + part * 8 < D ? p + (s + i) * 4 : &kNothing);
     };
-    uint32_t b = first + (share ? 0 : wave);
-    const u32x4_t* p = row_of(b < last ? b : 0);
-    if (b < last && count)
-        request(p, from * (2 * kAhead), w[0]);
+    Round now = round(0);
+    if (rounds)
+        request(now.row, now.from, 0, w[0]);
     // The hidden rows, zeros behind those that count.
     const uint32_t stride = (uint32_t)a.ldh + 16, chunks = (uint32_t)(a.ldh / 16);
     const uint32_t held = (uint32_t)a.c.rows, rows = a.count[0];
@@ -593,116 +608,88 @@ __device__ __forceinline__ void stream_layer(const Lce& a, char* lds, F f)
         *reinterpret_cast<u32x4_t*>(lds + i / chunks * stride + i % chunks * 16) =
             *(i / chunks < rows ? reinterpret_cast<const u32x4_t*>(a.h + i / chunks * a.ldh) + i % chunks
                                 : &kNothing);
-    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds + held * stride); // waves x G x lanes
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds + held * stride); // waves x lanes
     __syncthreads();
-    const char* mine[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const uint32_t n = lane % 16 + g * 16;
-        mine[g] = lds + (n < held ? n : held - 1) * stride + part * 16;
-    }
-    f32x4_t acc[G];
-    const auto multiply = [&](uint32_t s, const u32x4_t (&from)[kAhead]) {
+    const char* mine = lds + (lane % 16 < held ? lane % 16 : held - 1) * stride + part * 16;
+    f32x4_t acc;
+    const auto multiply = [&](uint32_t turn, uint32_t half, const u32x4_t (&from)[kAhead]) {
+        const uint32_t s = (turn * 2 + half) * kAhead;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if ((s + i) * 32 < D)
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    acc[g] = mfma16<T>(
-                        __builtin_bit_cast(s16x8_t, from[i]),
-                        *reinterpret_cast<const s16x8_t*>(mine[g] + (s + i) * 64), acc[g]);
+                acc = mfma16<T>(__builtin_bit_cast(s16x8_t, from[i]),
+                                *reinterpret_cast<const s16x8_t*>(mine + (s + i) * 64), acc);
     };
-    for (; b < last; b += step) {
-        const u32x4_t* next = row_of(b + step < last ? b + step : b);
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            acc[g] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t turn = from;
-        for (uint32_t k = 0; k < count; ++k) {
-            const uint32_t s = turn * (2 * kAhead);
-            turn += apart;
-            if (!share && turn == turns)
-                turn = 0;
-            const bool more = k + 1 < count;
-            request(p, s + kAhead, w[1]);
-            multiply(s, w[0]);
-            request(more ? p : next, (more ? turn : from) * (2 * kAhead), w[0]);
-            multiply(s + kAhead, w[1]);
+    for (uint32_t i = 0; i < rounds; ++i) {
+        const Round next = round(i + 1 < rounds ? i + 1 : i);
+        acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t turn = now.from;
+        for (uint32_t k = 0; k < now.count; ++k) {
+            const bool more = k + 1 < now.count;
+            const uint32_t after = turn + now.apart < turns ? turn + now.apart : 0;
+            request(now.row, turn, 1, w[1]);
+            multiply(turn, 0, w[0]);
+            request(more ? now.row : next.row, more ? after : next.from, 0, w[0]);
+            multiply(turn, 1, w[1]);
+            turn = after;
         }
-        p = next;
-        if (share) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                sums[(wave * G + g) * kWave + lane] = acc[g];
+        if (share && i >= whole) {
+            sums[wave * kWave + lane] = acc;
             __syncthreads();
             if (wave == 0) {
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int x = 1; x < kStreamWaves; ++x)
-                        acc[g] += sums[(x * G + g) * kWave + lane];
-                f(acc, b * 16 + part * 4);
+                for (int x = 1; x < kStreamWaves; ++x)
+                    acc += sums[x * kWave + lane];
+                f(acc, now.block * 16 + part * 4);
             }
             __syncthreads();
         } else {
-            f(acc, b * 16 + part * 4);
+            f(acc, now.block * 16 + part * 4);
         }
+        now = next;
     }
 }
 
-template <class T, int G, bool KEEP>
+template <class T, bool KEEP>
 __global__ __launch_bounds__(kStreamThreads) void lce_stream_stat_kernel(Lce a)
 {
     extern __shared__ __align__(16) char buffer[];
-    const uint32_t n0 = threadIdx.x % 16, rows = a.count[0], V = (uint32_t)a.c.V;
+    const uint32_t n = threadIdx.x % 16, rows = a.count[0], V = (uint32_t)a.c.V;
     const float c = a.c.scale * kLog2ef;
-    uint32_t target[G];
-    float m[G], s[G];
+    const uint32_t target = n < rows ? (uint32_t)a.target[n] : ~0u;
+    float m = -INFINITY, s = 0.0f;
+    stream_layer<T>(a, buffer, [&](const f32x4_t& z, uint32_t v) {
+        if (KEEP && n < rows && v < V)
+            *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v) = z;
+        float most = m;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        target[g] = n0 + g * 16 < rows ? (uint32_t)a.target[n0 + g * 16] : ~0u;
-        m[g] = -INFINITY;
-        s[g] = 0.0f;
-    }
-    stream_layer<T, G>(a, buffer, [&](const f32x4_t (&z)[G], uint32_t v) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const uint32_t n = n0 + g * 16;
-            if (KEEP && n < rows && v < V)
-                *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v) = z[g];
-            float most = m[g];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                most = fmaxf(most, v + e < V ? z[g][e] : -INFINITY);
-                if (v + e == target[g])
-                    a.zt[n] = z[g][e];
-            }
-            const float ref = most == -INFINITY ? 0.0f : most;
-            s[g] *= __builtin_amdgcn_exp2f((m[g] - ref) * c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[g] += v + e < V ? __builtin_amdgcn_exp2f((z[g][e] - ref) * c) : 0.0f;
-            m[g] = most;
+        for (int e = 0; e < 4; ++e) {
+            most = fmaxf(most, v + e < V ? z[e] : -INFINITY);
+            if (v + e == target)
+                a.zt[n] = z[e];
         }
+        const float ref = most == -INFINITY ? 0.0f : most;
+        s *= __builtin_amdgcn_exp2f((m - ref) * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            s += v + e < V ? __builtin_amdgcn_exp2f((z[e] - ref) * c) : 0.0f;
+        m = most;
     });
     // The workgroup's lanes that have the same row, in order (the sums' LDS).
     constexpr int kParts = kStreamThreads / 16;
     float2* part = reinterpret_cast<float2*>(buffer + a.c.rows * (a.ldh + 16));
-    static_assert(kParts * 16 * sizeof(float2) <= kStreamWaves * kWave * sizeof(f32x4_t), "a group's");
+    static_assert(kParts * 16 * sizeof(float2) <= kStreamWaves * kWave * sizeof(f32x4_t), "they fit");
     __syncthreads();
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-        part[threadIdx.x / 16 * (G * 16) + g * 16 + n0] = make_float2(m[g], s[g]);
+    part[threadIdx.x] = make_float2(m, s);
     __syncthreads();
-    const uint32_t n = threadIdx.x;
-    if (n >= G * 16 || n >= rows)
+    if (threadIdx.x >= 16 || n >= rows)
         return;
     float most = -INFINITY, sum = 0.0f;
     for (int k = 0; k < kParts; ++k)
-        most = fmaxf(most, part[k * (G * 16) + n].x);
+        most = fmaxf(most, part[k * 16 + n].x);
     const float ref = most == -INFINITY ? 0.0f : most;
     for (int k = 0; k < kParts; ++k)
-        sum += part[k * (G * 16) + n].y * __builtin_amdgcn_exp2f((part[k * (G * 16) + n].x - ref) * c);
+        sum += part[k * 16 + n].y * __builtin_amdgcn_exp2f((part[k * 16 + n].x - ref) * c);
     a.stat[(size_t)n * a.tiles_v + blockIdx.x] = make_float2(most, sum);
 }
 
@@ -901,17 +888,26 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
 // Where the vocabulary is one piece and its products (fp32) take no more than this,
 // they are kept from the first pass for the gradients: writing and reading them costs
-// less than the layer's rows again, unless those are short.
-constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640;
+// less than the layer's rows again, unless those are short and the rows many.  (1040
+// rows against 50001: width 512, 348 us kept and 336 not, 640 399 and 405, 1024 509 and
+// 553; 32 rows, width 512, 64 and 73.)
+constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640, kKeptRows = 128;
 
-// Rows up to which lce_gather_kernel goes alone.
-constexpr size_t kRowsAlone = 2048;
+// Rows up to which lce_gather_kernel goes alone (1024: 18.6 us a call so, 20.2
+// otherwise; 2048: 23.7 and 22.4).
+constexpr size_t kRowsAlone = 1024;
 
 enum class Kind { Few, Mid, Big };
 
-// Tiles by the work: 32 rows by 128 columns where there are few rows, whose
-// product only reads the layer; 256 x 256, the fastest, where there are enough of
-// them to give every compute unit one; 128 x 128 in between.
+// Tiles by the work: 32 rows by 128 columns where there are few rows, whose product
+// only reads the layer, or so little of both that larger tiles leave most compute units
+// without one; 256 x 256, the fastest, where every compute unit gets one; 128 x 128 in
+// between.  Bf16, both gradients wanted, us with the rule's tile and with its neighbour's:
+//   48 x 50001 x 1024        101 (128 x 128)    112 (32 x 128)
+//   300 x 4000 x 2048        67.5 (128 x 128)   73.5 (32 x 128)
+//   100 x 8000 x 1024        47.7 (32 x 128)    51.5 (128 x 128)
+//   600 x 12000 x 1024       104 (128 x 128)    119 (256 x 256)
+//   600 x 30000 x 1024       211 (256 x 256)    218 (128 x 128)
 struct LcePlan {
     Kind kind, kind_w; // of the products over rows; of the layer's gradient
     uint32_t tiles_v, tiles_n, tiles_d;
@@ -954,9 +950,10 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     o.ldh = round_up(c.D, kWidthPad) * 2;
     p.stream_lds = stream_lds(c.rows, o.ldh);
     p.stream = c.rows <= kStreamRowsMax && p.stream_lds <= kStreamLds;
-    p.kind = c.rows <= 32                             ? Kind::Few
-             : c.rows > 128 && big >= (size_t)dev.cus ? Kind::Big
-                                                      : Kind::Mid;
+    const size_t mid = round_up(c.V, 128) / 128 * (round_up(c.rows, 128) / 128);
+    p.kind = c.rows <= 32 || 4 * mid <= (size_t)dev.cus ? Kind::Few
+             : c.rows > 128 && big >= (size_t)dev.cus   ? Kind::Big
+                                                        : Kind::Mid;
     size_t tile = 0; // elements
     with_shape(p.kind, [&](auto s) {
         p.tiles_v = (uint32_t)((c.V + s.M - 1) / s.M);
@@ -993,7 +990,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     o.splits = (uint32_t)p.splits;
     o.cus = (uint32_t)dev.cus;
     p.keep = grad && p.piece >= c.V && 4 * p.piece * c.rows <= kKeptBytes &&
-             (p.stream || c.D >= kKeptWidth);
+             (c.rows <= kKeptRows || c.D >= kKeptWidth);
     if (p.keep)
         w.take(o.z, 4 * p.piece * c.rows);
     if (grad)
@@ -1019,16 +1016,9 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
     const auto stat = [&](auto keep) {
         constexpr bool KEEP = decltype(keep)::value;
         if (p.stream) {
-            const auto go = [&](auto groups) {
-                hipLaunchKernelGGL((lce_stream_stat_kernel<T, decltype(groups)::value, KEEP>),
-                                   dim3(p.tiles_v), dim3(kStreamThreads), p.stream_lds, s, a);
-            };
-            switch ((c.rows + 15) / 16) {
-            case 1: return go(std::integral_constant<int, 1>());
-            case 2: return go(std::integral_constant<int, 2>());
-            case 3: return go(std::integral_constant<int, 3>());
-            default: return go(std::integral_constant<int, 4>());
-            }
+            hipLaunchKernelGGL((lce_stream_stat_kernel<T, KEEP>), dim3(p.tiles_v),
+                               dim3(kStreamThreads), p.stream_lds, s, a);
+            return;
         }
         with_shape(p.kind, [&](auto shape) {
             typedef decltype(shape) S;
