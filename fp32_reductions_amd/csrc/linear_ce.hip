@@ -341,19 +341,33 @@ __device__ __forceinline__ void stat_tile(const Lce& a, char* buffer, uint32_t t
     const float c = a.c.scale * kLog2ef;
     const uint32_t left = (uint32_t)a.c.V - v0; // columns of this tile
     if constexpr (KEEP) {
+        // Each wave turns its 32 x 32 blocks in LDS of its own, so that a store writes whole
+        // lines of 8 rows, not 32 bytes of 32 (1531 rows against 65537 x 1000: 781 us, 795).
+        typedef __attribute__((address_space(3))) f32x4_t* ptr;
+        constexpr uint32_t kRow = 32 * 4 + 16; // bytes
+        static_assert(S::WM * S::N * 8 + S::kWaves * 32 * kRow <= S::kLds, "behind `part`");
+        const uint32_t mine = lds + S::WM * S::N * 8 + threadIdx.x / kWave * (32 * kRow);
+        const uint32_t lane = threadIdx.x % kWave;
 #pragma unroll
-        for (int j = 0; j < S::NS; ++j) {
-            const uint32_t n = n0 + acc.n(j);
-            if (n < rows)
+        for (int j = 0; j < S::NS; ++j)
 #pragma unroll
-                for (int i = 0; i < S::MS; ++i)
+            for (int i = 0; i < S::MS; ++i) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        if (acc.m(i, e) < left) // a.piece is a multiple of 4
-                            *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v0 + acc.m(i, e)) =
-                                f32x4_t{acc.c[i][j][e], acc.c[i][j][e + 1], acc.c[i][j][e + 2],
-                                        acc.c[i][j][e + 3]};
-        }
+                for (int e = 0; e < 16; e += 4)
+                    *(ptr)(uintptr_t)(mine + lane % 32 * kRow + (e / 4 * 8 + lane / 32 * 4) * 4) =
+                        f32x4_t{acc.c[i][j][e], acc.c[i][j][e + 1], acc.c[i][j][e + 2],
+                                acc.c[i][j][e + 3]};
+                __builtin_amdgcn_wave_barrier(); // LDS keeps a wave's order
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t r = k * 8 + lane / 8, n = n0 + acc.wave_n() + j * 32 + r;
+                    const uint32_t m = acc.wave_m() + i * 32 + lane % 8 * 4;
+                    const f32x4_t v = *(ptr)(uintptr_t)(mine + r * kRow + lane % 8 * 16);
+                    if (n < rows && m < left) // a.piece is a multiple of 4
+                        *reinterpret_cast<f32x4_t*>(a.z + (size_t)n * a.piece + v0 + m) = v;
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
     }
     float2* part = reinterpret_cast<float2*>(buffer); // [WM][N]
 #pragma unroll
@@ -704,7 +718,9 @@ __global__ __launch_bounds__(kBlock) void lce_kept_kernel(Lce a, uint32_t blocks
     if (n >= a.count[0] || v >= V)
         return;
     const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.z + (size_t)n * a.piece + v);
-    const f32x4_t z[2] = {p[0], p[1]}; // past V anything
+    // Read once; past V anything.  (1531 rows against 65537 x 1000: 804 us a
+    // call so, 831 otherwise.)
+    const f32x4_t z[2] = {__builtin_nontemporal_load(p), __builtin_nontemporal_load(p + 1)};
     const float c = a.c.scale * kLog2ef, m = a.m[n], ls = a.ls[n], fa = a.fa[n], fb = a.fb[n];
     const uint32_t target = (uint32_t)a.target[n];
     float d[8];
