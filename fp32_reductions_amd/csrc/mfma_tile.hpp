@@ -16,6 +16,12 @@
 //
 // Elements outside an operand are zeros: their lanes load from past the end of
 // the buffer descriptor, which gives zeros, so nothing outside is read.
+// What bounds it: 256 x 256 tiles of 64 steps keep the matrix cores busy in 66 % of the
+// cycles, at a clock that the power limit sets (3584 rows against 131072 x 4096, with the
+// rows' sums of exponentials: 3.06 ms, 1.26 PFLOP/s; the library's product of 4096 rows
+// alone, 1.44).  8 waves of 128 x 64 with two buffers: 13.0 ms for that loss with its
+// gradients; 4 waves of 128 x 128 14.7; steps of 32 in 3 to 5 buffers 13.4; tiles of 256 x 128
+// 16.5, 128 x 128 15.9.
 #pragma once
 
 #include <hip/hip_runtime.h>
