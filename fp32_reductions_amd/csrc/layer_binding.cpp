@@ -251,8 +251,8 @@ const char kLinearDoc[] =
     "($self, hidden, weight, targets, loss, logp=None, lse=None, dhidden=None, dweight=None, "
     "row_weight=None, scale=1.0, z_coef=0.0, accum=False, workspace=None, stream=None)\n--\n\n"
     "loss[0] = [loss[0] +] sum_r row_weight[r] (-logp[r] + z_coef lse[r]^2),\n"
-    "the cross entropy of softmax(scale * hidden @ weight.T) without logits in\n"
-    "memory: hidden (rows, D), weight (V, D), targets (rows) int64.  logp and\n"
+    "the cross entropy of softmax(scale * hidden @ weight.T) without a matrix\n"
+    "of logits: hidden (rows, D), weight (V, D), targets (rows) int64.  logp and\n"
     "lse (fp32) take the rows' values, dhidden and dweight the gradients.\n"
     "row_weight: 1 / rows each when None; rows of weight 0, or without a target\n"
     "in [0, V), do not count.  D a multiple of 8, weight's rows 16-byte aligned.\n"

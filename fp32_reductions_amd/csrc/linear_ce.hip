@@ -1,5 +1,5 @@
-// linear_ce.hip -- the cross entropy of hidden rows against an output layer,
-// without keeping the logits, and its gradients.
+// linear_ce.hip -- the cross entropy of hidden rows against an output layer and its
+// gradients, with no logits of the caller's.
 //
 //     z = s h W^T,  lse = ln sum_v exp z_v,  row loss = lse - z_t + c lse^2
 //     d_v = w s ((1 + 2 c lse) p_v - [v = t]),  dh = d W,  dW = d^T h
@@ -7,12 +7,13 @@
 // The products run on the matrix cores (mfma_tile.hpp).  Forward, a workgroup's
 // tile of logits stays in its registers and leaves one maximum and one sum of
 // exponentials for each of its rows, which a second kernel joins.  The
-// gradients need the whole row's sum before the first of them, so the logits are
-// computed a second time, a piece of the vocabulary at a time: the piece's d,
-// rounded to the inputs' type, goes to the workspace (it is an operand of both
-// further products), dh gathers d W over the pieces in fp32, and the piece's
-// rows of dW are finished at once.  So 8 rows V D operations where keeping the
-// logits would take 6, and a workspace that does not grow with V.
+// gradients need the whole row's sum before the first of them.  So the products are
+// kept, in fp32, where the vocabulary is one piece and they take little room; otherwise
+// they are computed a second time, a piece of the vocabulary at a time: 8 rows V D
+// operations where keeping them takes 6, and a workspace that does not grow with V.
+// The piece's d, rounded to the inputs' type, goes to the workspace (it is an operand of
+// both further products), dh gathers d W over the pieces in fp32, and the piece's rows of
+// dW are finished at once.
 //
 // Rows that do not count are left out first: the others' hidden rows are copied
 // together (rows D elements, nothing beside rows V D), which also keeps a NaN in
@@ -833,7 +834,8 @@ __global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t t
 {
     constexpr uint32_t kRow = 32 + 8; // elements of a row in LDS
     __shared__ __align__(16) uint16_t lds[32 * kRow];
-    const uint32_t rows = a.count[0], n0 = (first + blockIdx.x / blocks_m) * 32, m0 = blockIdx.x % blocks_m * 32;
+    const uint32_t rows = a.count[0];
+    const uint32_t n0 = (first + blockIdx.x / blocks_m) * 32, m0 = blockIdx.x % blocks_m * 32;
     if (n0 >= rows)
         return;
     const uint32_t in_m = m0 % S::M, in_n = n0 % S::N;
