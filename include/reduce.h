@@ -28,8 +28,8 @@
  *   4. The operators around the output layer whose logits those are: the
  *      root-mean-square norm of its rows with the residual's addition and an
  *      8-bit output, the balance loss of a router of experts, and the cross
- *      entropy of hidden rows against the layer without keeping the logits,
- *      each with its gradient.
+ *      entropy of hidden rows against the layer, with no logits of the
+ *      caller's, each with its gradient.
  *
  * Conventions shared by every entry point:
  *
@@ -583,8 +583,9 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
  * that share one must be ordered.  RED_ERR_SCRATCH where it is too small.  It
  * takes the hidden rows once or, for dweight, twice, 8 bytes a row for each 128
  * or 256 columns, for gradients a piece of their logits' gradients (256 MiB or
- * 2048 columns), the logits themselves in fp32 where they are one piece and at
- * most 512 MiB (larger ones are computed a second time), and for dhidden its
+ * 2048 columns), the logits themselves in fp32 where they are one piece, at most
+ * 512 MiB and, for more than 128 rows, D at least 640 (others are computed a
+ * second time), and for dhidden its
  * fp32 sums. */
 int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
                       const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
