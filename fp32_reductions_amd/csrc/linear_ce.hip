@@ -22,9 +22,13 @@
 // What is rounded is d without its row's weight: d / (w s) times the mantissa of w over
 // the largest weight, so that where all weights are equal the target's element, the
 // largest, of a row that is unsure of it is -1, exactly.  The weights' exponents and the
-// largest go where they are exact: dh takes them behind its product, in fp32; for dW,
-// whose sum runs over rows, a copy of the hidden rows has the exponents.  In half
-// precision d is 2^4 times larger, which keeps probabilities down to 4e-6 normal
+// largest come back later: dh takes them behind its product, in fp32, exactly; for dW,
+// whose sum runs over rows, a copy of the hidden rows has the exponents, exactly but for
+// values below the type's normal range.  Half precision has no room there, so its rows
+// are put in order of groups of 4 exponents: the copy has what is left within a group
+// (2^-3 at least: values are off by 2^-22 at most), and dW's sum is scaled, in fp32, from
+// one group to the next.  Weights within a factor of 8 are one group.
+// In half precision d is 2^4 times larger, which keeps probabilities down to 4e-6 normal
 // numbers and overflows where 1 + 2 c lse passes 2000.
 //
 // Bf16, us a call: 4096 rows (512 masked) against 131072 x 4096 with both gradients 13200,
@@ -56,12 +60,18 @@ typedef TileShape<128, 32, 4, 1, 128, 3> FewTile;
 // The hidden rows are padded with zeros to multiples of these.
 constexpr uint32_t kRowPad = 64, kWidthPad = 64;
 
+// Exponents of a weight over the largest (share_of), in groups: the first has the largest.
+constexpr int kExponentMin = -100, kGroupExponents = 4;
+constexpr uint32_t kGroups = -kExponentMin / kGroupExponents + 1;
+static_assert(kGroups <= kWave, "a lane for each");
+
 // What the kernels share.  Pointers into the workspace, except those of the call.
 struct Lce {
     LinearCall c;
     // [0]: rows that count; [1]: the largest of their weights' magnitudes (float);
     // [2]: arrivals
     uint32_t* count;
+    uint32_t* group;   // half precision's dW: rows of each group of weights
     int32_t* where;    // of each row of the call: its place among those that count, or -1
     int32_t *row, *target; // of each row that counts: its number, its target
     // Weight, target's product, largest product, log2 of the sum of 2^((z - m) scale log2 e),
@@ -102,53 +112,109 @@ __device__ __forceinline__ Share share_of(float w, float largest)
 {
     const float r = w / largest;
     int e = fabsf(r) > 0.0f && fabsf(r) <= 1.0f ? ilogbf(r) : 0; // 0 where one is no number
-    e = e < -100 ? -100 : e;
+    e = e < kExponentMin ? kExponentMin : e;
     return {ldexpf(r, -e), e};
 }
+template <bool GROUPED>
+__device__ __forceinline__ uint32_t group_of(float w, float largest)
+{
+    return GROUPED ? (uint32_t)-share_of(w, largest).exponent / kGroupExponents : 0;
+}
 
+// The places of the rows that count: in the order of their groups, and of the call
+// within one.  One workgroup.
+template <bool GROUPED>
 __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
 {
-    __shared__ uint32_t lds[1024 / kWave];
-    __shared__ float lds_w[1024 / kWave];
+    constexpr uint32_t kThreads = 1024, kAll = kThreads / kWave, kOf = GROUPED ? kGroups : 1;
+    // Each wave's rows of each group and the groups' next places, twice: a turn's are read
+    // while the next one's are written.
+    __shared__ uint32_t lds[2][kAll][kOf], lds_first[2][kOf + 1];
+    __shared__ float lds_w[kAll];
     float largest = 0.0f;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    uint32_t before = 0;
-    for (size_t first = 0; first < a.c.rows; first += 1024) {
+    const auto share_largest = [&] {
+        largest = wave_reduce<OpMax>(largest);
+        if (lane == 0)
+            lds_w[wave] = largest;
+        __syncthreads();
+        for (uint32_t k = 0; k < kAll; ++k)
+            largest = fmaxf(largest, lds_w[k]);
+    };
+    if (threadIdx.x <= kOf)
+        lds_first[0][threadIdx.x] = 0;
+    if constexpr (GROUPED) {
+        for (size_t r = threadIdx.x; r < a.c.rows; r += kThreads)
+            if (counted(a.c, r))
+                largest = fmaxf(largest, fabsf(weight_of(a.c, r)));
+        share_largest();
+        // Each group's rows, at the place of the one before it: then their sums.
+        for (size_t r = threadIdx.x; r < a.c.rows; r += kThreads)
+            if (counted(a.c, r))
+                atomicAdd(&lds_first[0][group_of<true>(weight_of(a.c, r), largest) + 1], 1u);
+        __syncthreads();
+        if (threadIdx.x < kOf)
+            a.group[threadIdx.x] = lds_first[0][threadIdx.x + 1];
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (uint32_t g = 1; g < kOf; ++g)
+                lds_first[0][g] += lds_first[0][g - 1];
+    }
+    uint32_t turn = 0;
+    for (size_t first = 0; first < a.c.rows; first += kThreads, turn ^= 1) {
         const size_t r = first + threadIdx.x;
         const bool counts = r < a.c.rows && counted(a.c, r);
-        const uint64_t all = __ballot(counts);
-        if (lane == 0)
-            lds[wave] = __popcll(all);
-        __syncthreads();
-        uint32_t at = before, total = 0;
-        for (uint32_t k = 0; k < 1024 / kWave; ++k) {
-            at += k < wave ? lds[k] : 0;
-            total += lds[k];
+        const float w = counts ? weight_of(a.c, r) : 0.0f;
+        const uint32_t g = counts ? group_of<GROUPED>(w, largest) : 0;
+        if (lane < kOf)
+            lds[turn][wave][lane] = 0;
+        __builtin_amdgcn_wave_barrier(); // LDS keeps a wave's order
+        uint32_t before = 0; // rows of the group in this wave before this one
+        for (uint64_t left = __ballot(counts); left;) {
+            const uint32_t of = __builtin_amdgcn_readlane(g, __builtin_ctzll(left));
+            const uint64_t same = __ballot(counts && g == of);
+            if (g == of)
+                before = __popcll(same & ((1ull << lane) - 1));
+            if (lane == 0)
+                lds[turn][wave][of] = __popcll(same);
+            left &= ~same;
         }
-        at += __popcll(all & ((1ull << lane) - 1));
+        __syncthreads();
+        uint32_t at = lds_first[turn][g] + before;
+#pragma unroll
+        for (uint32_t k = 0; k < kAll; ++k)
+            at += k < wave ? lds[turn][k][g] : 0;
         if (r < a.c.rows)
             a.where[r] = counts ? (int32_t)at : -1;
         if (counts) {
             a.row[at] = (int32_t)r;
             a.target[at] = (int32_t)a.c.targets[r];
-            a.w[at] = weight_of(a.c, r);
-            largest = fmaxf(largest, fabsf(weight_of(a.c, r)));
+            a.w[at] = w;
+            if (!GROUPED)
+                largest = fmaxf(largest, fabsf(w));
         }
-        before += total;
-        __syncthreads();
+        if (threadIdx.x < kOf) {
+            uint32_t next = lds_first[turn][threadIdx.x];
+#pragma unroll
+            for (uint32_t k = 0; k < kAll; ++k)
+                next += lds[turn][k][threadIdx.x];
+            lds_first[turn ^ 1][threadIdx.x] = next;
+        }
     }
-    largest = wave_reduce<OpMax>(largest);
-    if (lane == 0)
-        lds_w[wave] = largest;
-    __syncthreads();
+    if constexpr (GROUPED)
+        __syncthreads();
+    else
+        share_largest();
     if (threadIdx.x == 0) {
-        for (int k = 0; k < 1024 / kWave; ++k)
-            largest = fmaxf(largest, lds_w[k]);
-        a.count[0] = before;
+        a.count[0] = lds_first[turn][kOf - 1];
         a.count[1] = __float_as_uint(largest);
         a.count[2] = 0;
     }
 }
+
+// Rows up to which lce_gather_kernel goes alone (1024: 18.6 us a call so, 20.2
+// otherwise; 2048: 23.7 and 22.4).
+constexpr size_t kRowsAlone = 1024;
 
 // One workgroup a row of the call, and kRowPad more for the zeros after the last
 // row that counts.  ALONE: there has been no lce_rows_kernel; with few rows each
@@ -174,26 +240,43 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
     uint32_t to;
     int32_t at;
     float largest = 0.0f;
+    constexpr bool kMayGroup = __is_same(T, ElemF16);
+    const bool grouped = kMayGroup && a.hs;
+    const auto of_group = [&](float w) { return grouped ? group_of<kMayGroup>(w, largest) : 0; };
     if constexpr (ALONE) {
-        __shared__ uint32_t lds[kWaves];
+        __shared__ uint32_t lds[kWaves], lds_group[kGroups];
         __shared__ float lds_w[kWaves];
-        uint32_t n = 0;
-#pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < a.c.rows; i += 256)
-            if (counted(a.c, i)) {
-                n += i < r;
-                largest = fmaxf(largest, fabsf(weight_of(a.c, i)));
-            }
-        const bool counts = real && counted(a.c, r);
-        n = (uint32_t)wave_sum64((double)n);
-        largest = wave_reduce<OpMax>(largest);
-        if (threadIdx.x % kWave == 0) {
-            lds[threadIdx.x / kWave] = n;
-            lds_w[threadIdx.x / kWave] = largest;
+        constexpr uint32_t kHeld = (uint32_t)kRowsAlone / 256;
+        float w[kHeld]; // of rows that count; 0: they do not
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k) {
+            const uint32_t i = threadIdx.x + k * 256;
+            w[k] = i < a.c.rows && counted(a.c, i) ? weight_of(a.c, i) : 0.0f;
+            largest = fmaxf(largest, fabsf(w[k]));
         }
+        const bool counts = real && counted(a.c, r);
+        largest = wave_reduce<OpMax>(largest);
+        if (threadIdx.x % kWave == 0)
+            lds_w[threadIdx.x / kWave] = largest;
+        if (kMayGroup && threadIdx.x < kGroups)
+            lds_group[threadIdx.x] = 0;
+        __syncthreads();
+        largest = fmaxf(fmaxf(lds_w[0], lds_w[1]), fmaxf(lds_w[2], lds_w[3]));
+        const uint32_t mine = !real ? kGroups : counts ? of_group(weight_of(a.c, r)) : 0;
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kHeld; ++k)
+            if (w[k] != 0.0f) {
+                const uint32_t i = threadIdx.x + k * 256, g = of_group(w[k]);
+                n += g < mine || (g == mine && i < r);
+                if (!real && grouped)
+                    atomicAdd(&lds_group[g], 1u);
+            }
+        n = (uint32_t)wave_sum64((double)n);
+        if (threadIdx.x % kWave == 0)
+            lds[threadIdx.x / kWave] = n;
         __syncthreads();
         at = (int32_t)(lds[0] + lds[1] + lds[2] + lds[3]);
-        largest = fmaxf(fmaxf(lds_w[0], lds_w[1]), fmaxf(lds_w[2], lds_w[3]));
         if (threadIdx.x == 0) {
             if (counts) {
                 a.row[at] = (int32_t)r;
@@ -206,6 +289,8 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
                 a.count[2] = 0;
             }
         }
+        if (grouped && r == a.c.rows && threadIdx.x < kGroups)
+            a.group[threadIdx.x] = lds_group[threadIdx.x];
         if (real && !counts)
             at = -1;
     } else {
@@ -235,7 +320,12 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
     }
     u32x4_t* out = reinterpret_cast<u32x4_t*>(a.h + to * a.ldh);
     u32x4_t* scaled = a.hs ? reinterpret_cast<u32x4_t*>(a.hs + to * a.ldh) : nullptr;
-    const int e = scaled && real ? share_of(weight_of(a.c, r), largest).exponent : 0;
+    // The exponent of its weight, or what its group leaves of that.
+    int e = 0;
+    if (scaled && real) {
+        const float w = weight_of(a.c, r);
+        e = share_of(w, largest).exponent + (int)of_group(w) * kGroupExponents;
+    }
     const auto put = [&](uint32_t i, const u32x4_t& v) {
         out[i] = v;
         if (!scaled)
@@ -878,7 +968,24 @@ __device__ __forceinline__ void dw_tile(const Lce& a, char* buffer, uint32_t fir
     const Operand H = {a.hs, a.ldh, (uint32_t)(a.ldh / 2), rows};
     const Operand d = {a.d, (size_t)a.piece * 2, a.piece, rows};
     TileAcc<S> acc;
-    multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
+    if constexpr (__is_same(T, ElemF16)) {
+        // The groups of rows, from that of the smallest weights on.
+        const uint32_t lane = threadIdx.x % kWave, size = lane < kGroups ? a.group[lane] : 0;
+        uint32_t end = rows, last = 0;
+        acc.clear();
+        for (uint64_t left_groups = __ballot(size != 0); left_groups;) {
+            const uint32_t g = 63 - __builtin_clzll(left_groups);
+            const uint32_t begin = end - __builtin_amdgcn_readlane(size, g);
+            if (end != rows)
+                acc.scale(ldexpf(1.0f, -(int)(last - g) * kGroupExponents));
+            multiply<T, S, false, false, true>(acc, H, d, m0, n0, begin, end, lds);
+            end = begin;
+            last = g;
+            left_groups &= ~(1ull << g);
+        }
+    } else {
+        multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
+    }
     const float f = (float)((double)__uint_as_float(a.count[1]) * (double)a.c.scale /
                             (__is_same(T, ElemF16) ? (double)kHalfScale : 1.0));
     store_tile<T, true>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
@@ -915,10 +1022,6 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 // rows against 50001: width 512, 348 us kept and 336 not, 640 399 and 405, 1024 509 and
 // 553; 32 rows, width 512, 64 and 73.)
 constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640, kKeptRows = 128;
-
-// Rows up to which lce_gather_kernel goes alone (1024: 18.6 us a call so, 20.2
-// otherwise; 2048: 23.7 and 22.4).
-constexpr size_t kRowsAlone = 1024;
 
 enum class Kind { Few, Mid, Big };
 
@@ -997,6 +1100,7 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     o.c = c;
     const size_t n = p.rows;
     w.take(o.count, 12);
+    w.take(o.group, 4 * kGroups);
     w.take(o.where, 4 * n);
     w.take(o.row, 4 * n);
     w.take(o.target, 4 * n);
@@ -1033,7 +1137,10 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
     if (c.rows <= kRowsAlone) {
         hipLaunchKernelGGL((lce_gather_kernel<T, true>), gather, dim3(256), 0, s, a);
     } else {
-        hipLaunchKernelGGL(lce_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+        if (std::is_same<T, ElemF16>::value && c.dweight)
+            hipLaunchKernelGGL(lce_rows_kernel<true>, dim3(1), dim3(1024), 0, s, a);
+        else
+            hipLaunchKernelGGL(lce_rows_kernel<false>, dim3(1), dim3(1024), 0, s, a);
         hipLaunchKernelGGL((lce_gather_kernel<T, false>), gather, dim3(256), 0, s, a);
     }
     const auto stat = [&](auto keep) {

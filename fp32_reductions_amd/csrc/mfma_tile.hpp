@@ -107,8 +107,8 @@ struct TileOperand {
     uint64_t advance;
     uint32_t k;
 
-    // first: the tile's first row; begin, end: its steps of k (begin a multiple
-    // of 8).
+    // first: the tile's first row; begin, end: its steps of k (in row form begin is
+    // a multiple of 8).
     __device__ __forceinline__ TileOperand(const Operand& o, uint32_t first, uint32_t begin,
                                            uint32_t end)
     {
@@ -206,12 +206,33 @@ struct TileAcc {
         return wave_m() + i * 32 + (e / 4) * 8 + threadIdx.x % kWave / 32 * 4 + e % 4;
     }
     static __device__ __forceinline__ uint32_t n(int j) { return wave_n() + j * 32 + threadIdx.x % 32; }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    c[i][j][e] = 0.0f;
+    }
+    __device__ __forceinline__ void scale(float f)
+    {
+#pragma unroll
+        for (int i = 0; i < S::MS; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NS; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    c[i][j][e] *= f;
+    }
 };
 
 // The tile at (m0, n0) over steps [begin, end) of k, in the order of the stages from
 // number `turn` on and round.  (Workgroups that read rows of the same length from
 // memory in step ask the same few channels at a time; different turns spread them.)
-template <class T, class S, bool AROW, bool BROW>
+// MORE: added to what acc holds.
+template <class T, class S, bool AROW, bool BROW, bool MORE = false>
 __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, const Operand& b,
                                          uint32_t m0, uint32_t n0, uint32_t begin, uint32_t end,
                                          uint32_t lds, uint32_t turn = 0)
@@ -221,13 +242,8 @@ __device__ __forceinline__ void multiply(TileAcc<S>& acc, const Operand& a, cons
     const A ta(a, m0, begin, end);
     const B tb(b, n0, begin, end);
     const uint32_t stages = (end - begin + S::K - 1) / S::K;
-#pragma unroll
-    for (int i = 0; i < S::MS; ++i)
-#pragma unroll
-        for (int j = 0; j < S::NS; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc.c[i][j][e] = 0.0f;
+    if constexpr (!MORE)
+        acc.clear();
     const uint32_t wm = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_m());
     const uint32_t wn = __builtin_amdgcn_readfirstlane(TileAcc<S>::wave_n());
     constexpr int kSteps = S::K / 16, kLoads = A::kLoads + B::kLoads;
