@@ -68,7 +68,7 @@ static_assert(kGroups <= kWave, "a lane for each");
 // What the kernels share.  Pointers into the workspace, except those of the call.
 struct Lce {
     LinearCall c;
-    // [0]: rows that count; [1]: the largest of their weights' magnitudes (float);
+    // [0]: rows that count; [1]: the largest of their weights' finite magnitudes (float);
     // [2]: arrivals
     uint32_t* count;
     uint32_t* group;   // half precision's dW: rows of each group of weights
@@ -101,6 +101,13 @@ __device__ __forceinline__ bool counted(const LinearCall& c, size_t r)
 {
     const int64_t t = c.targets[r];
     return weight_of(c, r) != 0.0f && t >= 0 && t < (int64_t)c.V;
+}
+
+// What the largest is taken of: no infinity or NaN, which would be every row's factor.
+__device__ __forceinline__ float magnitude(float w)
+{
+    const float m = fabsf(w);
+    return m < INFINITY ? m : 0.0f;
 }
 
 // A weight over the largest: mantissa, 1 to 2 in magnitude, and exponent, 0 or less.
@@ -146,7 +153,7 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
     if constexpr (GROUPED) {
         for (size_t r = threadIdx.x; r < a.c.rows; r += kThreads)
             if (counted(a.c, r))
-                largest = fmaxf(largest, fabsf(weight_of(a.c, r)));
+                largest = fmaxf(largest, magnitude(weight_of(a.c, r)));
         share_largest();
         // Each group's rows, at the place of the one before it: then their sums.
         for (size_t r = threadIdx.x; r < a.c.rows; r += kThreads)
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(1024) void lce_rows_kernel(Lce a)
             a.target[at] = (int32_t)a.c.targets[r];
             a.w[at] = w;
             if (!GROUPED)
-                largest = fmaxf(largest, fabsf(w));
+                largest = fmaxf(largest, magnitude(w));
         }
         if (threadIdx.x < kOf) {
             uint32_t next = lds_first[turn][threadIdx.x];
@@ -252,7 +259,7 @@ __global__ __launch_bounds__(256) void lce_gather_kernel(Lce a)
         for (uint32_t k = 0; k < kHeld; ++k) {
             const uint32_t i = threadIdx.x + k * 256;
             w[k] = i < a.c.rows && counted(a.c, i) ? weight_of(a.c, i) : 0.0f;
-            largest = fmaxf(largest, fabsf(w[k]));
+            largest = fmaxf(largest, magnitude(w[k]));
         }
         const bool counts = real && counted(a.c, r);
         largest = wave_reduce<OpMax>(largest);

@@ -570,12 +570,13 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
  * to the inputs' type before it is multiplied by weight or hidden rows: half a
  * step of each term, 2^-8 (bf16) or 2^-11 (f16) of it at most, and in f16 at
  * least 2^-29 of the row's weight.  For dweight in f16 the hidden values are
- * taken to within 2^-22 where the rows' weights differ, and exactly where they
- * are within a factor of two; a row's part of dweight keeps that accuracy however
- * small its weight is beside others', down to 2^-100 of the largest.  In f16
- * 1 + 2 z_coef lse must stay below
- * 2000 in magnitude (gradients overflow otherwise).  A row with a NaN or an
+ * taken to within 2^-22 where the rows' weights differ in magnitude; a row's part
+ * of dweight keeps that accuracy however small its weight is beside others', down
+ * to 2^-100 of the largest.  In f16 1 + 2 z_coef lse must stay below 2000 in
+ * magnitude (gradients overflow otherwise).  A row with a NaN or an
  * infinity has a NaN loss, and NaN in dhidden's row; dweight sums over rows.
+ * A weight that is NaN or infinite leaves logp and lse as they are and makes the
+ * loss no finite number and dhidden's row NaN.
  *
  * D a multiple of 8 and at most 65536; the rows of weight aligned to 16 bytes
  * (RED_ERR_ALIGN, or RED_ERR_INVALID where ldw is no multiple of 8);

@@ -94,3 +94,25 @@ def test_weights_of_all_sizes_in_any_order(red, rows, masked, t):
         assert (b > 0).all()
         want["dweight"] = v, b
     check(run(red, h, W, y, w, t, zc=0.05), want)
+
+
+@pytest.mark.parametrize("t", HALF)
+@pytest.mark.parametrize("rows", [12, 200, 1500])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_weight_that_is_no_number(red, rows, bad, t):
+    """It makes the loss and its row's gradient no number, and dW, which sums over
+    rows; the other rows' gradients are what they are beside a weight of 0."""
+    h, W, y, w = draw(rows, 700, 64, t, rows)
+    at = rows // 2
+    h[at] = h[0]
+    say("weight %g of %d rows %s" % (bad, rows, t))
+    w[at] = 0.0
+    want = run(red, h, W, y, w, t)
+    w[at], y[at] = bad, 3
+    got = run(red, h, W, y, w, t)
+    keep = torch.arange(rows, device="cuda") != at
+    for k in ("logp", "lse", "dhidden"):
+        assert torch.equal(got[k][keep], want[k][keep]), k
+    assert torch.isfinite(got["logp"][at]) and torch.isfinite(got["lse"][at])
+    assert not torch.isfinite(got["loss"]) and got["dhidden"][at].isnan().all()
+    assert not torch.isfinite(got["dweight"]).any()
