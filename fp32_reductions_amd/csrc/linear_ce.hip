@@ -65,6 +65,13 @@ constexpr int kExponentMin = -100, kGroupExponents = 4;
 constexpr uint32_t kGroups = -kExponentMin / kGroupExponents + 1;
 static_assert(kGroups <= kWave, "a lane for each");
 
+// A number that may be past fp32's range, where a product with it need not be.
+struct Factor {
+    float mantissa;
+    int exponent;
+    __device__ __forceinline__ float times(float v) const { return ldexpf(v * mantissa, exponent); }
+};
+
 // What the kernels share.  Pointers into the workspace, except those of the call.
 struct Lce {
     LinearCall c;
@@ -75,8 +82,9 @@ struct Lce {
     int32_t* where;    // of each row of the call: its place among those that count, or -1
     int32_t *row, *target; // of each row that counts: its number, its target
     // Weight, target's product, largest product, log2 of the sum of 2^((z - m) scale log2 e),
-    // factors of d, factor of dh.
-    float *w, *zt, *m, *ls, *fa, *fb, *fs;
+    // factors of d.
+    float *w, *zt, *m, *ls, *fa, *fb;
+    Factor* fs; // of dh
     double* loss_part; // of each workgroup that joins rows
     char *h, *hs;      // hidden rows, and a copy times 2^(exponent of their weight)
     size_t ldh;        // bytes
@@ -111,16 +119,21 @@ __device__ __forceinline__ float magnitude(float w)
 }
 
 // A weight over the largest: mantissa, 1 to 2 in magnitude, and exponent, 0 or less.
-struct Share {
-    float mantissa;
-    int exponent;
-};
-__device__ __forceinline__ Share share_of(float w, float largest)
+__device__ __forceinline__ Factor share_of(float w, float largest)
 {
     const float r = w / largest;
     int e = fabsf(r) > 0.0f && fabsf(r) <= 1.0f ? ilogbf(r) : 0; // 0 where one is no number
     e = e < kExponentMin ? kExponentMin : e;
     return {ldexpf(r, -e), e};
+}
+// What d is multiplied by behind its products, beside its row's share.
+template <class T>
+__device__ __forceinline__ Factor factor_of(float largest, float scale)
+{
+    constexpr double kUp = __is_same(T, ElemF16) ? kHalfScale : 1.0;
+    int e;
+    const double m = frexp((double)largest * (double)scale / kUp, &e);
+    return {(float)m, e};
 }
 template <bool GROUPED>
 __device__ __forceinline__ uint32_t group_of(float w, float largest)
@@ -586,11 +599,11 @@ __device__ __forceinline__ double join_row(const Lce& a, uint32_t n, uint32_t la
     a.m[n] = ref;
     a.ls[n] = (float)(ln * kLog2e64);
     const float largest = __uint_as_float(a.count[1]);
-    const Share share = share_of(weight, largest);
+    const Factor share = share_of(weight, largest), f = factor_of<T>(largest, a.c.scale);
     const float up = __is_same(T, ElemF16) ? kHalfScale : 1.0f;
     a.fb[n] = share.mantissa * up;
     a.fa[n] = (float)((double)(share.mantissa * up) * (1.0 + 2.0 * (double)a.c.z * lse));
-    a.fs[n] = ldexpf((float)((double)largest * scale / up), share.exponent);
+    a.fs[n] = {f.mantissa, f.exponent + share.exponent};
     return w * ((double)a.c.z * lse * lse - logp);
 }
 
@@ -948,11 +961,11 @@ __global__ __launch_bounds__(kBlock) void lce_dh_finish_kernel(Lce a, uint32_t t
     for (uint32_t k = 1; k < a.splits; ++k)
         v += p[k * split];
     const uint32_t n = lane % 32;
-    v *= n0 + n < rows ? a.fs[n0 + n] : 0.0f;
+    const Factor f = n0 + n < rows ? a.fs[n0 + n] : Factor{0.0f, 0};
     uint64_t packed = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-        packed |= (uint64_t)(uint16_t)T::narrow(v[x]) << (16 * x);
+        packed |= (uint64_t)(uint16_t)T::narrow(f.times(v[x])) << (16 * x);
     *reinterpret_cast<uint64_t*>(lds + n * kRow + q * 8 + lane / 32 * 4) = packed;
     __syncthreads();
     const uint32_t r = threadIdx.x / 4, c = threadIdx.x % 4 * 8; // D is a multiple of 8
@@ -993,14 +1006,14 @@ __device__ __forceinline__ void dw_tile(const Lce& a, char* buffer, uint32_t fir
     } else {
         multiply<T, S, false, false>(acc, H, d, m0, n0, 0, rows, lds);
     }
-    const float f = (float)((double)__uint_as_float(a.count[1]) * (double)a.c.scale /
-                            (__is_same(T, ElemF16) ? (double)kHalfScale : 1.0));
-    store_tile<T, true>(acc, lds, (uint32_t)a.c.D - m0, [&](float v, int, int, int) { return v * f; },
-                  [&](uint32_t n) -> uint16_t* {
-                      return n0 + n < left ? static_cast<uint16_t*>(a.c.dweight) +
-                                                 (size_t)(first + n0 + n) * a.c.lddw + m0
-                                           : nullptr;
-                  });
+    const Factor f = factor_of<T>(__uint_as_float(a.count[1]), a.c.scale);
+    store_tile<T, true>(acc, lds, (uint32_t)a.c.D - m0,
+                        [&](float v, int, int, int) { return f.times(v); },
+                        [&](uint32_t n) -> uint16_t* {
+                            return n0 + n < left ? static_cast<uint16_t*>(a.c.dweight) +
+                                                       (size_t)(first + n0 + n) * a.c.lddw + m0
+                                                 : nullptr;
+                        });
 }
 
 template <class T, class S>
@@ -1111,8 +1124,9 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
     w.take(o.where, 4 * n);
     w.take(o.row, 4 * n);
     w.take(o.target, 4 * n);
-    for (float** f : {&o.w, &o.zt, &o.m, &o.ls, &o.fa, &o.fb, &o.fs})
+    for (float** f : {&o.w, &o.zt, &o.m, &o.ls, &o.fa, &o.fb})
         w.take(*f, 4 * n);
+    w.take(o.fs, sizeof(Factor) * n);
     w.take(o.loss_part, 8 * n / kJoinWaves + 8);
     w.take(o.h, o.ldh * n);
     o.hs = nullptr;

@@ -116,3 +116,19 @@ def test_a_weight_that_is_no_number(red, rows, bad, t):
     assert torch.isfinite(got["logp"][at]) and torch.isfinite(got["lse"][at])
     assert not torch.isfinite(got["loss"]) and got["dhidden"][at].isnan().all()
     assert not torch.isfinite(got["dweight"]).any()
+
+
+@pytest.mark.parametrize("rows", [12, 200])
+@pytest.mark.parametrize("top,scale", [(1e30, 1e10), (1e30, 1e-20), (1e-20, 1e-25), (1e-30, 1e20)])
+def test_weights_and_scales_past_one_another(red, rows, top, scale):
+    """A weight times the scale need not be an fp32 number, where the values that meet
+    it are small or large."""
+    h, W, y, w = draw(rows, 500, 64, "bf16", rows)
+    w = torch.where(w == 0, 0.0, top * 2.0 ** -(torch.arange(rows, device="cuda") % 60).float())
+    size = scale ** -0.5
+    h, W = (h.double() * size).bfloat16(), (W.double() * size).bfloat16()
+    assert h.isfinite().all() and W.isfinite().all()
+    say("weight %g scale %g, %d rows" % (top, scale, rows))
+    want = ref.linear_ce(h, W, y, w, scale, 0.0)
+    assert want["dhidden"][0].abs().max() < 1e37 and want["dweight"][0].abs().max() < 1e37
+    check(run(red, h, W, y, w, "bf16", scale=scale), want)
