@@ -12,10 +12,11 @@
 // an element hide behind the loads); every output is rounded once, and y is
 // computed from the sum before its rounding.
 //
-// The weight's gradient is a sum over rows: each workgroup keeps its columns'
-// sums in fp32 registers over the rows that it takes, a fixed few dozen where
-// rows are many, and a second kernel adds the workgroups' sums in fp64, in
-// order.  No atomics: the result does not depend on timing.
+// The weight's gradient is a sum over rows: each thread keeps its columns' sums in
+// fp32 registers over 64 of its rows at most, and adds those to fp64 sums of its own in
+// LDS where it has more; a second kernel adds the workgroups' sums in fp64, in order.
+// So a column's error does not grow with the rows.  No atomics: the result does not
+// depend on timing.
 //
 // Bf16: 8192 x 8192 with a residual and 8 bits out 71.9 us a call, 6.5 TB/s; 1 x 4096 4.2,
 // of which the host takes 3.3; the gradient of 16384 x 4096 95.2, 89 of them at 6.0 TB/s.
@@ -281,10 +282,17 @@ add_rmsnorm_kernel(NormCall a)
     }
 }
 
+// Rows whose terms a thread adds up in fp32.  (16384 x 4096 bf16 has 32 a thread,
+// 262144 x 4096 512: 1590 us with an fp64 sum behind each 64 of them, 1594 without.)
+constexpr uint32_t kRun = 64;
+// fp64 sums of a thread in LDS and one more, so that neighbours' lie in other banks.
+__host__ __device__ constexpr uint32_t fold_stride(uint32_t sums) { return sums + 1; }
+
 struct GradArgs {
     NormGradCall c;
     float* partial; // a row of D column sums per workgroup; null: no weight gradient
     int last;       // one workgroup: it writes the gradient itself
+    int folds;      // some thread has more than kRun rows
 };
 
 template <class T, int GT, int NV, bool STREAM>
@@ -294,6 +302,12 @@ __global__ __launch_bounds__((most_threads<GT>())) void rmsnorm_grad_kernel(Grad
     typedef typename T::S S;
     const NormGradCall& a = args.c;
     __shared__ double lds_sum[2][kMostWaves];
+    // A thread's column sums: in fp64 over its rows (folds), or in fp32 behind them
+    // where rows share the workgroup.
+    extern __shared__ double lds_fold[];
+    const auto fold = [&](int k, int i) -> double& {
+        return lds_fold[threadIdx.x * fold_stride(NV * W) + k * W + i];
+    };
     const Row<T, GT, NV, STREAM> at((uint32_t)a.D);
     const size_t step = (size_t)gridDim.x * RB;
     // Four vectors a thread leave no registers for the weight between rows, nor for
@@ -303,6 +317,13 @@ __global__ __launch_bounds__((most_threads<GT>())) void rmsnorm_grad_kernel(Grad
     if (!kFull)
         at.load_again(a.weight, w);
     float acc[NV][W] = {};
+    if (args.folds)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                fold(k, i) = 0.0;
+    uint32_t run = 0;
     int turn = 0;
     for (size_t r = (size_t)blockIdx.x * RB + (GT ? threadIdx.x / (GT ? GT : 1) : 0); r < a.rows;
          r += step) {
@@ -350,18 +371,57 @@ __global__ __launch_bounds__((most_threads<GT>())) void rmsnorm_grad_kernel(Grad
             }
             at.store(static_cast<S*>(a.dx) + r * a.lddx, k, d);
         }
+        if (args.folds && ++run == kRun) {
+            run = 0;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    fold(k, i) += (double)acc[k][i];
+                    acc[k][i] = 0.0f;
+                }
+        }
     }
     if (!args.partial)
         return;
+    float* out = args.last ? a.dweight : args.partial + (size_t)blockIdx.x * a.D;
+    const auto put = [&](int k, int i, double sum) {
+        const uint32_t j = (k * at.threads + at.t) * W + i;
+        if (j < a.D)
+            out[j] = (float)((args.last && a.accum ? (double)out[j] : 0.0) + sum);
+    };
     // Rows that share a workgroup: their sums meet in its first row's threads.
-    if constexpr (RB > 1) {
-        __shared__ float lds_acc[RB][GT * NV * W];
-        const uint32_t g = threadIdx.x / GT;
+    const uint32_t g = GT ? threadIdx.x / (GT ? GT : 1) : 0;
+    if (args.folds) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                lds_acc[g][(k * W + i) * GT + at.t] = acc[k][i];
+                fold(k, i) += (double)acc[k][i];
+        if constexpr (RB > 1) {
+            __syncthreads();
+            if (g > 0)
+                return;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                double sum = fold(k, i);
+#pragma unroll
+                for (int b = 1; b < RB; ++b)
+                    sum += lds_fold[(b * GT + at.t) * fold_stride(NV * W) + k * W + i];
+                put(k, i, sum);
+            }
+        return;
+    }
+    if constexpr (RB > 1) {
+        float* lds_acc = reinterpret_cast<float*>(lds_fold);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                lds_acc[(k * W + i) * kBlock + threadIdx.x] = acc[k][i];
         __syncthreads();
         if (g > 0)
             return;
@@ -371,18 +431,13 @@ __global__ __launch_bounds__((most_threads<GT>())) void rmsnorm_grad_kernel(Grad
             for (int i = 0; i < W; ++i)
 #pragma unroll
                 for (int b = 1; b < RB; ++b)
-                    acc[k][i] += lds_acc[b][(k * W + i) * GT + at.t];
+                    acc[k][i] += lds_acc[(k * W + i) * kBlock + b * GT + at.t];
     }
-    float* out = args.last ? a.dweight : args.partial + (size_t)blockIdx.x * a.D;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const uint32_t first = (k * at.threads + at.t) * W;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            if (first + i < a.D)
-                out[first + i] =
-                    (args.last && a.accum ? out[first + i] : 0.0f) + acc[k][i];
-    }
+            put(k, i, (double)acc[k][i]);
 }
 
 // dweight[j] = [dweight[j] +] the sum of n partial rows: 64 columns a
@@ -447,19 +502,25 @@ struct Shape {
                                       std::max(1u, kGradWavesPerCu * kWave / threads(vecs)));
         if (a.dweight)
             groups = std::min(groups, ws.partial_bytes / (a.D * sizeof(float)));
-        GradArgs args = {a, a.dweight ? static_cast<float*>(ws.partials) : nullptr, 0};
+        GradArgs args = {a, a.dweight ? static_cast<float*>(ws.partials) : nullptr, 0, 0};
         if (a.dweight && groups == 1) {
             args.last = 1;
             args.partial = a.dweight;
         }
+        args.folds = a.dweight && (a.rows + groups * RB - 1) / (groups * RB) > kRun;
+        // At most 136 KiB for the waves that a compute unit gets.
+        const size_t of = threads(vecs);
+        const unsigned lds = (unsigned)(args.folds ? of * fold_stride(NV * T::W) * sizeof(double)
+                                        : a.dweight && RB > 1 ? of * NV * T::W * sizeof(float)
+                                                              : 0);
         const Aligned al = {a.rows};
         if (al(a.h, a.ldh * sizeof(typename T::S)) && al(a.dy, a.lddy * sizeof(typename T::S)) &&
             al(a.dsum, a.ldds * sizeof(typename T::S)) && al(a.dx, a.lddx * sizeof(typename T::S)))
             hipLaunchKernelGGL((rmsnorm_grad_kernel<T, GT, NV, true>), dim3((unsigned)groups),
-                               dim3(threads(vecs)), 0, s, args);
+                               dim3(threads(vecs)), lds, s, args);
         else
             hipLaunchKernelGGL((rmsnorm_grad_kernel<T, GT, NV, false>), dim3((unsigned)groups),
-                               dim3(threads(vecs)), 0, s, args);
+                               dim3(threads(vecs)), lds, s, args);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !a.dweight || groups == 1)
             return e;
