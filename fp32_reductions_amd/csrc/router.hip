@@ -7,9 +7,10 @@
 //     dz_r = w_r p_r (q - sum_e p_re q_e + 2 c lse_r),  q = b E f
 //
 // A row is short (its experts), and the rows are many: 4, 16 or 64 lanes share
-// one, and a lane keeps the column sums of its experts in registers over the
-// rows that it takes.  Counts are integer atomics in LDS, whose order changes
-// nothing.  The gradient needs every row's counts, so there are two kernels: the
+// one, and a lane keeps the column sums of its experts in fp32 registers over the
+// rows that it takes, 256 at most: more rows go in several launches of the first
+// kernel, whose sums are added in fp64.  Counts are integer atomics in LDS, whose order
+// changes nothing.  The gradient needs every row's counts, so there are two kernels: the
 // sums of each workgroup's rows, which the last of 16 workgroups to arrive adds
 // up for its team, and the gradient, whose workgroups each add up the teams (a
 // few KB), and which reads the logits again, from a cache in most sizes, and takes
@@ -38,6 +39,10 @@ constexpr float kLn2f = 0.6931471805599453f;
 
 // Workgroups whose sums one of them adds up, and the most teams of them.
 constexpr uint32_t kTeam = 16, kTeams = 32;
+
+// Rows that a lane adds up in fp32.  (4194304 x 256 f32, 4 launches: 2866 us, 2835 in one;
+// 1048576 are one launch.)
+constexpr uint32_t kRun = 256;
 static_assert(kTeams * kCountStride <= kCounterWords, "a count for each team");
 
 struct RouterArgs {
@@ -50,6 +55,7 @@ struct RouterArgs {
     double* team_z;                 // teams
     unsigned* arrivals;             // of each team's workgroups
     uint32_t groups;
+    size_t first, end; // rows of a launch of the sums
 };
 
 // Every lane of a row's GT neighbours gets their sum or maximum.  Up to 16 by
@@ -213,10 +219,11 @@ __global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
     float acc[NV][W] = {};
     double zsum = 0.0;
     const size_t step = (size_t)a.groups * RB;
+    const bool more = a.first > 0; // added to the launches' before
     // The next row is requested before this one is worked on (not where a row takes
     // a quarter of the registers).
     constexpr bool kAhead = NV < 8;
-    size_t r = (size_t)blockIdx.x * RB + threadIdx.x / GT;
+    size_t r = a.first + (size_t)blockIdx.x * RB + threadIdx.x / GT;
     u32x4_t next[NV] = {};
     float wn = 0.0f;
     int64_t en = -1;
@@ -225,9 +232,9 @@ __global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
         en = first_choice(c, row, at.t);
         at.load(static_cast<const typename T::S*>(c.m.z) + row * c.m.ld, next);
     };
-    if (kAhead && r < c.m.rows)
+    if (kAhead && r < a.end)
         request(r);
-    for (; r < c.m.rows; r += step) {
+    for (; r < a.end; r += step) {
         if (!kAhead)
             request(r);
         u32x4_t v[NV];
@@ -236,7 +243,7 @@ __global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
             v[k] = next[k];
         const float w = wn;
         const int64_t chosen = en;
-        if (kAhead && r + step < c.m.rows)
+        if (kAhead && r + step < a.end)
             request(r + step);
         if (w == 0.0f)
             continue;
@@ -308,14 +315,15 @@ __global__ __launch_bounds__(kThreads) void router_sum_kernel(RouterArgs a)
                 chosen += from + k < size ? n[k] : 0;
             }
         }
-        a.team_prob[(size_t)team * E + e] = sum;
-        a.team_count[(size_t)team * E + e] = chosen;
+        const size_t at_team = (size_t)team * E + e;
+        a.team_prob[at_team] = more ? a.team_prob[at_team] + sum : sum;
+        a.team_count[at_team] = more ? a.team_count[at_team] + chosen : chosen;
     }
     if (threadIdx.x == 0) {
         double v = 0.0;
         for (uint32_t k = 0; k < size; ++k)
             v += load_shared(a.z_part + first + k);
-        a.team_z[team] = v;
+        a.team_z[team] = more ? a.team_z[team] + v : v;
     }
 }
 
@@ -593,8 +601,12 @@ hipError_t launch(const RouterCall& c, const DeviceInfo& dev, const Workspace& w
     a.arrivals = ws.counters;
     // One workgroup a compute unit in both kernels (65536 x 128 f32: 27.1 us; two in
     // the sums 32.2, two in the gradient 28.8).
-    hipLaunchKernelGGL((router_sum_kernel<T, GT, NV>), dim3(a.groups), dim3(kThreads),
-                       RouterLds<T>::bytes(E, kThreads / kWave), s, a);
+    const size_t most = (size_t)kRun * RB * a.groups;
+    for (; a.first < c.m.rows; a.first += most) {
+        a.end = std::min(a.first + most, c.m.rows);
+        hipLaunchKernelGGL((router_sum_kernel<T, GT, NV>), dim3(a.groups), dim3(kThreads),
+                           RouterLds<T>::bytes(E, kThreads / kWave), s, a);
+    }
     const size_t groups = 1 + (c.m.dz ? std::min(wanted, (size_t)dev.cus) : 0);
     hipLaunchKernelGGL((router_grad_kernel<T, GT, NV>), dim3((unsigned)groups), dim3(kThreads),
                        sizeof(float) * GT * NV * T::W, s, a);
