@@ -717,11 +717,15 @@ int rmsnorm_grad(LogitType t, const red::NormGradCall& a, red_stream_t stream)
     });
 }
 
-int router_balance(LogitType t, const red::RouterCall& a, red_stream_t stream)
+int router_balance(LogitType t, red::RouterCall a, red_stream_t stream)
 {
-    const Logits& m = a.m;
+    Logits& m = a.m;
     if (m.rows == 0 || m.V == 0)
         return RED_OK;
+    if (m.rows == 1) { // its strides are not looked at
+        m.ld = m.ldd = m.V;
+        a.ldk = a.K;
+    }
     if (m.V > red::kRouterExpertsMax || m.rows >= (size_t(1) << 31) || a.K < 1 ||
         a.K > red::kTopkMax || a.ldk < a.K || !extent_ok(m.rows, a.ldk, a.K, 8) ||
         !std::isfinite(a.balance) || !std::isfinite(a.z))
@@ -743,10 +747,12 @@ bool linear_sizes_ok(size_t rows, size_t D, size_t V)
            D % 8 == 0;
 }
 
-int linear_ce(LogitType t, const red::LinearCall& a, red_stream_t stream)
+int linear_ce(LogitType t, red::LinearCall a, red_stream_t stream)
 {
     if (a.rows == 0 || a.V == 0 || a.D == 0)
         return RED_OK;
+    if (a.V == 1)
+        a.ldw = a.lddw = a.D; // of one row, not looked at
     if (!linear_sizes_ok(a.rows, a.D, a.V) || a.ldw % 8 || a.ldw > red::kLinearStrideMax ||
         !scale_ok(a.scale) || !std::isfinite(a.z) || !a.workspace ||
         (a.dhidden && a.dhidden == a.hidden) || (a.dweight && a.dweight == a.weight))

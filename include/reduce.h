@@ -526,7 +526,7 @@ int red_rmsnorm_grad_bf16(const uint16_t* h, size_t rows, size_t D, size_t ldh,
 /* Balance loss of a router of E experts, E <= 2048, over rows of logits, of
  * which each row has chosen the K experts experts[r * ldk + k] (one that is
  * not in [0, E) is padding; one listed twice counts twice; 1 <= K <= 1024,
- * ldk >= K).  With p_r the softmax of row r and n_e the number of choices of
+ * ldk >= K, not looked at for one row).  With p_r the softmax of row r and n_e the number of choices of
  * expert e among the rows that count,
  *   P_e = sum_r weight[r] p_re,   f_e = n_e / sum n,
  *   loss = balance_coef E sum_e f_e P_e + z_coef sum_r weight[r] lse_r^2.
