@@ -778,13 +778,13 @@ int linear_ce(LogitType t, red::LinearCall a, red_stream_t stream)
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != RED_OK)
         return st;
-    if (red::linear_ce_workspace(t, a, info) > a.workspace_bytes)
+    if (red::linear_ce_workspace(a, info) > a.workspace_bytes)
         return RED_ERR_SCRATCH;
     clear_stale_error();
     return hip_status(red::launch_linear_ce(t, a, info, static_cast<hipStream_t>(stream)));
 }
 
-int linear_ce_workspace(LogitType t, size_t rows, size_t D, size_t V, int dhidden, int dweight,
+int linear_ce_workspace(size_t rows, size_t D, size_t V, int dhidden, int dweight,
                         size_t* bytes)
 {
     if (!bytes)
@@ -804,7 +804,7 @@ int linear_ce_workspace(LogitType t, size_t rows, size_t D, size_t V, int dhidde
     a.V = V;
     a.dhidden = dhidden ? bytes : nullptr;
     a.dweight = dweight ? bytes : nullptr;
-    *bytes = red::linear_ce_workspace(t, a, info);
+    *bytes = red::linear_ce_workspace(a, info);
     return RED_OK;
 }
 
@@ -1159,7 +1159,7 @@ int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
 int red_linear_ce_workspace_f16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
                                 size_t* bytes)
 {
-    return linear_ce_workspace(LogitType::F16, rows, D, V, dhidden, dweight, bytes);
+    return linear_ce_workspace(rows, D, V, dhidden, dweight, bytes);
 }
 
 int red_linear_ce_bf16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
@@ -1175,7 +1175,7 @@ int red_linear_ce_bf16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh
 int red_linear_ce_workspace_bf16(size_t rows, size_t D, size_t V, int dhidden, int dweight,
                                 size_t* bytes)
 {
-    return linear_ce_workspace(LogitType::BF16, rows, D, V, dhidden, dweight, bytes);
+    return linear_ce_workspace(rows, D, V, dhidden, dweight, bytes);
 }
 
 int red_release_workspace(red_stream_t stream)

@@ -1085,7 +1085,7 @@ struct Places {
     }
 };
 
-LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
+LcePlan plan_of(const LinearCall& c, const DeviceInfo& dev, Lce* a)
 {
     LcePlan p;
     const bool grad = c.dhidden || c.dweight;
@@ -1150,10 +1150,10 @@ LcePlan plan_of(LogitType t, const LinearCall& c, const DeviceInfo& dev, Lce* a)
 }
 
 template <class T>
-hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStream_t s)
+hipError_t run(const LinearCall& c, const DeviceInfo& dev, hipStream_t s)
 {
     Lce a;
-    const LcePlan p = plan_of(t, c, dev, &a);
+    const LcePlan p = plan_of(c, dev, &a);
     const dim3 gather((unsigned)c.rows + kRowPad);
     if (c.rows <= kRowsAlone) {
         hipLaunchKernelGGL((lce_gather_kernel<T, true>), gather, dim3(256), 0, s, a);
@@ -1244,15 +1244,15 @@ hipError_t run(LogitType t, const LinearCall& c, const DeviceInfo& dev, hipStrea
 
 } // namespace
 
-size_t linear_ce_workspace(LogitType t, const LinearCall& a, const DeviceInfo& dev)
+size_t linear_ce_workspace(const LinearCall& a, const DeviceInfo& dev)
 {
-    return plan_of(t, a, dev, nullptr).bytes;
+    return plan_of(a, dev, nullptr).bytes;
 }
 
 hipError_t launch_linear_ce(LogitType t, const LinearCall& a, const DeviceInfo& dev,
                             hipStream_t stream)
 {
-    return t == LogitType::F16 ? run<ElemF16>(t, a, dev, stream) : run<ElemBF16>(t, a, dev, stream);
+    return t == LogitType::F16 ? run<ElemF16>(a, dev, stream) : run<ElemBF16>(a, dev, stream);
 }
 
 } // namespace red

@@ -33,8 +33,8 @@ struct LinearCall {
 };
 
 // Bytes of workspace that the call needs (its pointers only say which outputs
-// are wanted); SIZE_MAX where that does not fit size_t.
-size_t linear_ce_workspace(LogitType t, const LinearCall& a, const DeviceInfo& dev);
+// are wanted); the sizes within the limits above all fit size_t.
+size_t linear_ce_workspace(const LinearCall& a, const DeviceInfo& dev);
 hipError_t launch_linear_ce(LogitType t, const LinearCall& a, const DeviceInfo& dev,
                             hipStream_t stream);
 
