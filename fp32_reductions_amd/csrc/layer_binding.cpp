@@ -232,7 +232,8 @@ const char kNormDoc[] =
     "rmsnorm_grad needs.  y is of x's type, or torch.float8_e4m3fn with\n"
     "yscale (rows, fp32): y * yscale is the row.  y8 is the 8-bit output\n"
     "beside a y of x's type (y may be None then).  sum and y may each be x or\n"
-    "residual themselves.";
+    "residual themselves.  A row with an infinity has rstd 0, NaN there and zeros\n"
+    "elsewhere.";
 const char kNormGradDoc[] =
     "($self, h, weight, rstd, dy, dx, dsum=None, dweight=None, accum=False, stream=None)\n--\n\n"
     "The gradient of add_rmsnorm from its h (sum) and rstd: dx of x and of the\n"

@@ -471,9 +471,9 @@ int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size
  * their columns (where there is one row the stride is not looked at).
  * Elements between the columns and the stride are neither read nor written.
  * Values are widened exactly to fp32; every result is rounded once to its
- * type.  A row with a NaN or an infinity has NaN results and touches no other
- * row's (it does touch what is summed over rows).  All results are
- * deterministic.
+ * type.  A row with a NaN or an infinity has NaN results (but see the norm for
+ * an infinity) and touches no other row's (it does touch what is summed over
+ * rows).  All results are deterministic.
  * ------------------------------------------------------------------- */
 
 /* Root-mean-square norm of rows of D values, D <= 16384, with the residual's
@@ -487,6 +487,9 @@ int red_preference_loss_bf16(const uint16_t* logits, size_t rows, size_t V, size
  * whose largest |y| is below 1e-35 has scale 0 and zeros, and a NaN in y is a
  * NaN in y8 and does not count for the scale.  rstd (NULL: not wanted) is what
  * the gradient needs.  The sum of squares is fp64: no finite row overflows.
+ * A row in whose h there is an infinity and no NaN has rstd 0: its y and y8 are
+ * NaN at the infinities and 0 elsewhere, with a scale of 0; a test of rstd for 0
+ * finds it, its gradient is NaN.
  * weight has D values.  eps >= 0 and finite; with eps 0 a row of zeros has NaN.
  * sum and y may each be x or residual themselves, with the same stride (two
  * outputs never the same). */
