@@ -1036,12 +1036,20 @@ constexpr uint32_t kTilesPerLaunch = 1u << 22;
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-// Where the vocabulary is one piece and its products (fp32) take no more than this,
-// they are kept from the first pass for the gradients: writing and reading them costs
-// less than the layer's rows again, unless those are short and the rows many.  (1040
-// rows against 50001: width 512, 348 us kept and 336 not, 640 399 and 405, 1024 509 and
-// 553; 32 rows, width 512, 64 and 73.)
-constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640, kKeptRows = 128;
+// Where the vocabulary is one piece its products (fp32) may be kept from the first pass for
+// the gradients: writing and reading them costs less than the layer's rows and the
+// products again where the products fit the caches or the rows are wide.  Bf16, us with
+// the products kept and computed again:
+//    200 x  50001 x  128 (38 MB)     68.5   68.5      1040 x 50001 x  128 (198 MB)   207  183
+//    600 x  50001 x  256 (114 MB)    153    160       2000 x 12000 x  256 (96 MB)    142  140
+//   1040 x  50001 x  512 (198 MB)    308    329       4000 x 12000 x  512 (192 MB)   297  292
+//    136 x  50001 x  512 (26 MB)     106    120       4000 x 12000 x  640 (192 MB)   350  356
+//  70000 x   2000 x  512 (560 MB)   2127   2094      70000 x  2000 x  640 (560 MB)  2280 2265
+//   1040 x  50001 x 1024 (198 MB)    473    538      70000 x  2000 x 1024 (560 MB)  2431 2518
+// So they are kept from this width on, and of narrower rows up to so many bytes for each
+// element of a row.  kKeptBytes is for the workspace's sake: one piece takes no more, but for
+// more than 65536 rows.
+constexpr size_t kKeptBytes = size_t(512) << 20, kKeptWidth = 640, kKeptOfWidth = size_t(384) << 10;
 
 enum class Kind { Few, Mid, Big };
 
@@ -1137,10 +1145,11 @@ LcePlan plan_of(const LinearCall& c, const DeviceInfo& dev, Lce* a)
     o.piece = (uint32_t)p.piece;
     o.splits = (uint32_t)p.splits;
     o.cus = (uint32_t)dev.cus;
-    p.keep = grad && p.piece >= c.V && 4 * p.piece * c.rows <= kKeptBytes &&
-             (c.rows <= kKeptRows || c.D >= kKeptWidth);
+    const size_t kept = 4 * p.piece * c.rows;
+    p.keep = grad && p.piece >= c.V && kept <= kKeptBytes &&
+             (c.D >= kKeptWidth || kept <= c.D * kKeptOfWidth);
     if (p.keep)
-        w.take(o.z, 4 * p.piece * c.rows);
+        w.take(o.z, kept);
     if (grad)
         w.take(o.d, 2 * p.piece * n);
     if (c.dhidden)

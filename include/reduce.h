@@ -592,9 +592,8 @@ int red_router_balance_bf16(const uint16_t* logits, size_t rows, size_t E, size_
  * takes the hidden rows once or, for dweight, twice, 8 bytes a row for each 128
  * or 256 columns, for gradients a piece of their logits' gradients (256 MiB or
  * 2048 columns), the logits themselves in fp32 where they are one piece, at most
- * 512 MiB and, for more than 128 rows, D at least 640 (others are computed a
- * second time), and for dhidden its
- * fp32 sums. */
+ * 512 MiB and, for D below 640, at most 384 KiB times D (others are computed a
+ * second time), and for dhidden its fp32 sums. */
 int red_linear_ce_f16(const uint16_t* hidden, size_t rows, size_t D, size_t ldh,
                       const uint16_t* weight, size_t V, size_t ldw, const int64_t* targets,
                       const float* row_weight, float scale, float z_coef, float* loss, int accum,
