@@ -1029,7 +1029,11 @@ __global__ __launch_bounds__(S::kThreads) void lce_dw_kernel(Lce a, uint32_t fir
 
 // ---- plan -------------------------------------------------------------------
 
-constexpr size_t kPieceBytes = size_t(256) << 20; // of d, where that is 2048 columns or more
+// Of a piece's d, where that is 2048 columns or more: a piece costs its launches and their
+// last rounds of tiles, and past the Infinity Cache d is read from memory.  Bf16, ms with 96,
+// 256 and 768 MiB: 4096 x 131072 x 4096 14.6, 14.5, 16.8; 16384 x 32768 x 1024 6.06, 4.57, 4.92;
+// 8192 x 131072 x 512 7.01, 5.42, 5.15.
+constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr size_t kRowsPad = 256, kColPad = 256; // of rows in the workspace, of a piece
 // A launch holds at most 2^32 - 1 work-items, of which a tile takes up to 512.
 constexpr uint32_t kTilesPerLaunch = 1u << 22;
