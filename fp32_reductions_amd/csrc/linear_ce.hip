@@ -69,7 +69,8 @@ static_assert(kGroups <= kWave, "a lane for each");
 struct Factor {
     float mantissa;
     int exponent;
-    __device__ __forceinline__ float times(float v) const { return ldexpf(v * mantissa, exponent); }
+    // The exact step first: the other one is one with the rounding to f16.
+    __device__ __forceinline__ float times(float v) const { return ldexpf(v, exponent) * mantissa; }
 };
 
 // What the kernels share.  Pointers into the workspace, except those of the call.
@@ -133,7 +134,7 @@ __device__ __forceinline__ Factor factor_of(float largest, float scale)
     constexpr double kUp = __is_same(T, ElemF16) ? kHalfScale : 1.0;
     int e;
     const double m = frexp((double)largest * (double)scale / kUp, &e);
-    return {(float)m, e};
+    return {(float)(2.0 * m), e - 1};
 }
 template <bool GROUPED>
 __device__ __forceinline__ uint32_t group_of(float w, float largest)
