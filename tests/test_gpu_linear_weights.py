@@ -132,3 +132,35 @@ def test_weights_and_scales_past_one_another(red, rows, top, scale):
     want = ref.linear_ce(h, W, y, w, scale, 0.0)
     assert want["dhidden"][0].abs().max() < 1e37 and want["dweight"][0].abs().max() < 1e37
     check(run(red, h, W, y, w, "bf16", scale=scale), want)
+
+
+@pytest.mark.parametrize("rows", [300, 1500])
+def test_captured_and_replayed_with_other_weights(red, rows):
+    """The groups of weights are found anew in every replay: one group, many, none."""
+    h, W, y, w = draw(rows, 700, 72, "f16", rows)
+    loss, dh, dw = torch.zeros(1, device="cuda"), torch.empty_like(h), torch.empty_like(W)
+    room = torch.empty(red.linear_ce_workspace(h, W), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call = red.plan("linear_ce_f16", h, W, y, loss, dhidden=dh, dweight=dw, row_weight=w,
+                        workspace=room)
+        call()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+    torch.cuda.synchronize()
+    for span in (0, 30, 3, 90, None, 12):
+        say("replay over weights of 2^-%s" % span)
+        h2, _, y2, w2 = draw(rows, 700, 72, "f16", rows + (span or 0))
+        h.copy_(h2)
+        y.copy_(y2)
+        w.copy_(torch.zeros_like(w2) if span is None else w2 * 2.0 ** (-span * torch.rand_like(w2)))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(red, h, W, y, w, "f16")
+        assert torch.equal(loss, want["loss"]) and torch.equal(dh, want["dhidden"])
+        assert torch.equal(dw, want["dweight"])
+        if span is not None:
+            check(want, ref.linear_ce(h, W, y, w, 1.0, 0.0))

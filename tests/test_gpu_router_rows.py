@@ -79,3 +79,41 @@ def test_ordinary_rows(red, monkeypatch, E, t):
         assert all(torch.equal(got[k], again[k]) for k in got)
         added = run(red, z, experts, w, t, old=3.0, grad=False)
         assert torch.equal(added["prob"], got["prob"]) and torch.equal(added["counts"], got["counts"])
+
+
+def test_captured_and_replayed(red, monkeypatch):
+    """Several launches of the sums in a graph, replayed with new rows."""
+    monkeypatch.setenv("RED_TEST_CUS", "1")
+    rows, E = 3 * 256 * 64 + 5, 48
+    say("router replays")
+    _, z, experts, w = draw(rows, E, 2, "bf16", 1)
+    zd, ed, wd = z.cuda(), experts.cuda(), w.cuda()
+    loss, prob = torch.empty(1, device="cuda"), torch.empty(E, device="cuda")
+    counts = torch.empty(E, dtype=torch.int64, device="cuda")
+    dz = torch.empty_like(zd)
+
+    def call():
+        red.router_balance_bf16(zd, ed, loss, counts, dlogits=dz, weight=wd, prob=prob,
+                                balance_coef=0.02, z_coef=0.003)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+    torch.cuda.synchronize()
+    for seed in (2, 3, 4):
+        _, z2, e2, w2 = draw(rows, E, 2, "bf16", seed)
+        for old, new in ((zd, z2), (ed, e2), (wd, w2)):
+            old.copy_(new)
+        with torch.cuda.stream(s):
+            graph.replay()
+        s.synchronize()
+        got = [v.clone() for v in (loss, counts, prob, dz)]
+        want = run(red, z2, e2, w2, "bf16")
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, want[k]) for a, k in zip(got, ("loss", "counts", "prob", "dlogits")))
+        check(want, ref.router_balance(z2, e2, w2, 0.02, 0.003))
