@@ -18,8 +18,8 @@
 // So a column's error does not grow with the rows.  No atomics: the result does not
 // depend on timing.
 //
-// Bf16: 8192 x 8192 with a residual and 8 bits out 71.9 us a call, 6.5 TB/s; 1 x 4096 4.2,
-// of which the host takes 3.3; the gradient of 16384 x 4096 95.2, 89 of them at 6.0 TB/s.
+// Bf16: 8192 x 8192 with a residual and 8 bits out 71.4 us a call, 6.6 TB/s; 1 x 4096 4.1,
+// of which the host takes 3.3; the gradient of 16384 x 4096 95.1, 89 of them at 6.0 TB/s.
 #include <algorithm>
 
 #include "elements.hpp"
